@@ -358,6 +358,191 @@ int mova_ffn_moe_forward(const void* x, const void* router_w, const float* route
                          size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * The paged key-value cache around the value projection.
+ *
+ * mova_value_forward_paged keeps the routed value rows in the ordinary
+ * paged-attention pools (page "IFM K2 Horizon Deep Dive: Inside
+ * Mixture-of-Value Attention (MoVA) ...", section "The Two Architectural
+ * Caching Strategies for MoVA", Option A), and attention reads them with an
+ * unchanged kernel (page "MoVA: routing the value vectors ...", section "Where
+ * the routing happens").  The entry points below are the rest of such a
+ * cache's decode step: blocks and slots for the step's tokens
+ * (mova_paged_plan), their keys, and values for an 8-bit pool, stored
+ * (mova_kv_store_paged), the blocks worth reading chosen (mova_block_select,
+ * optional), and one new token per request attending over the cache
+ * (mova_attention_paged).
+ *
+ * Shared layouts
+ *   k_cache, v_cache  [num_blocks, block_size, n_kv_heads, head_dim], bf16 or
+ *                     8-bit e4m3 (cache_dtype); slot s is row s % block_size
+ *                     of block s / block_size
+ *   k_scale, v_scale  float [n_kv_heads]: an 8-bit element e of key head h
+ *                     stands for e * scale[h]; NULL = 1.  Must be NULL for
+ *                     bf16 pools.
+ *   block_table       int32 [B, max_blocks]: the pool block of each run of
+ *                     block_size positions of each request, any order
+ *   seq_lens          int32 [B]: tokens of each request, the newest included.
+ *                     On the device, never read by the host: it counts as 0
+ *                     below 0 and as max_blocks * block_size above that.
+ * Table entries outside [0, num_blocks) -- e.g. -1 -- stand for blocks that
+ * are not there: their keys take no part.  Entries behind a request's last
+ * block are not read.  Any block_size > 0 is taken.
+ * Domain: B <= 2048, max_blocks * block_size <= 2^30; pools that are read have
+ * at most 2^31 - 1 slots; head_dim 64, 128 or 256, n_heads a multiple of
+ * n_kv_heads, n_kv_heads * head_dim <= 16384, n_heads * head_dim <= 131072.
+ * int32 and float arrays are 4-byte aligned, slot_mapping 8-byte, tensors 16,
+ * workspaces 256.  Errors as for mova_value_forward; T == 0 (store) and B == 0
+ * (selection, attention) return MOVA_OK and enqueue nothing.
+ */
+enum mova_cache_dtype {
+  MOVA_CACHE_BF16 = 0,
+  MOVA_CACHE_FP8 = 1 /* e4m3: 4 exponent bits, 3 mantissa bits, largest value 448, no infinity */
+};
+
+/*
+ * Block tables and slot maps of one step.  Request b has cached_lens[b]
+ * tokens in the cache, in its first ceil(cached_lens[b] / block_size) table
+ * entries.
+ *
+ *   new_lens[b] >= 0: it gets that many new tokens; their rows are
+ *     [cu_new[b], cu_new[b + 1]) of the step's packed tokens.
+ *   new_lens[b] < 0: it has ended; its blocks go back on the free stack.
+ *
+ * free_blocks [free_capacity] is a stack of free block ids, *free_count of
+ * them in use, the last one on top.  First the blocks of ended requests are
+ * pushed, by request and position (those beyond free_capacity are dropped).
+ * Then each request in turn takes the blocks that it still needs for its new
+ * tokens from the top and has them written to its table row.  A request is
+ * admitted when it needs no more blocks, or when the blocks needed up to and
+ * with it are there.  One that is not, or whose tokens reach past its table
+ * row or past row T, gets nothing: its table row and length stay and its tokens
+ * have no slot.
+ *
+ *   cached_lens, new_lens int32 [B] (cached_lens kept within [0, max_blocks *
+ *                block_size])
+ *   block_table  int32 [B, max_blocks]   in / out; only new entries are written
+ *   free_blocks  int32 [free_capacity]   in / out; popped entries stay as they are
+ *   free_count   int32 [1];  free_count_out int32 [1], not the same address
+ *   seq_lens     int32 [B]      out: the length with the new tokens, 0 for an
+ *                               ended request; not the address of cached_lens
+ *                               or new_lens
+ *   cu_new       int32 [B + 1]  out (sums beyond 2^31 - 1 count as that)
+ *   slot_mapping int64 [T]      out: slot of each token row, -1 where there is
+ *                               none (tokens of requests not admitted, rows
+ *                               behind the last token); what
+ *                               mova_value_forward_paged takes
+ *   positions    int32 [T]      out: position in its request, -1 without slot
+ *
+ * No output may overlap an input or another output, free_blocks and
+ * block_table as named apart.  The same inputs give the same outputs; a call
+ * may be repeated as long as its inputs are as they were (the entries it
+ * writes in block_table and free_blocks are not among what it reads again).
+ * T <= 2^24.
+ */
+int mova_paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int B, int T,
+                    int block_size, int max_blocks, int32_t* block_table, int32_t* free_blocks,
+                    int free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                    int32_t* seq_lens, int32_t* cu_new, int64_t* slot_mapping, int32_t* positions,
+                    hipStream_t stream);
+
+/*
+ * Rows stored at their slots of the pools:
+ *   k_cache[slot_mapping[t]] = k[t],  v_cache[slot_mapping[t]] = v[t]
+ *
+ *   k, v       bf16 [T, n_kv_heads, head_dim]; either may be NULL, with its pool
+ *   8-bit pools hold x / scale[h] (fp32 quotient) rounded to e4m3, nearest
+ *              even; beyond +-448 it is +-448, NaN stays NaN
+ *   slot_mapping int64 [T]; slots outside the pool store nothing
+ *   k_bounds   bf16 [num_blocks, n_kv_heads, 2, head_dim] or NULL: for each
+ *              block touched, per channel the smallest (index 0) and largest
+ *              (1) stored key element over the block's rows 0 .. o, o the row
+ *              that the last token of a run of consecutive slots in the block
+ *              went to.  With slots in the order that mova_paged_plan gives,
+ *              these are the block's rows that hold keys.  Elements are taken
+ *              as stored (8-bit ones without their scale); a NaN makes its
+ *              channel's bounds NaN.
+ *
+ * Rows and bounds that no slot names stay untouched.  Two tokens naming the
+ * same slot race, and so do two runs in one block as to its bounds: those
+ * contents are unspecified.  Domain: head_dim % 16 == 0, n_kv_heads *
+ * head_dim <= 16384, at most 2^40 slots, T <= 2^24.
+ */
+int mova_kv_store_paged(const void* k, const void* v, int T, int n_kv_heads, int head_dim,
+                        void* k_cache, void* v_cache, int cache_dtype, const float* k_scale,
+                        const float* v_scale, int num_blocks, int block_size,
+                        const int64_t* slot_mapping, void* k_bounds, hipStream_t stream);
+
+/* Bytes of workspace of mova_block_select; (size_t)-1 outside the domain. */
+size_t mova_block_select_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim,
+                                         int max_blocks, int block_size, int keep);
+
+/*
+ * The blocks worth reading, per request and key head.  A block's score is the
+ * largest logit that any key within its bounds could have with any of the
+ * head's queries,
+ *
+ *   s[b, h, j] = max over the query heads g of h of
+ *                sum_d ( q > 0 ? hi : lo ) * q,   q = q[b, g, d],
+ *                (lo, hi) = k_bounds[block_table[b, j], h, :, d]
+ *
+ * summed in 64 bits, so that the choice does not hang on an order of
+ * summation.  The first keep_first and the last keep_last blocks of a request
+ * are always in; the others follow by score, the lower position first among
+ * equals, a NaN score last (with -infinity), up to keep blocks.
+ *
+ *   q           bf16  [B, n_heads, head_dim]; query head i belongs to key head
+ *               i / (n_heads / n_kv_heads)
+ *   k_bounds    as mova_kv_store_paged leaves them
+ *   sel_blocks  int32 [B, n_kv_heads, keep] out: positions in the request's
+ *               table row, ascending, -1 behind the last
+ *
+ * keep_first + keep_last <= keep <= 2^20.  Positive key scales do not change
+ * the choice, so none are taken.  Blocks that are not there are never chosen.
+ */
+int mova_block_select(const void* q, const void* k_bounds, int num_blocks, int block_size,
+                      const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int B,
+                      int n_heads, int n_kv_heads, int head_dim, int keep, int keep_first,
+                      int keep_last, int32_t* sel_blocks, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/* Bytes of workspace of mova_attention_paged (keep = 0 without sel_blocks);
+ * (size_t)-1 outside the domain. */
+size_t mova_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim,
+                                      int max_blocks, int block_size, int keep);
+
+/*
+ * One new token per request attending over the cache:
+ *
+ *   out[b, i] = sum_p softmax_p( scale * q[b, i] . K[p, h] ) V[p, h],
+ *               h = i / (n_heads / n_kv_heads)
+ *
+ * over the request's positions p < seq_lens[b]; with window > 0 only the last
+ * `window` of them; with sel_blocks only those in the listed blocks of
+ * (b, h).  sel_blocks is int32 [B, n_kv_heads, keep] of positions in the table
+ * row, any order; entries outside the request are skipped, one listed twice
+ * counts twice.  Pass keep = 0 and NULL for all blocks.
+ *
+ *   q, out  bf16 [B, n_heads, head_dim]
+ *   lse     float [B, n_heads] or NULL: log of the softmax's sum,
+ *           log sum_p exp(scale * q . K[p]), -infinity for an empty row
+ *
+ * A row without keys (length 0, every block missing) gives zeros.  Products
+ * accumulate in fp32; the softmax's maximum and sum are fp32, its weights are
+ * rounded to bf16 for the product with V (the sum is over the unrounded ones);
+ * the result is rounded once to bf16.  Results are bitwise reproducible for
+ * identical inputs; how a request's keys are split among workgroups, and so
+ * the last bits of its row, depends on the lengths of the whole batch.
+ * keep * block_size <= 2^30, scale finite.
+ */
+int mova_attention_paged(const void* q, const void* k_cache, const void* v_cache, int cache_dtype,
+                         const float* k_scale, const float* v_scale, int num_blocks,
+                         int block_size, const int32_t* block_table, int max_blocks,
+                         const int32_t* seq_lens, const int32_t* sel_blocks, int keep, int B,
+                         int n_heads, int n_kv_heads, int head_dim, float scale, int window,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
  * Kernel-choice overrides, for tests and measurements only.  A production
  * call chooses its kernels from the shapes alone and reads no environment
  * variable; an override set here forces one choice instead, for every later

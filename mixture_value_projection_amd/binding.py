@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Tuple
+from typing import List, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -70,6 +70,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mova_dense_workspace_bytes.argtypes = [i, i, i, i]
     lib.mova_dense_value_proj.restype = i
     lib.mova_dense_value_proj.argtypes = [vp, vp, i, i, i, i, vp, vp, sz, vp]
+    lib.mova_paged_plan.restype = i
+    lib.mova_paged_plan.argtypes = [vp, vp, i, i, i, i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp]
+    lib.mova_kv_store_paged.restype = i
+    lib.mova_kv_store_paged.argtypes = [vp, vp, i, i, i, vp, vp, i, vp, vp, i, i, vp, vp, vp]
+    lib.mova_block_select_workspace_bytes.restype = sz
+    lib.mova_block_select_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.mova_block_select.restype = i
+    lib.mova_block_select.argtypes = [vp, vp, i, i, vp, i, vp, i, i, i, i, i, i, i, vp, vp, sz, vp]
+    lib.mova_attention_workspace_bytes.restype = sz
+    lib.mova_attention_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.mova_attention_paged.restype = i
+    lib.mova_attention_paged.argtypes = [vp, vp, vp, i, vp, vp, i, i, vp, i, vp, vp, i, i, i, i, i,
+                                         f, i, vp, vp, vp, sz, vp]
     lib.mova_debug_override.restype = i
     lib.mova_debug_override.argtypes = [i, i]
     lib.mova_debug_override_get.restype = i
@@ -493,6 +506,222 @@ def dense_value_proj(x: torch.Tensor, w_v: torch.Tensor, n_kv_heads: Optional[in
                                    _ptr(workspace), workspace.numel(), _stream(dev))
     if rc != MOVA_OK:
         raise MovaError(rc, "mova_dense_value_proj")
+    return out
+
+
+# ---- the paged key-value cache ------------------------------------------------
+
+# Element types of a cache pool (mova_cache_dtype).
+CACHE_DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+class PagedPlan(NamedTuple):
+    """Outputs of ``paged_plan``."""
+    seq_lens: torch.Tensor      # int32 [B]
+    cu_new: torch.Tensor        # int32 [B + 1]
+    slot_mapping: torch.Tensor  # int64 [T]
+    positions: torch.Tensor     # int32 [T]
+    free_count: torch.Tensor    # int32 [1]
+
+
+def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype, shape, device)
+    return t
+
+
+def _scratch(workspace: Optional[torch.Tensor], nbytes: int, what: str, device) -> torch.Tensor:
+    if nbytes == ctypes.c_size_t(-1).value:
+        raise MovaError(-2, what)
+    if workspace is not None and workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _launch(fn, name: str, device, *args) -> None:
+    """Call an entry point on the device's current stream, with that device
+    current."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs GPU tensors, got {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(device))
+    if rc != MOVA_OK:
+        raise MovaError(rc, name)
+
+
+def _dims(t: torch.Tensor, name: str, n: int, layout: str) -> Tuple[int, ...]:
+    if t.dim() != n:
+        raise ValueError(f"{name} must be {layout}")
+    return tuple(t.shape)
+
+
+def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_size: int,
+               block_table: torch.Tensor, free_blocks: torch.Tensor, free_count: torch.Tensor,
+               seq_lens: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None,
+               slot_mapping: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None) -> PagedPlan:
+    """mova_paged_plan: blocks and slots of one step's T token rows.
+
+    ``block_table`` (int32 [B, max_blocks]) and ``free_blocks`` (int32, a stack
+    with ``free_count`` (int32 [1]) entries in use) are updated in place; the
+    lengths are int32 [B], a negative ``new_lens`` entry ends its request.
+    The new lengths and count are new tensors (pass two sets in turn to
+    allocate nothing)."""
+    lib = load_library()
+    B, mb = _dims(block_table, "block_table", 2, "[B, max_blocks]")
+    (cap,) = _dims(free_blocks, "free_blocks", 1, "[capacity]")
+    dev = block_table.device
+    i32 = torch.int32
+    _check(block_table, "block_table", i32, (B, mb), dev)
+    _check(free_blocks, "free_blocks", i32, (cap,), dev)
+    _check(free_count, "free_count", i32, (1,), dev)
+    _check(cached_lens, "cached_lens", i32, (B,), dev)
+    _check(new_lens, "new_lens", i32, (B,), dev)
+    if T < 0:
+        raise ValueError("T must not be negative")
+    plan = PagedPlan(_out(seq_lens, "seq_lens", i32, (B,), dev),
+                     _out(cu_new, "cu_new", i32, (B + 1,), dev),
+                     _out(slot_mapping, "slot_mapping", torch.int64, (T,), dev),
+                     _out(positions, "positions", i32, (T,), dev),
+                     _out(free_count_out, "free_count_out", i32, (1,), dev))
+    _launch(lib.mova_paged_plan, "mova_paged_plan", dev, _ptr(cached_lens), _ptr(new_lens), B, T,
+            block_size, mb, _ptr(block_table), _ptr(free_blocks), cap, _ptr(free_count),
+            _ptr(plan.free_count), _ptr(plan.seq_lens), _ptr(plan.cu_new),
+            _ptr(plan.slot_mapping), _ptr(plan.positions))
+    return plan
+
+
+def _check_pool(pool: torch.Tensor, name: str, shape, device) -> int:
+    if pool.dtype not in CACHE_DTYPES:
+        raise ValueError(f"{name} has dtype {pool.dtype}, expected bfloat16 or float8_e4m3fn")
+    _check(pool, name, pool.dtype, shape, device)
+    return CACHE_DTYPES[pool.dtype]
+
+
+def _check_scales(k_scale, v_scale, heads: int, device) -> None:
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _check(t, name, torch.float32, (heads,), device)
+
+
+def kv_store_paged(k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                   k_cache: Optional[torch.Tensor], v_cache: Optional[torch.Tensor],
+                   slot_mapping: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None,
+                   k_bounds: Optional[torch.Tensor] = None) -> None:
+    """mova_kv_store_paged: stores key and value rows (bf16 [T, n_kv_heads,
+    head_dim], either may be None with its pool) at their slots of the pools
+    ([num_blocks, block_size, n_kv_heads, head_dim], bfloat16 or
+    float8_e4m3fn with float32 [n_kv_heads] scales) and, if given, refreshes
+    ``k_bounds`` (bf16 [num_blocks, n_kv_heads, 2, head_dim]) of the blocks
+    touched."""
+    lib = load_library()
+    if (k is None) != (k_cache is None) or (v is None) != (v_cache is None):
+        raise ValueError("k and k_cache, and v and v_cache, go together")
+    if k is None and v is None:
+        raise ValueError("neither keys nor values are given")
+    rows, pool = (k, k_cache) if k is not None else (v, v_cache)
+    T, H, D = _dims(rows, "k and v", 3, "[T, n_kv_heads, head_dim]")
+    nb, bs = _dims(pool, "the pools", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")[:2]
+    dev = rows.device
+    dtype = CACHE_DTYPES.get(pool.dtype)
+    for t, p, name in ((k, k_cache, "k"), (v, v_cache, "v")):
+        if t is not None:
+            _check(t, name, torch.bfloat16, (T, H, D), dev)
+            if _check_pool(p, name + "_cache", (nb, bs, H, D), dev) != dtype:
+                raise ValueError("the pools must have the same dtype")
+    _check(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
+    _check_scales(k_scale, v_scale, H, dev)
+    if k_bounds is not None:
+        _check(k_bounds, "k_bounds", torch.bfloat16, (nb, H, 2, D), dev)
+    _launch(lib.mova_kv_store_paged, "mova_kv_store_paged", dev, _ptr(k), _ptr(v), T, H, D,
+            _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale), nb, bs,
+            _ptr(slot_mapping), _ptr(k_bounds))
+
+
+def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
+                 block_table: torch.Tensor, seq_lens: torch.Tensor, keep: int,
+                 keep_first: int = 1, keep_last: int = 1,
+                 sel_blocks: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mova_block_select: int32 [B, n_kv_heads, keep] positions in each
+    request's block table of the blocks whose keys can reach the highest
+    logits, ascending, -1 behind the last."""
+    lib = load_library()
+    B, Hq, D = _dims(q, "q", 3, "[B, n_heads, head_dim]")
+    nb, H = _dims(k_bounds, "k_bounds", 4, "[num_blocks, n_kv_heads, 2, head_dim]")[:2]
+    mb = _dims(block_table, "block_table", 2, "[B, max_blocks]")[1]
+    dev = q.device
+    _check(q, "q", torch.bfloat16, (B, Hq, D), dev)
+    _check(k_bounds, "k_bounds", torch.bfloat16, (nb, H, 2, D), dev)
+    _check(block_table, "block_table", torch.int32, (B, mb), dev)
+    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    nbytes = lib.mova_block_select_workspace_bytes(B, Hq, H, D, mb, block_size, keep)
+    workspace = _scratch(workspace, nbytes, "mova_block_select", dev)
+    sel_blocks = _out(sel_blocks, "sel_blocks", torch.int32, (B, H, keep), dev)
+    _launch(lib.mova_block_select, "mova_block_select", dev, _ptr(q), _ptr(k_bounds), nb,
+            block_size, _ptr(block_table), mb, _ptr(seq_lens), B, Hq, H, D, keep, keep_first,
+            keep_last, _ptr(sel_blocks), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
+    return sel_blocks
+
+
+def attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                              max_blocks: int, block_size: int, keep: int = 0) -> int:
+    n = load_library().mova_attention_workspace_bytes(B, n_heads, n_kv_heads, head_dim, max_blocks,
+                                                      block_size, keep)
+    if n == ctypes.c_size_t(-1).value:
+        raise MovaError(-2, "mova_attention_workspace_bytes")
+    return n
+
+
+def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                    k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, window: int = 0,
+                    sel_blocks: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mova_attention_paged: one new token per request attending over the
+    paged cache; returns bf16 [B, n_heads, head_dim].
+
+    ``window`` > 0 keeps the last ``window`` positions, ``sel_blocks`` (int32
+    [B, n_kv_heads, keep], as from ``block_select``) the listed blocks;
+    ``lse`` (float32 [B, n_heads]) receives the log-sum-exp of the logits."""
+    lib = load_library()
+    B, Hq, D = _dims(q, "q", 3, "[B, n_heads, head_dim]")
+    nb, bs, H, _ = _dims(k_cache, "k_cache", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")
+    mb = _dims(block_table, "block_table", 2, "[B, max_blocks]")[1]
+    dev = q.device
+    _check(q, "q", torch.bfloat16, (B, Hq, D), dev)
+    dtype = _check_pool(k_cache, "k_cache", (nb, bs, H, D), dev)
+    if _check_pool(v_cache, "v_cache", (nb, bs, H, D), dev) != dtype:
+        raise ValueError("the pools must have the same dtype")
+    _check(block_table, "block_table", torch.int32, (B, mb), dev)
+    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _check_scales(k_scale, v_scale, H, dev)
+    keep = 0
+    if sel_blocks is not None:
+        keep = _dims(sel_blocks, "sel_blocks", 3, "[B, n_kv_heads, keep]")[2]
+        _check(sel_blocks, "sel_blocks", torch.int32, (B, H, keep), dev)
+        if keep == 0:
+            raise ValueError("sel_blocks lists no blocks")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (B, Hq), dev)
+    nbytes = lib.mova_attention_workspace_bytes(B, Hq, H, D, mb, bs, keep)
+    workspace = _scratch(workspace, nbytes, "mova_attention_paged", dev)
+    out = _out(out, "out", torch.bfloat16, (B, Hq, D), dev)
+    _launch(lib.mova_attention_paged, "mova_attention_paged", dev, _ptr(q), _ptr(k_cache),
+            _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale), nb, bs, _ptr(block_table), mb,
+            _ptr(seq_lens), _ptr(sel_blocks), keep, B, Hq, H, D, float(scale), int(window),
+            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size())
     return out
 
 

@@ -15,7 +15,7 @@ namespace {
 
 using namespace mova;
 
-constexpr int kVersion = 200;  // 0.2.0
+constexpr int kVersion = 300;  // 0.3.0
 constexpr int kMaxT = 1 << 24;
 // Token counts up to this take the weight-streaming decode path by default
 // (measured faster than the grouped path for every T up to its limit).
