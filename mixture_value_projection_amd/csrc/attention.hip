@@ -1,80 +1,652 @@
-// Attention of one new token per request over the paged key-value cache.
+// Attention of one new token per request over the paged key-value cache
+// (page "MoVA: routing the value vectors ...", section "Where the routing
+// happens": 32 query heads over 8 key heads of 128; the cache holds ordinary
+// key and routed value vectors).
+//
+//   out_i = sum_p exp(s_ip - m_i) v_p / sum_p exp(s_ip - m_i),  s_ip = scale q_i . k_p
+//
+// in one pass over the keys with the running maximum m and sum of a softmax.
+// A key and its value are read once for the group of query heads that share
+// them: 4 flops a byte at a group of 4, so the kernel is bound by reading the
+// cache, and everything below serves that stream.
+//
+// Work: the keys of a request, per group of key heads, are cut into tiles.
+// All tiles of the batch lie in one line, request after request, and each of
+// the kGrid workgroups (one per CU) takes an equal stretch of it, so ragged
+// batches and single long requests fill the chip alike and the host needs no
+// lengths.  A request whose tiles lie in one stretch is finished there; else
+// each stretch leaves its part (m, sum, unnormalised out; fp32) in the
+// workspace and attention_join_kernel adds them.
+//
+// A workgroup's four waves take four key heads at the same positions (rows of
+// 4 x head_dim elements are contiguous), or stripes of the tiles when there
+// are fewer heads.  Each wave is a pipeline of its own: a ring of tiles in
+// LDS, filled by direct-to-LDS loads with kStages - 1 tiles in flight while
+// one is used; no barrier but at the ends.  The block table (and the list of
+// chosen blocks) is fetched the same way, kStages tiles ahead of the tile
+// whose addresses need it.
+//
+// A tile's logits are MFMA products K Q^T (16 keys x 16 query heads, heads
+// past the group are zero), so a lane holds four keys of one query head and
+// the softmax needs two lane exchanges a tile.  Their weights are then, as
+// they lie in the registers, the second operand of out^T = V^T P^T, whose
+// first operand the transposing LDS reads deliver; the sums over keys may run
+// in any order as long as both operands agree.  Weights are rounded to bf16 for this product (nearest even;
+// relative 2^-9 on average below, against bf16 outputs); maxima, sums and
+// accumulators are fp32.  8-bit elements are widened to bf16, which is exact.
 #include <algorithm>
+#include <atomic>
 
+#include "kernels.h"
 #include "paged.h"
 
 namespace mova {
 
-// Workgroup (query head, request); a wave takes every fourth key.
+// Numbers of the line of tiles that the join needs: prefix[b] is the first
+// tile of request b, prefix[B] the tiles of a stretch.
+struct Parts {
+  long long* prefix;
+  float* ml;  // [two a workgroup][heads per group][rows][2]
+  float* o;   // [two a workgroup][heads per group][rows][D]
+};
+
+namespace {
+
+constexpr int kGrid = 256;         // one workgroup per CU
+constexpr int kRingBytes = 32768;  // keys and values in LDS per wave
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+
+// Waves of a workgroup on different key heads; the others split the tiles.
+int heads_per_group(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
+
+template <int D, bool kFp8>
+struct Tile {
+  static constexpr int kBytes = kFp8 ? 1 : 2;                   // of an element
+  static constexpr int kKeys = (!kFp8 && D >= 128) ? 16 : 32;   // of a tile
+  static constexpr int kRow = D * kBytes;                       // bytes of a key
+  static constexpr int kChunks = kRow / 16;                     // 16-byte pieces of a key
+  static constexpr int kRowsPerLoad = 64 / kChunks;
+  static constexpr int kLoads = kKeys / kRowsPerLoad;           // wave loads per side
+  static constexpr int kSide = kKeys * kRow;                    // bytes of a side (K or V)
+  static constexpr int kStages = kRingBytes / (2 * kSide);
+  static constexpr int kLds = kRingBytes + 2 * kStages * 256;   // with the block numbers
+  static_assert(kStages >= 2 && kChunks <= 32 && kRowsPerLoad >= 2, "tile shape");
+  // Piece c of row r lies at piece c ^ swizzle(r), so that the 8 rows of one
+  // phase of the key fragments' reads, and the rows that 16 lanes of a
+  // transposing read take, fall into different banks.
+  static __device__ __forceinline__ int swizzle_k(int r) {
+    return (kChunks >= 8 ? r : r / (8 / kChunks)) & (kChunks - 1) & 15;
+  }
+  static __device__ __forceinline__ int swizzle_v(int r) {
+    if constexpr (!kFp8) return (kChunks >= 16 ? 2 * r : 2 * (r / (16 / kChunks))) & (kChunks - 1) & 15;
+    else if constexpr (kChunks == 4) return ((r >> 4) & 1) | ((r >> 1) & 2);
+    else if constexpr (kChunks == 8) return ((r >> 1) & 1) | ((r >> 3) & 2) | (r & 4);
+    else return (r & 3) | ((r >> 2) & 4) | ((r << 1) & 8);
+  }
+};
+
+size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
+
+Parts parts_of(const AttentionArgs& a) {
+  const size_t rows = (size_t)kGrid * 2 * heads_per_group(a.H) * std::min(a.Hq / a.H, 16);
+  Parts p;
+  p.prefix = (long long*)a.part;
+  p.ml = a.part + prefix_floats(a.B);
+  p.o = p.ml + (rows * 2 + 63) / 64 * 64;
+  return p;
+}
+
+// Keys request b reads, [lo, lo + keys) or, with a list, keep * block_size
+// listed positions.
+struct Span {
+  int len, lo;
+  int keys;
+};
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
+  Span s;
+  s.len = a.num_blocks > 0 ? request_len(a.seq_lens, b, a.max_blocks, a.block_size) : 0;
+  s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
+  s.keys = a.sel != nullptr ? (s.len > 0 ? a.keep * a.block_size : 0) : s.len - s.lo;
+  return s;
+}
+
+// Direct-to-LDS loads of 16 and 4 bytes a lane, to consecutive places.
+__device__ __forceinline__ void stream_to_lds(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, kLdsLoadNonTemporal);
+}
+__device__ __forceinline__ void word_to_lds(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 4, 0, 0);
+}
+
+// Four transposing LDS reads of 8 bytes a lane (16 lanes hand out 16 columns of
+// the 128 bytes that they address) and the wait for them, in one block: as
+// builtins, each read would first wait for every direct load in flight (the
+// compiler cannot tell which part of the ring those fill), which would empty
+// the pipeline.
 template <bool kFp8>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a) {
-  constexpr int kMaxPer = 4;  // channels a lane: D <= 256
-  __shared__ float s_m[4], s_l[4], s_o[4][64 * kMaxPer];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int hq = blockIdx.x, b = blockIdx.y;
-  const int h = hq / (a.Hq / a.H);
-  const int per = a.D / 64;
-  const int len = request_len(a.seq_lens, b, a.max_blocks, a.block_size);
-  const int lo = a.window > 0 ? max(0, len - a.window) : 0;
-  const int blocks = ceil_div(len, a.block_size);
-  const long long total = a.sel != nullptr ? (long long)a.keep * a.block_size : len;
-  const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f);
-  float q[kMaxPer], o[kMaxPer] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < per; ++i) q[i] = (float)a.q[((size_t)b * a.Hq + hq) * a.D + i * 64 + lane];
-  float m = -__builtin_huge_valf(), l = 0.f;
-  auto elem = [&](const void* pool, size_t at) -> float {
-    if constexpr (kFp8) return __builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t*)pool)[at], 0);
-    else return (float)((const __bf16*)pool)[at];
-  };
-  for (long long v = wave; v < total; v += 4) {
-    int j = (int)(v / a.block_size);
-    const int r = (int)(v - (long long)j * a.block_size);
-    if (a.sel != nullptr) j = a.sel[((size_t)b * a.H + h) * a.keep + j];
-    if (j < 0 || j >= blocks) continue;
-    const int p = j * a.block_size + r;
-    if (p < lo || p >= len) continue;
-    const int page = a.table[(size_t)b * a.max_blocks + j];
-    if (page < 0 || page >= a.num_blocks) continue;
-    const size_t at = (((size_t)page * a.block_size + r) * a.H + h) * a.D + lane;
-    float s = 0.f;
-    for (int i = 0; i < per; ++i) s += q[i] * elem(a.k_cache, at + i * 64);
-    for (int x = 32; x > 0; x >>= 1) s += __shfl_xor(s, x);
-    s *= qs;
-    const float mn = fmaxf(m, s);
-    const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
-    const float keep = expf(m - safe), p1 = expf(s - safe);
-    m = mn;
-    l = l * keep + p1;
-    for (int i = 0; i < per; ++i) o[i] = o[i] * keep + p1 * elem(a.v_cache, at + i * 64);
+__device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (&at)[4]) {
+  if constexpr (kFp8)
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %4\n\tds_read_b64_tr_b8 %1, %5\n\t"
+        "ds_read_b64_tr_b8 %2, %6\n\tds_read_b64_tr_b8 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+        : "memory");
+  else
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %5\n\t"
+        "ds_read_b64_tr_b16 %2, %6\n\tds_read_b64_tr_b16 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+        : "memory");
+}
+
+// A use of x: the load behind it is waited for here and not later.
+template <class X>
+__device__ __forceinline__ void loaded(X& x) {
+  asm volatile("" : "+v"(x));
+}
+
+// Waits until at most `left` <= kMost groups of kOps vector-memory operations
+// are outstanding, and for LDS.
+template <int kMost, int kOps>
+__device__ __forceinline__ void wait_groups(int left) {
+  if constexpr (kMost == 0) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+  } else {
+    if (left == kMost) __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kMost * kOps));
+    else wait_groups<kMost - 1, kOps>(left);
   }
-  if (lane == 0) { s_m[wave] = m; s_l[wave] = l; }
-  for (int i = 0; i < per; ++i) s_o[wave][i * 64 + lane] = o[i];
+}
+
+}  // namespace
+
+// kHeads: key heads of a workgroup; 4 / kHeads waves share a head's tiles.
+template <int D, bool kFp8, int kHeads, bool kList>
+__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts, FastDiv by_block) {
+  using T = Tile<D, kFp8>;
+  constexpr int kStripes = 4 / kHeads;
+  constexpr int S = T::kStages;
+  constexpr int kSub = T::kKeys / 16;      // 16-key parts of a tile
+  constexpr int kCols = D / 16;
+  constexpr int kGroupLoads = 2 * T::kLoads + (kList ? 2 : 1);
+  static_assert((S - 1) * kGroupLoads < 64, "outstanding loads");
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  __shared__ long long s_tmp[4], s_first;
+  __shared__ int s_b;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int hsub = wave / kStripes, stripe = wave % kStripes;
+  const int G = a.Hq / a.H;
+  const int qtiles = ceil_div(G, 16);
+  const int rows_per_b = a.H / kHeads * qtiles;
+  char* ring = lds + wave * T::kLds;
+  int* pages = (int*)(ring + kRingBytes);
+  int* listed = pages + S * 64;
+
+  // Where this workgroup's stretch of the line of tiles begins.
+  auto tiles_of = [&](const Span& s) { return ceil_div(s.keys, T::kKeys * kStripes); };
+  const int per = ceil_div(a.B, 256);
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += (long long)tiles_of(span_of(a, b)) * rows_per_b;
+  long long before = block_exclusive_scan<4>(mine, s_tmp, &total);
+  const long long stretch = max((total + kGrid - 1) / kGrid, 1ll);
+  const long long start = stretch * blockIdx.x;
+  const long long end = min(start + stretch, total);
+  if (before <= start && start < before + mine) {
+    long long p = before;
+    int b = b0;
+    for (;; ++b) {
+      const long long c = (long long)tiles_of(span_of(a, b)) * rows_per_b;
+      if (start < p + c) break;
+      p += c;
+    }
+    s_b = b;
+    s_first = p;
+  }
+  if (blockIdx.x == 0) {
+    for (int b = b0; b < b1; ++b) {
+      parts.prefix[b] = before;
+      before += (long long)tiles_of(span_of(a, b)) * rows_per_b;
+    }
+    if (tid == 0) parts.prefix[a.B] = stretch;
+  }
+  if (start >= total) return;
   __syncthreads();
-  const float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float safe = M == -__builtin_huge_valf() ? 0.f : M;
-  float L = 0.f;
-  for (int w = 0; w < 4; ++w) L += s_l[w] * expf(s_m[w] - safe);
-  if (threadIdx.x < a.D) {
-    float x = 0.f;
-    for (int w = 0; w < 4; ++w) x += s_o[w][threadIdx.x] * expf(s_m[w] - safe);
-    x = L == 0.f ? 0.f : x / L * (a.v_scale != nullptr ? a.v_scale[h] : 1.f);
-    a.out[((size_t)b * a.Hq + hq) * a.D + threadIdx.x] = (__bf16)x;
+
+  const size_t row_bytes = (size_t)a.H * T::kRow;
+  int b = s_b;
+  long long at = s_first;  // first tile of request b
+  Span sp = span_of(a, b);
+  int n = tiles_of(sp);
+  for (long long pos = start; pos < end;) {
+    while (pos >= at + (long long)n * rows_per_b) {
+      at += (long long)n * rows_per_b;
+      sp = span_of(a, ++b);
+      n = tiles_of(sp);
+    }
+    const int row = (int)((pos - at) / n);
+    const int t0 = (int)(pos - at - (long long)row * n);
+    const int t1 = (int)min((long long)n, t0 + (end - pos));
+    pos += t1 - t0;
+    const int hgroup = row / qtiles, qt = row - hgroup * qtiles;
+    const int h = hgroup * kHeads + hsub;
+    const int nt = t1 - t0;
+    const int blocks = ceil_div(sp.len, a.block_size);
+    const int32_t* table = a.table + (size_t)b * a.max_blocks;
+    const int32_t* list = kList ? a.sel + ((size_t)b * a.H + h) * a.keep : nullptr;
+    const int rows = min(G - qt * 16, 16);
+    const bool has_row = r16 < rows;
+    const size_t qrow = (size_t)b * a.Hq + h * G + qt * 16 + r16;
+
+    // The lane's key of tile x: its index in the span, its block in the span
+    // or list, and its row of that block.
+    auto locate = [&](int x, int* blk, int* r) {
+      const int v = ((t0 + x) * kStripes + stripe) * T::kKeys + (lane & (T::kKeys - 1));
+      const int p = kList ? v : sp.lo + v;
+      *blk = fast_div(p, by_block);
+      *r = p - *blk * a.block_size;
+    };
+    auto list_address = [&](int x) {
+      int blk, r;
+      locate(x, &blk, &r);
+      return list + min(blk, a.keep - 1);
+    };
+    // Table row entry to fetch for tile x; `blk` from the list in that mode.
+    auto table_address = [&](int blk) { return table + min(max(blk, 0), a.max_blocks - 1); };
+    auto block_of = [&](int x, int from_list) {
+      int blk, r;
+      locate(x, &blk, &r);
+      return kList ? from_list : blk;
+    };
+    // Issues tile x: addresses from its block numbers, the loads of its keys
+    // and values, and the fetches for later tiles.  Returns which of its keys
+    // take part (bit = key).
+    auto issue = [&](int x, int page, int from_list, int next_list) -> uint32_t {
+      int blk, r;
+      locate(x, &blk, &r);
+      bool ok;
+      if constexpr (kList) {
+        ok = blk < a.keep && from_list >= 0 && from_list < blocks;
+        const int p = from_list * a.block_size + r;
+        ok = ok && p >= sp.lo && p < sp.len;
+      } else {
+        ok = blk * a.block_size + r < sp.len;
+      }
+      ok = ok && page >= 0 && page < a.num_blocks;
+      const uint32_t mask = (uint32_t)__ballot(ok) & (uint32_t)((1ull << T::kKeys) - 1);
+      const int slot = ok ? page * a.block_size + r : 0;
+      char* stage = ring + (x % S) * 2 * T::kSide;
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) {
+        const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
+        const size_t off = (size_t)(uint32_t)__shfl(slot, rr) * row_bytes + (size_t)h * T::kRow;
+        const int c = lane % T::kChunks;
+        stream_to_lds((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16, stage + i * 1024);
+        stream_to_lds((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
+                      stage + T::kSide + i * 1024);
+      }
+      word_to_lds(table_address(block_of(x + S, next_list)), pages + (x % S) * 64);
+      if constexpr (kList) word_to_lds(list_address(x + 2 * S), listed + (x % S) * 64);
+      return mask;
+    };
+
+    // Queries: with 8-bit keys a lane's 16-byte piece serves two products.
+    Frag16 qf[D / 32];
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const int d = kFp8 ? 64 * (u / 2) + 16 * g4 + 8 * (u & 1) : 32 * u + 8 * g4;
+      qf[u].u = u32x4{0u, 0u, 0u, 0u};
+      if (has_row) qf[u].u = load16(a.q + qrow * D + d);
+    }
+    const float ks = a.k_scale != nullptr ? a.k_scale[h] : 1.f;
+    const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
+    const float qs = a.scale * ks * 1.44269504088896340736f;  // logits in powers of two
+
+    uint32_t masks[S];  // of the tiles in the ring
+    int ahead[S];       // list entries of the S tiles after them
+    // The last segment's LDS reads are done before the ring is filled again.
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+    asm volatile("" ::: "memory");
+    {
+      int lst[2 * S], pg[S];
+#pragma unroll
+      for (int i = 0; i < 2 * S; ++i) lst[i] = kList ? *list_address(i) : 0;
+#pragma unroll
+      for (int i = 0; i < S; ++i) pg[i] = *table_address(block_of(i, lst[i]));
+      // All of them here, so that no wait for one comes between the loads below.
+#pragma unroll
+      for (int i = 0; i < S; ++i) loaded(pg[i]), loaded(lst[S + i]);
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) loaded(qf[u].u);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        masks[i] = 0;
+        if (i < nt) masks[i] = issue(i, pg[i], lst[i], lst[S + i]);
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) ahead[i] = lst[S + i];
+    }
+
+    f32x4 o[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_huge_valf(), l = 0.f;
+
+    for (int x = 0; x < nt; ++x) {
+      // Tile x and the fetches issued with it have landed.
+      wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
+      asm volatile("" ::: "memory");
+      char* stage = ring + (x % S) * 2 * T::kSide;
+      const uint32_t mask = masks[0];
+#pragma unroll
+      for (int i = 0; i + 1 < S; ++i) masks[i] = masks[i + 1];
+      constexpr uint32_t kAll = (uint32_t)((1ull << T::kKeys) - 1);
+      if (mask != 0) {
+        if (mask != kAll) {
+          // Values that take no part become zeros: their weight is zero, but
+          // what lies there may be infinite or NaN.
+#pragma unroll
+          for (int i = 0; i < T::kLoads; ++i)
+            if (!((mask >> (i * T::kRowsPerLoad + lane / T::kChunks)) & 1))
+              *reinterpret_cast<u32x4*>(stage + T::kSide + i * 1024 + lane * 16) =
+                  u32x4{0u, 0u, 0u, 0u};
+        }
+        float p[kSub][4];
+        float top = -__builtin_huge_valf();
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+          f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+          const int rr = 16 * t + r16;
+          const char* kr = stage + rr * T::kRow;
+          if constexpr (!kFp8) {
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) {
+              Frag16 kf;
+              kf.u = *reinterpret_cast<const u32x4*>(kr + ((4 * u + g4) ^ T::swizzle_k(rr)) * 16);
+              s = mfma16x16x32(kf.h, qf[u].h, s);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+              const u32x4 w = *reinterpret_cast<const u32x4*>(kr + ((4 * u + g4) ^ T::swizzle_k(rr)) * 16);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                Frag16 kf;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int ww = (int)w[2 * half + i];
+                  kf.u[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ww, 1.f, false));
+                  kf.u[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ww, 1.f, true));
+                }
+                s = mfma16x16x32(kf.h, qf[2 * u + half].h, s);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[t][i] = s[i] * qs;
+            if (mask != kAll && !((mask >> (16 * t + 4 * g4 + i)) & 1)) p[t][i] = -__builtin_huge_valf();
+            top = fmaxf(top, p[t][i]);
+          }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
+        if (__any(mn > m)) {
+          const float keep = __builtin_amdgcn_exp2f(m - safe);
+          l *= keep;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c][i] *= keep;
+        }
+        m = mn;
+        union PFrag {
+          s16x4 h[2];
+          bf16x8 w;
+        } pf;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = __builtin_amdgcn_exp2f(p[t][i] - safe);
+            l += e;
+            pf.h[t][i] = (short)f32_to_bf16_bits(e);
+          }
+        const uint32_t vt = (uint32_t)(uintptr_t)(lds_void*)(stage + T::kSide);
+        constexpr int kPer = kFp8 ? 1 : kSub;  // reads a 16-column part
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 4 / kPer) {
+          uint32_t from[4];
+          i32x2 got[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i / kPer, t = i % kPer;
+            const int rr = kFp8 ? 4 * g4 + (r16 / 2 & 3) + 16 * (r16 / 8) : 16 * t + 4 * g4 + r16 / 4;
+            const int piece = kFp8 ? c : 2 * c + (r16 & 3) / 2;
+            from[i] = vt + rr * T::kRow + (piece ^ T::swizzle_v(rr)) * 16 + 8 * (r16 & 1);
+          }
+          read4_transposed<kFp8>(got, from);
+#pragma unroll
+          for (int i = 0; i < 4 / kPer; ++i) {
+            f32x4& acc = o[c0 + i];
+            if constexpr (kFp8) {
+              Frag16 vf;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                vf.u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, false));
+                vf.u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, true));
+              }
+              acc = mfma16x16x32(vf.h, pf.w, acc);
+            } else if constexpr (kSub == 2) {
+              PFrag vf;
+              vf.h[0] = __builtin_bit_cast(s16x4, got[2 * i]);
+              vf.h[1] = __builtin_bit_cast(s16x4, got[2 * i + 1]);
+              acc = mfma16x16x32(vf.w, pf.w, acc);
+            } else {
+              acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, got[i]), pf.h[0],
+                                                              acc, 0, 0, 0);
+            }
+          }
+        }
+      }
+      if (x + S < nt) {
+        // Tile x + S takes this tile's place; the block numbers of it (and
+        // the list entries of tile x + 2 S) came with tile x.
+        const int page = pages[(x % S) * 64 + lane];
+        const int nxt = kList ? listed[(x % S) * 64 + lane] : 0;
+        const int cur = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < S; ++i) ahead[i] = ahead[i + 1];
+        ahead[S - 1] = nxt;
+        __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+        asm volatile("" ::: "memory");
+        masks[S - 1] = issue(x + S, page, cur, nxt);
+      }
+    }
+
+    // The four lanes of a query head hold its sum in parts.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if constexpr (kStripes > 1) {
+      // Stripes of a head meet in its first wave, through the ring.
+      __syncthreads();
+      float* box = (float*)(lds + wave * T::kLds);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) *reinterpret_cast<f32x4*>(box + (c * 64 + lane) * 4) = o[c];
+      float* ml = (float*)(ring + kRingBytes);
+      ml[lane] = m;
+      ml[64 + lane] = l;
+      __syncthreads();
+      if (stripe == 0) {
+#pragma unroll 1
+        for (int s = 1; s < kStripes; ++s) {
+          const char* other = lds + (wave + s) * T::kLds;
+          const float* oml = (const float*)(other + kRingBytes);
+          const float m2 = oml[lane], l2 = oml[64 + lane];
+          const float mn = fmaxf(m, m2);
+          const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
+          const float e1 = __builtin_amdgcn_exp2f(m - safe), e2 = __builtin_amdgcn_exp2f(m2 - safe);
+          l = l * e1 + l2 * e2;
+          m = mn;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            const f32x4 o2 = *reinterpret_cast<const f32x4*>((const float*)other + (c * 64 + lane) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c][i] = o[c][i] * e1 + o2[i] * e2;
+          }
+        }
+      }
+      __syncthreads();
+      if (stripe != 0) continue;
+    }
+    if (!has_row) continue;
+    if (nt == n) {
+      const float f = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        uint2 w;
+        w.x = (uint32_t)f32_to_bf16_bits(o[c][0] * f) | ((uint32_t)f32_to_bf16_bits(o[c][1] * f) << 16);
+        w.y = (uint32_t)f32_to_bf16_bits(o[c][2] * f) | ((uint32_t)f32_to_bf16_bits(o[c][3] * f) << 16);
+        *reinterpret_cast<uint2*>(a.out + qrow * D + 16 * c + 4 * g4) = w;
+      }
+      if (a.lse != nullptr && g4 == 0)
+        a.lse[qrow] = l == 0.f ? -__builtin_huge_valf()
+                               : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+    } else {
+      const int cap = min(G, 16);
+      const size_t part = ((size_t)(blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kHeads + hsub) * cap + r16;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        *reinterpret_cast<f32x4*>(parts.o + part * D + 16 * c + 4 * g4) = o[c];
+      if (g4 == 0) {
+        parts.ml[2 * part] = m;
+        parts.ml[2 * part + 1] = l;
+      }
+    }
   }
-  if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[(size_t)b * a.Hq + hq] = L == 0.f ? -__builtin_huge_valf() : safe + logf(L);
+}
+
+// Adds the parts of a request's query head that was split over stretches, and
+// writes the rows of requests without keys.  Workgroup (query head, request).
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int heads,
+                                                             int tile_keys) {
+  __shared__ float s_o[256 * 4], s_m[4], s_l[4];
+  const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, D = a.D;
+  const size_t out_row = (size_t)b * a.Hq + hq;
+  const int n = ceil_div(span_of(a, b).keys, tile_keys);
+  if (n == 0) {
+    if (tid < D / 2) ((uint32_t*)(a.out + out_row * D))[tid] = 0u;
+    if (tid == 0 && a.lse != nullptr) a.lse[out_row] = -__builtin_huge_valf();
+    return;
+  }
+  const int G = a.Hq / a.H, h = hq / G, gi = hq - h * G;
+  const int qtiles = ceil_div(G, 16), cap = min(G, 16);
+  // Quotients of whole numbers below 2^52, exact when floored.
+  const double stretch = (double)parts.prefix[a.B];
+  const long long first = parts.prefix[b] + (long long)(h / heads * qtiles + gi / 16) * n;
+  const int w0 = (int)((double)first / stretch), w1 = (int)((double)(first + n - 1) / stretch);
+  if (w0 == w1) return;
+  auto part_of = [&](int w) {
+    return ((size_t)(w * 2 + (w == w0 ? 1 : 0)) * heads + h % heads) * cap + gi % 16;
+  };
+  // The largest maximum, then sums over the parts, in a fixed order.
+  float m = -__builtin_huge_valf();
+  for (int w = w0 + tid; w <= w1; w += 256) m = fmaxf(m, parts.ml[2 * part_of(w)]);
+  for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+  if ((tid & 63) == 0) s_m[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
+  float l = 0.f;
+  for (int w = w0 + tid; w <= w1; w += 256) {
+    const size_t p = part_of(w);
+    l += parts.ml[2 * p + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
+  }
+  for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x);
+  if ((tid & 63) == 0) s_l[tid >> 6] = l;
+  const int lanes = D / 4, sub = tid / lanes, subs = 256 / lanes, c = tid % lanes;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int w = w0 + sub; w <= w1; w += subs) {
+    const size_t p = part_of(w);
+    const float e = __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
+    const f32x4 x = *reinterpret_cast<const f32x4*>(parts.o + p * D + 4 * c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += x[i] * e;
+  }
+  *reinterpret_cast<f32x4*>(s_o + tid * 4) = o;
+  __syncthreads();
+  if (tid < D) {
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    float x = 0.f;
+    for (int s = 0; s < subs; ++s) x += s_o[s * D + tid];
+    const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
+    a.out[out_row * D + tid] = (__bf16)(l == 0.f ? 0.f : x * (vs / l));
+    if (tid == 0 && a.lse != nullptr)
+      a.lse[out_row] = l == 0.f ? -__builtin_huge_valf()
+                                : (safe + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+  }
 }
 
 size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int block_size,
                                 int keep) {
-  (void)Hq; (void)H; (void)D; (void)max_blocks; (void)block_size; (void)keep;
-  return B > 0 ? 64 : 0;
+  (void)max_blocks; (void)block_size; (void)keep;
+  if (B == 0) return 0;
+  const size_t rows = (size_t)kGrid * 2 * heads_per_group(H) * std::min(Hq / H, 16);
+  return prefix_floats(B) + (rows * 2 + 63) / 64 * 64 + rows * D;
 }
 
-hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
-  const dim3 grid(a.Hq, a.B);
-  if (a.dtype == kCacheFp8) attention_kernel<true><<<grid, 256, 0, stream>>>(a);
-  else attention_kernel<false><<<grid, 256, 0, stream>>>(a);
+namespace {
+
+template <int D, bool kFp8, int kHeads, bool kList>
+hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
+  using T = Tile<D, kFp8>;
+  static std::atomic<unsigned long long> done{0};
+  hipError_t e = once_per_device(done, [&] {
+    return hipFuncSetAttribute(
+        reinterpret_cast<const void*>(attention_kernel<D, kFp8, kHeads, kList>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, 4 * T::kLds);
+  });
+  if (e != hipSuccess) return e;
+  const Parts parts = parts_of(a);
+  attention_kernel<D, kFp8, kHeads, kList>
+      <<<kGrid, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size));
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  attention_join_kernel<<<dim3(a.Hq, a.B), 256, 0, stream>>>(a, parts, kHeads,
+                                                              T::kKeys * (4 / kHeads));
   return hipGetLastError();
+}
+
+template <int D, bool kFp8>
+hipError_t launch_heads(const AttentionArgs& a, hipStream_t stream) {
+  const bool list = a.sel != nullptr;
+  switch (heads_per_group(a.H)) {
+    case 4: return list ? launch_cfg<D, kFp8, 4, true>(a, stream) : launch_cfg<D, kFp8, 4, false>(a, stream);
+    case 2: return list ? launch_cfg<D, kFp8, 2, true>(a, stream) : launch_cfg<D, kFp8, 2, false>(a, stream);
+    default: return list ? launch_cfg<D, kFp8, 1, true>(a, stream) : launch_cfg<D, kFp8, 1, false>(a, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
+  const bool fp8 = a.dtype == kCacheFp8;
+  switch (a.D) {
+    case 64: return fp8 ? launch_heads<64, true>(a, stream) : launch_heads<64, false>(a, stream);
+    case 128: return fp8 ? launch_heads<128, true>(a, stream) : launch_heads<128, false>(a, stream);
+    case 256: return fp8 ? launch_heads<256, true>(a, stream) : launch_heads<256, false>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace mova

@@ -88,6 +88,46 @@ hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
 // ---- device helpers ---------------------------------------------------------
 
+// n / d for 0 <= n < 2^31 as a product and a shift (d > 0).  With
+// s = ceil(log2 d), mul = floor(2^(31 + s) / d) + 1 exceeds 2^(31 + s) / d by at
+// most 1, so the product exceeds n / d by less than n / 2^(31 + s) < 1 / d.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+inline FastDiv make_fast_div(int d) {
+  uint32_t s = 0;
+  while ((1ll << s) < d) ++s;
+  return {(uint32_t)((1ull << (31 + s)) / (unsigned)d + 1), 31 + s};
+}
+__device__ __forceinline__ int fast_div(int n, FastDiv f) {
+  return (int)(((unsigned long long)(uint32_t)n * f.mul) >> f.shift);
+}
+
+// Exclusive scan of one number a thread over a workgroup of kWaves waves;
+// *total gets the sum.  `tmp` holds one number a wave and may be used again
+// after the next barrier.
+template <int kWaves>
+__device__ __forceinline__ long long block_exclusive_scan(long long x, long long* tmp,
+                                                          long long* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const long long up = __shfl_up(inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 63) tmp[wave] = inc;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += tmp[w];
+    sum += tmp[w];
+  }
+  *total = sum;
+  return before + inc - x;
+}
+
 // Tokens of request b: its length, kept inside its row of the block table.
 __device__ __forceinline__ int request_len(const int32_t* seq_lens, int b, int max_blocks,
                                            int block_size) {

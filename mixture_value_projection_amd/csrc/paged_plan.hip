@@ -31,29 +31,6 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 
-// Exclusive scan of one number a thread over the workgroup; *total gets the
-// sum.  `tmp` holds one number a wave; it may be reused after the next barrier.
-__device__ __forceinline__ long long block_exclusive_scan(long long x, long long* tmp,
-                                                          long long* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  long long inc = x;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const long long up = __shfl_up(inc, o);
-    if (lane >= o) inc += up;
-  }
-  if (lane == 63) tmp[wave] = inc;
-  __syncthreads();
-  long long before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanThreads / 64; ++w) {
-    if (w < wave) before += tmp[w];
-    sum += tmp[w];
-  }
-  *total = sum;
-  return before + inc - x;
-}
-
 // The last i in [0, n) with a[i] <= x (a[0] <= x, a not decreasing).
 __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
   int lo = 0, hi = n;
@@ -95,8 +72,8 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     else back += (min((long long)max(a.cached[b], 0), most) + bs - 1) / bs;
   }
   long long all_rows, all_back, all_need;
-  const long long row0 = block_exclusive_scan(rows, tmp[0], &all_rows);
-  const long long back0 = block_exclusive_scan(back, tmp[1], &all_back);
+  const long long row0 = block_exclusive_scan<kPlanThreads / 64>(rows, tmp[0], &all_rows);
+  const long long back0 = block_exclusive_scan<kPlanThreads / 64>(back, tmp[1], &all_back);
   const int have = (int)min((long long)count + all_back, (long long)a.free_capacity);
 
   // Needs of the requests whose tokens fit their table row and the T rows.
@@ -110,7 +87,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     at += max(n, 0);
     need += max(need_of(min((long long)max(a.cached[b], 0), most), n, at), 0ll);
   }
-  const long long need0 = block_exclusive_scan(need, tmp[2], &all_need);
+  const long long need0 = block_exclusive_scan<kPlanThreads / 64>(need, tmp[2], &all_need);
 
   long long upto = need0, taken = 0, given = back0;
   at = row0;
