@@ -175,8 +175,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   constexpr int kGroupLoads = 2 * T::kLoads + (kList ? 2 : 1);
   static_assert((S - 1) * kGroupLoads < 64, "outstanding loads");
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  __shared__ long long s_tmp[4], s_first;
-  __shared__ int s_b;
+  __shared__ LineShared s_line;
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -190,43 +189,18 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   int* pages = (int*)(ring + kRingBytes);
   int* listed = pages + S * 64;
 
-  // Where this workgroup's stretch of the line of tiles begins.
   auto tiles_of = [&](const Span& s) { return ceil_div(s.keys, T::kKeys * kStripes); };
-  const int per = ceil_div(a.B, 256);
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += (long long)tiles_of(span_of(a, b)) * rows_per_b;
-  long long before = block_exclusive_scan<4>(mine, s_tmp, &total);
-  const long long stretch = max((total + kGrid - 1) / kGrid, 1ll);
-  const long long start = stretch * blockIdx.x;
-  const long long end = min(start + stretch, total);
-  if (before <= start && start < before + mine) {
-    long long p = before;
-    int b = b0;
-    for (;; ++b) {
-      const long long c = (long long)tiles_of(span_of(a, b)) * rows_per_b;
-      if (start < p + c) break;
-      p += c;
-    }
-    s_b = b;
-    s_first = p;
-  }
-  if (blockIdx.x == 0) {
-    for (int b = b0; b < b1; ++b) {
-      parts.prefix[b] = before;
-      before += (long long)tiles_of(span_of(a, b)) * rows_per_b;
-    }
-    if (tid == 0) parts.prefix[a.B] = stretch;
-  }
-  if (start >= total) return;
-  __syncthreads();
+  Line line;
+  if (!line_begin(a.B, [&](int b) { return (long long)tiles_of(span_of(a, b)) * rows_per_b; }, s_line,
+                  parts.prefix, &line))
+    return;
 
   const size_t row_bytes = (size_t)a.H * T::kRow;
-  int b = s_b;
-  long long at = s_first;  // first tile of request b
+  int b = line.b;
+  long long at = line.first;  // first tile of request b
   Span sp = span_of(a, b);
   int n = tiles_of(sp);
-  for (long long pos = start; pos < end;) {
+  for (long long pos = line.start; pos < line.end;) {
     while (pos >= at + (long long)n * rows_per_b) {
       at += (long long)n * rows_per_b;
       sp = span_of(a, ++b);
@@ -234,7 +208,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
     }
     const int row = (int)((pos - at) / n);
     const int t0 = (int)(pos - at - (long long)row * n);
-    const int t1 = (int)min((long long)n, t0 + (end - pos));
+    const int t1 = (int)min((long long)n, t0 + (line.end - pos));
     pos += t1 - t0;
     const int hgroup = row / qtiles, qt = row - hgroup * qtiles;
     const int h = hgroup * kHeads + hsub;

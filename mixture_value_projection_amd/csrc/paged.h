@@ -57,7 +57,7 @@ struct SelectArgs {
   int B, Hq, H, D;
   int keep, first, last;
   int32_t* sel;    // [B, H, keep]
-  double* scores;  // [B, H, max_blocks] scratch
+  unsigned long long* keys;  // [B, H, max_blocks] scratch
 };
 hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream);
 
@@ -126,6 +126,53 @@ __device__ __forceinline__ long long block_exclusive_scan(long long x, long long
   }
   *total = sum;
   return before + inc - x;
+}
+
+// A line of work over a ragged batch: request b brings cost(b) units, one
+// request after the other, and each of gridDim.x workgroups takes an equal
+// stretch [start, end) of them.  The workgroup finds the request that its
+// stretch begins in, and that request's first unit, from the lengths alone.
+struct Line {
+  long long stretch, start, end;
+  long long first;  // first unit of request b
+  int b;
+};
+struct LineShared {
+  long long tmp[4], first;
+  int b;
+};
+// For workgroups of 256 threads.  False: nothing to do.  `prefix` (null, or
+// B + 1 numbers): workgroup 0 writes the requests' first units and the stretch.
+template <class Cost>
+__device__ __forceinline__ bool line_begin(int B, Cost cost, LineShared& sh, long long* prefix,
+                                           Line* line) {
+  const int per = ceil_div(B, 256);
+  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += cost(b);
+  long long before = block_exclusive_scan<4>(mine, sh.tmp, &total);
+  line->stretch = max((total + gridDim.x - 1) / gridDim.x, 1ll);
+  line->start = line->stretch * blockIdx.x;
+  line->end = min(line->start + line->stretch, total);
+  if (before <= line->start && line->start < before + mine) {
+    long long at = before;
+    int b = b0;
+    for (long long c; line->start >= at + (c = cost(b)); ++b) at += c;
+    sh.b = b;
+    sh.first = at;
+  }
+  if (prefix != nullptr && blockIdx.x == 0) {
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = before;
+      before += cost(b);
+    }
+    if (threadIdx.x == 0) prefix[B] = line->stretch;
+  }
+  if (line->start >= total) return false;
+  __syncthreads();
+  line->b = sh.b;
+  line->first = sh.first;
+  return true;
 }
 
 // Tokens of request b: its length, kept inside its row of the block table.

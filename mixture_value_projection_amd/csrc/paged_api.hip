@@ -164,7 +164,7 @@ int mova_block_select(const void* q, const void* k_bounds, int num_blocks, int b
   if (rc != MOVA_OK) return rc;
   const SelectArgs a{(const __bf16*)q, (const __bf16*)k_bounds, num_blocks, block_size,
                      block_table, max_blocks, seq_lens, B, n_heads, n_kv_heads, head_dim, keep,
-                     keep_first, keep_last, sel_blocks, (double*)workspace};
+                     keep_first, keep_last, sel_blocks, (unsigned long long*)workspace};
   return launch_block_select(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
 }
 
