@@ -57,7 +57,7 @@ struct SelectArgs {
   int B, Hq, H, D;
   int keep, first, last;
   int32_t* sel;    // [B, H, keep]
-  unsigned long long* keys;  // [B, H, max_blocks] scratch
+  unsigned long long* scratch;  // [B, H, max_blocks]
 };
 hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream);
 

@@ -236,14 +236,16 @@ SELECT = [
     ([3000, 17, 2900], 3, 3, 64, 1, 64, 3, 5),
     ([640] * 9, 8, 8, 128, 32, 20, 1, 1),       # keep == blocks
     ([640] * 9, 20, 4, 128, 32, 33, 1, 1),      # keep > blocks
-    ([-5, 100000, 48], 6, 2, 64, 16, 6, 1, 1),  # lengths out of range
+    ([40000, 100], 4, 1, 64, 2, 1500, 2, 2),    # more blocks and candidates than are held at once
+    ([17000], 2, 1, 128, 1, 90, 20, 70),        # only the forced ones
+    ([-5, 10 ** 6, 48], 6, 2, 64, 16, 6, 1, 1),  # lengths out of range
 ]
 
 
 @pytest.mark.parametrize("lens,Hq,H,D,bs,keep,first,last", SELECT)
 def test_select(lens, Hq, H, D, bs, keep, first, last):
     rng = np.random.default_rng(len(lens) + D + keep)
-    mb = max(1, min(max(R.ceil_div(n, bs) for n in lens), 2600)) + 3
+    mb = max(1, min(max(R.ceil_div(n, bs) for n in lens), 20000)) + 3
     nb = sum(min(R.ceil_div(max(n, 0), bs), mb) for n in lens) + 2
     table = make_table(rng, lens, bs, nb, mb)
     q = torch.from_numpy(rng.standard_normal((len(lens), Hq, D), dtype=np.float32)).to(torch.bfloat16)
@@ -275,6 +277,23 @@ def test_select_extreme_values():
     check_select(q, kb, bs, table, lens, 40, 1, 1, "extremes")
     q[:, :, 4] = 0  # 0 * inf
     check_select(q, kb, bs, table, lens, 40, 1, 1, "zero times infinity")
+
+
+def test_select_near_ties():
+    """Scores of hundreds that differ in their 30th to 45th bit: the choice is
+    that of the 64-bit sums."""
+    rng = np.random.default_rng(9)
+    for lens, H, D, keep in [([20000, 700], 2, 128, 50), ([9000], 1, 64, 300), ([5000], 4, 256, 7)]:
+        bs = 8
+        mb = max(R.ceil_div(n, bs) for n in lens)
+        nb = sum(R.ceil_div(n, bs) for n in lens) + 1
+        table = make_table(rng, lens, bs, nb, mb)
+        q = torch.from_numpy(rng.standard_normal((len(lens), 2 * H, D), dtype=np.float32)).to(torch.bfloat16)
+        q[:, :, 7] = 2.0 ** -20
+        row = np.sort(rng.standard_normal((1, H, 2, D), dtype=np.float32) * 4, axis=2)
+        kb = torch.from_numpy(np.repeat(row, nb, axis=0)).to(torch.bfloat16)
+        kb[:, :, :, 7] = torch.from_numpy(rng.integers(1, 200, (nb, 1, 1)) * 2.0 ** -8).to(torch.bfloat16)
+        check_select(q, kb, bs, table, lens, keep, 1, 1, f"near ties {lens}")
 
 
 # ---- attention ------------------------------------------------------------------
