@@ -113,14 +113,6 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   return s;
 }
 
-// Direct-to-LDS loads of 16 and 4 bytes a lane, to consecutive places.
-__device__ __forceinline__ void stream_to_lds(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, kLdsLoadNonTemporal);
-}
-__device__ __forceinline__ void word_to_lds(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 4, 0, 0);
-}
-
 // Four transposing LDS reads of 8 bytes a lane (16 lanes hand out 16 columns of
 // the 128 bytes that they address) and the wait for them, in one block: as
 // builtins, each read would first wait for every direct load in flight (the
@@ -142,24 +134,6 @@ __device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (
         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
         : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
         : "memory");
-}
-
-// A use of x: the load behind it is waited for here and not later.
-template <class X>
-__device__ __forceinline__ void loaded(X& x) {
-  asm volatile("" : "+v"(x));
-}
-
-// Waits until at most `left` <= kMost groups of kOps vector-memory operations
-// are outstanding, and for LDS.
-template <int kMost, int kOps>
-__device__ __forceinline__ void wait_groups(int left) {
-  if constexpr (kMost == 0) {
-    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
-  } else {
-    if (left == kMost) __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kMost * kOps));
-    else wait_groups<kMost - 1, kOps>(left);
-  }
 }
 
 }  // namespace
@@ -206,7 +180,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       sp = span_of(a, ++b);
       n = tiles_of(sp);
     }
-    const int row = (int)((pos - at) / n);
+    const int row = (int)floor_div(pos - at, n);
     const int t0 = (int)(pos - at - (long long)row * n);
     const int t1 = (int)min((long long)n, t0 + (line.end - pos));
     pos += t1 - t0;
@@ -257,7 +231,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       ok = ok && page >= 0 && page < a.num_blocks;
       const uint32_t mask = (uint32_t)__ballot(ok) & (uint32_t)((1ull << T::kKeys) - 1);
       const int slot = ok ? page * a.block_size + r : 0;
-      char* stage = ring + (x % S) * 2 * T::kSide;
+      char* stage = ring + (x & (S - 1)) * 2 * T::kSide;
 #pragma unroll
       for (int i = 0; i < T::kLoads; ++i) {
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
@@ -267,8 +241,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         stream_to_lds((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
                       stage + T::kSide + i * 1024);
       }
-      word_to_lds(table_address(block_of(x + S, next_list)), pages + (x % S) * 64);
-      if constexpr (kList) word_to_lds(list_address(x + 2 * S), listed + (x % S) * 64);
+      word_to_lds(table_address(block_of(x + S, next_list)), pages + (x & (S - 1)) * 64);
+      if constexpr (kList) word_to_lds(list_address(x + 2 * S), listed + (x & (S - 1)) * 64);
       return mask;
     };
 
@@ -284,46 +258,39 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
     const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
     const float qs = a.scale * ks * 1.44269504088896340736f;  // logits in powers of two
 
-    uint32_t masks[S];  // of the tiles in the ring
-    int ahead[S];       // list entries of the S tiles after them
+    uint32_t masks[S] = {};  // of the tiles in the ring
+    int ahead[S] = {};       // list entries of the tiles that come into it next
     // The last segment's LDS reads are done before the ring is filled again.
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
     asm volatile("" ::: "memory");
-    {
-      int lst[2 * S], pg[S];
+    if constexpr (kList) {
 #pragma unroll
-      for (int i = 0; i < 2 * S; ++i) lst[i] = kList ? *list_address(i) : 0;
-#pragma unroll
-      for (int i = 0; i < S; ++i) pg[i] = *table_address(block_of(i, lst[i]));
-      // All of them here, so that no wait for one comes between the loads below.
-#pragma unroll
-      for (int i = 0; i < S; ++i) loaded(pg[i]), loaded(lst[S + i]);
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) loaded(qf[u].u);
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        masks[i] = 0;
-        if (i < nt) masks[i] = issue(i, pg[i], lst[i], lst[S + i]);
-      }
-#pragma unroll
-      for (int i = 0; i < S; ++i) ahead[i] = lst[S + i];
+      for (int i = 0; i < S; ++i) ahead[i] = *list_address(i);
     }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      word_to_lds(table_address(block_of(i, ahead[i])), pages + i * 64);
+      if constexpr (kList) word_to_lds(list_address(S + i), listed + i * 64);
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+    asm volatile("" ::: "memory");
 
     f32x4 o[kCols];
 #pragma unroll
     for (int c = 0; c < kCols; ++c) o[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -__builtin_huge_valf(), l = 0.f;
 
-    for (int x = 0; x < nt; ++x) {
-      // Tile x and the fetches issued with it have landed.
-      wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
-      asm volatile("" ::: "memory");
-      char* stage = ring + (x % S) * 2 * T::kSide;
+    // The S turns before tile 0 only fill the ring.
+    for (int x = -S; x < nt; ++x) {
       const uint32_t mask = masks[0];
 #pragma unroll
       for (int i = 0; i + 1 < S; ++i) masks[i] = masks[i + 1];
+      // Tile x and the fetches issued with it have landed.
+      if (x >= 0) wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
+      asm volatile("" ::: "memory");
+      char* stage = ring + (x & (S - 1)) * 2 * T::kSide;
       constexpr uint32_t kAll = (uint32_t)((1ull << T::kKeys) - 1);
-      if (mask != 0) {
+      if (x >= 0 && mask != 0) {
         if (mask != kAll) {
           // Values that take no part become zeros: their weight is zero, but
           // what lies there may be infinite or NaN.
@@ -436,8 +403,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       if (x + S < nt) {
         // Tile x + S takes this tile's place; the block numbers of it (and
         // the list entries of tile x + 2 S) came with tile x.
-        const int page = pages[(x % S) * 64 + lane];
-        const int nxt = kList ? listed[(x % S) * 64 + lane] : 0;
+        const int page = pages[(x & (S - 1)) * 64 + lane];
+        const int nxt = kList ? listed[(x & (S - 1)) * 64 + lane] : 0;
         const int cur = ahead[0];
 #pragma unroll
         for (int i = 0; i + 1 < S; ++i) ahead[i] = ahead[i + 1];
@@ -514,7 +481,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 // writes the rows of requests without keys.  Workgroup (query head, request).
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int heads,
                                                              int tile_keys) {
-  __shared__ float s_o[256 * 4], s_m[4], s_l[4];
+  __shared__ __attribute__((aligned(16))) float s_o[256 * 4];
+  __shared__ float s_e[256], s_m[4], s_l[4];
   const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, D = a.D;
   const size_t out_row = (size_t)b * a.Hq + hq;
   const int n = ceil_div(span_of(a, b).keys, tile_keys);
@@ -525,46 +493,65 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   }
   const int G = a.Hq / a.H, h = hq / G, gi = hq - h * G;
   const int qtiles = ceil_div(G, 16), cap = min(G, 16);
-  // Quotients of whole numbers below 2^52, exact when floored.
-  const double stretch = (double)parts.prefix[a.B];
+  const long long stretch = parts.prefix[a.B];
   const long long first = parts.prefix[b] + (long long)(h / heads * qtiles + gi / 16) * n;
-  const int w0 = (int)((double)first / stretch), w1 = (int)((double)(first + n - 1) / stretch);
+  const int w0 = (int)floor_div(first, stretch), w1 = (int)floor_div(first + n - 1, stretch);
   if (w0 == w1) return;
-  auto part_of = [&](int w) {
-    return ((size_t)(w * 2 + (w == w0 ? 1 : 0)) * heads + h % heads) * cap + gi % 16;
+  const int np = w1 - w0 + 1;  // at most kGrid = 256, one a thread
+  auto part_of = [&](int i) {
+    return ((size_t)((w0 + i) * 2 + (i == 0 ? 1 : 0)) * heads + h % heads) * cap + gi % 16;
   };
-  // The largest maximum, then sums over the parts, in a fixed order.
-  float m = -__builtin_huge_valf();
-  for (int w = w0 + tid; w <= w1; w += 256) m = fmaxf(m, parts.ml[2 * part_of(w)]);
-  for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-  if ((tid & 63) == 0) s_m[tid >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
-  float l = 0.f;
-  for (int w = w0 + tid; w <= w1; w += 256) {
-    const size_t p = part_of(w);
-    l += parts.ml[2 * p + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
+  // Everything is asked for before the first wait: the thread's part's maximum
+  // and sum, and its first pieces of the outputs.
+  float m = -__builtin_huge_valf(), l = 0.f;
+  if (tid < np) {
+    const float2 v = *reinterpret_cast<const float2*>(parts.ml + 2 * part_of(tid));
+    m = v.x;
+    l = v.y;
   }
-  for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x);
-  if ((tid & 63) == 0) s_l[tid >> 6] = l;
+  constexpr int kBatch = 8;
   const int lanes = D / 4, sub = tid / lanes, subs = 256 / lanes, c = tid % lanes;
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int w = w0 + sub; w <= w1; w += subs) {
-    const size_t p = part_of(w);
-    const float e = __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
-    const f32x4 x = *reinterpret_cast<const f32x4*>(parts.o + p * D + 4 * c);
+  f32x4 x[kBatch];
+  auto load = [&](int i0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] += x[i] * e;
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * subs;
+      if (i < np) x[k] = *reinterpret_cast<const f32x4*>(parts.o + part_of(i) * D + 4 * c);
+    }
+  };
+  load(sub);
+  float M = wave_reduce(m, [](float p, float q) { return fmaxf(p, q); });
+  if ((tid & 63) == 0) s_m[tid >> 6] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float safe = M == -__builtin_huge_valf() ? 0.f : M;
+  const float e = __builtin_amdgcn_exp2f(m - safe);
+  s_e[tid] = e;
+  // Sums in a fixed order: over the lanes, then the waves.
+  const float ls = wave_sum(l * e);
+  if ((tid & 63) == 0) s_l[tid >> 6] = ls;
+  __syncthreads();
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i0 = sub; i0 < np; i0 += kBatch * subs) {
+    if (i0 != sub) load(i0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * subs;
+      if (i < np) {
+        const float f = s_e[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += x[k][j] * f;
+      }
+    }
   }
   *reinterpret_cast<f32x4*>(s_o + tid * 4) = o;
   __syncthreads();
   if (tid < D) {
     l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    float x = 0.f;
-    for (int s = 0; s < subs; ++s) x += s_o[s * D + tid];
+    float sum = 0.f;
+    for (int s = 0; s < subs; ++s) sum += s_o[s * D + tid];
     const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
-    a.out[out_row * D + tid] = (__bf16)(l == 0.f ? 0.f : x * (vs / l));
+    a.out[out_row * D + tid] = (__bf16)(l == 0.f ? 0.f : sum * (vs / l));
     if (tid == 0 && a.lse != nullptr)
       a.lse[out_row] = l == 0.f ? -__builtin_huge_valf()
                                 : (safe + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;

@@ -21,21 +21,24 @@
 // attention.hip.
 //
 // The second kernel finds, per request and key head, the keep-th largest lower
-// end, takes the blocks whose upper end reaches it -- a few more than `keep`
-// -- and computes only those in 64 bits, unless there are exactly as many as
-// wanted.  A histogram over 2048 equal parts of the ends' range narrows the
-// search to one part, and again, until the part's blocks are all wanted or are
-// equal.
+// end.  A block whose upper end stays below it is out, one whose lower end is
+// above every upper end that may still come in from below is in, and the few
+// between are computed in 64 bits.  A histogram over 2048 equal parts of the
+// ends' range narrows the search to one part, and again, until the part's
+// blocks are all wanted or are equal.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
+#include "kernels.h"
 #include "paged.h"
 
 namespace mova {
 
 namespace {
 
-constexpr int kScoreGrid = 1024;  // 4 workgroups a CU
+constexpr int kScoreGrid = 256;      // one workgroup a CU
+constexpr int kRingBytes = 32768;    // bounds in LDS per wave
 constexpr int kTileBlocks = 16;
 
 // Bound on the error of a 32-bit sum s of products with absolute sum t, in any
@@ -45,17 +48,17 @@ constexpr int kTileBlocks = 16;
 constexpr float kErrorRel = 1.f / 4096;
 constexpr float kErrorAbs = 7.5e-37f;  // 2^-120
 
-// [lower, upper] of a block's score.  Missing blocks: upper = -infinity;
-// blocks that are always in: lower = +infinity; a score that 32 bits cannot
-// enclose: (-infinity, +infinity).
-struct Interval {
-  float lower, upper;
-};
-
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
+
+// The order keys of the ends of a block's score, neither of them 0 or ~0; a
+// score that 32 bits cannot enclose has those of -infinity and +infinity.
+// Missing blocks: {0, 0}; blocks that are always in: {~0, ~0}.
+struct Ends {
+  uint32_t lower, upper;
+};
 
 constexpr unsigned long long kMissing = 0ull;  // below every score's key
 constexpr unsigned long long kForced = ~0ull;  // above every score's key
@@ -90,11 +93,28 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
 
 // kHeads: key heads of a workgroup; 4 / kHeads waves share a head's tiles.
 // MFMA rows are blocks, columns query heads (those past the group are left
-// out of the maxima).
+// out of the maxima).  Each wave reads through a ring of tiles in LDS, as in
+// attention.hip: with the fragments read straight into registers, one tile
+// ahead or none, the kernel took 40 and 35 us where this takes 
+template <int D>
+struct BoundsTile {
+  static constexpr int kRow = 4 * D;  // bytes of a block's bounds, lo then hi
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kRowsPerLoad = 64 / kChunks;
+  static constexpr int kBytes = kTileBlocks * kRow;
+  static constexpr int kLoads = kTileBlocks / kRowsPerLoad;
+  static constexpr int kStages = kRingBytes / kBytes;
+  static constexpr int kLds = kRingBytes + kStages * 256;
+};
+
 template <int D, int kHeads>
 __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
+  using T = BoundsTile<D>;
   constexpr int kStripes = 4 / kHeads;
   constexpr int kSteps = D / 32;
+  constexpr int S = T::kStages;
+  constexpr int kGroupLoads = T::kLoads + 1;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ LineShared s_line;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -108,6 +128,8 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
                   nullptr, &line))
     return;
 
+  char* ring = lds + wave * T::kLds;
+  int* fetched = (int*)(ring + kRingBytes);
   int b = line.b;
   long long at = line.first;
   int n = blocks_of(a, b), tiles = tiles_of(n);
@@ -117,13 +139,13 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
       n = blocks_of(a, ++b);
       tiles = tiles_of(n);
     }
-    const int hgroup = (int)((pos - at) / tiles);
+    const int hgroup = (int)floor_div(pos - at, tiles);
     const int t0 = (int)(pos - at - (long long)hgroup * tiles);
     const int t1 = (int)min((long long)tiles, t0 + (line.end - pos));
     pos += t1 - t0;
     const int h = hgroup * kHeads + hsub;
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
-    Interval* out = (Interval*)a.scratch + ((size_t)b * a.H + h) * a.max_blocks;
+    Ends* out = (Ends*)a.scratch + ((size_t)b * a.H + h) * select_stride(a.max_blocks);
 
     // q+ and |q-| of query head g0 + r16 as MFMA columns.
     Frag16 qp[kSteps], qn[kSteps];
@@ -143,38 +165,61 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
       }
     };
     load_q(0);
-    auto page_of = [&](int x) {
-      const int j = (x * kStripes + stripe) * kTileBlocks + r16;
-      const int p = x < t1 && j < n ? table[j] : -1;
-      return p < a.num_blocks ? p : -1;
-    };
-    int next = page_of(t0);
-    for (int x = t0; x < t1; ++x) {
-      const int page = next;
-      next = page_of(x + 1);
-      const __bf16* src = a.bounds + ((size_t)max(page, 0) * a.H + h) * 2 * D + 8 * g4;
-      Frag16 lo[kSteps], hi[kSteps];
+    // Table entry of the lane's block of tile x (a lane a block).
+    const int nt = t1 - t0;
+    auto block_at = [&](int x) { return ((t0 + x) * kStripes + stripe) * kTileBlocks + r16; };
+    auto address = [&](int x) { return table + min(block_at(x), a.max_blocks - 1); };
+    // Issues the loads of tile x and the fetch of the table entries of tile
+    // x + S; returns the lane's block number, -1 where there is none.
+    auto issue = [&](int x, int page) {
+      if (block_at(x) >= n || page < 0 || page >= a.num_blocks) page = -1;
+      const int row = max(page, 0);
+      char* stage = ring + (x & (S - 1)) * T::kBytes;
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        lo[u].u = load16_stream(src + 32 * u);
-        hi[u].u = load16_stream(src + D + 32 * u);
+      for (int i = 0; i < T::kLoads; ++i) {
+        const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
+        const int c = (lane % T::kChunks) ^ rr;
+        stream_to_lds((const char*)a.bounds +
+                          ((size_t)(uint32_t)__shfl(row, rr) * a.H + h) * T::kRow + c * 16,
+                      stage + i * 1024);
       }
-      Interval best[4];
+      word_to_lds(address(x + S), fetched + (x & (S - 1)) * 64);
+      return page;
+    };
+    int pages[S] = {};  // of the tiles in the ring, the lane's block of each
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+    asm volatile("" ::: "memory");
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) word_to_lds(address(i), fetched + i * 64);
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+    asm volatile("" ::: "memory");
+    for (int x = -S; x < nt; ++x) {
+      const int page = pages[0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) best[i] = {-__builtin_huge_valf(), -__builtin_huge_valf()};
+      for (int i = 0; i + 1 < S; ++i) pages[i] = pages[i + 1];
+      if (x >= 0) {
+      wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
+      asm volatile("" ::: "memory");
+      const char* stage = ring + (x & (S - 1)) * T::kBytes;
+      float lowest[4], highest[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lowest[i] = highest[i] = -__builtin_huge_valf();
       for (int g0 = 0; g0 < G; g0 += 16) {
         if (G > 16) load_q(g0);
         f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, t = s;
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-          Frag16 x0, x1;
-          s = mfma16x16x32(hi[u].h, qp[u].h, s);
-          x0.u = lo[u].u ^ 0x80008000u;
-          s = mfma16x16x32(x0.h, qn[u].h, s);
-          x0.u = hi[u].u & 0x7fff7fffu;
-          x1.u = lo[u].u & 0x7fff7fffu;
-          t = mfma16x16x32(x0.h, qp[u].h, t);
-          t = mfma16x16x32(x1.h, qn[u].h, t);
+          Frag16 lo, hi, f;
+          lo.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow + ((4 * u + g4) ^ r16) * 16);
+          hi.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow +
+                                                 ((T::kChunks / 2 + 4 * u + g4) ^ r16) * 16);
+          s = mfma16x16x32(hi.h, qp[u].h, s);
+          f.u = lo.u ^ 0x80008000u;
+          s = mfma16x16x32(f.h, qn[u].h, s);
+          f.u = hi.u & 0x7fff7fffu;
+          t = mfma16x16x32(f.h, qp[u].h, t);
+          f.u = lo.u & 0x7fff7fffu;
+          t = mfma16x16x32(f.h, qn[u].h, t);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -183,23 +228,30 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
           float lower = enclosed ? s[i] - e : -__builtin_huge_valf();
           float upper = enclosed ? s[i] + e : __builtin_huge_valf();
           if (g0 + r16 >= G) lower = upper = -__builtin_huge_valf();
-          best[i].lower = fmaxf(best[i].lower, lower);
-          best[i].upper = fmaxf(best[i].upper, upper);
+          lowest[i] = fmaxf(lowest[i], lower);
+          highest[i] = fmaxf(highest[i], upper);
         }
       }
-      Interval mine = {0.f, 0.f};
+      Ends mine = {0u, 0u};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Interval v = {max16(best[i].lower), max16(best[i].upper)};
+        const Ends v = {order_key(max16(lowest[i])), order_key(max16(highest[i]))};
         if (r16 == i) mine = v;
       }
       const int i = 4 * g4 + (r16 & 3);
-      const int j = (x * kStripes + stripe) * kTileBlocks + i;
+      const int j = ((t0 + x) * kStripes + stripe) * kTileBlocks + i;
       const int p = __shfl(page, i);
       if (r16 < 4 && j < n) {
-        if (p < 0) mine = {-__builtin_huge_valf(), -__builtin_huge_valf()};
-        else if (j < a.first || j >= n - a.last) mine = {__builtin_huge_valf(), __builtin_huge_valf()};
+        if (p < 0) mine = {0u, 0u};
+        else if (j < a.first || j >= n - a.last) mine = {~0u, ~0u};
         out[j] = mine;
+      }
+      }
+      if (x + S < nt) {
+        const int entry = fetched[(x & (S - 1)) * 64 + lane];
+        __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(63));
+        asm volatile("" ::: "memory");
+        pages[S - 1] = issue(x + S, entry);
       }
     }
   }
@@ -207,86 +259,69 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
 
 namespace {
 
-constexpr int kTopThreads = 1024;
-constexpr int kTopWaves = kTopThreads / 64;
-constexpr int kParts = 2048;
-constexpr int kHeld = 16;              // intervals a thread holds at a time
-constexpr int kMaxCandidates = 1024;   // computed in LDS; beyond, in memory
+constexpr int kParts = 2048;          // of a histogram
+constexpr int kMaxHeld = 14336;       // blocks whose ends LDS holds, a multiple of 4
+constexpr int kMaxOpen = 1024;        // undecided blocks computed in LDS
+constexpr int kMaxMarked = 65536;     // blocks with a mark in LDS
 
+template <int kWaves>
 struct TopShared {
-  int hist[kParts];
-  unsigned long long key[kMaxCandidates];
-  int block[kMaxCandidates];
-  int count[kHeld][kTopWaves];
-  unsigned long long lo[kTopWaves], hi[kTopWaves];
-  int n[kTopWaves], f[kTopWaves];
-  int part, above, in;
+  int hist[2][kParts];
+  uint32_t chosen[kMaxMarked / 32];
+  unsigned long long key[kMaxOpen];
+  int block[kMaxOpen];
+  unsigned long long lo[kWaves], hi[kWaves];
+  int n[kWaves], f[kWaves];
+  int part, above, in, open;
 };
-
-template <class K>
-__device__ __forceinline__ K wave_min(K x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = min(x, (K)__shfl_xor((long long)x, o));
-  return x;
-}
-template <class K>
-__device__ __forceinline__ K wave_max(K x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = max(x, (K)__shfl_xor((long long)x, o));
-  return x;
-}
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
 
 // Narrows [lo, hi] around the left-th largest of the keys in it, which
 // for_each(f) hands to f one after the other.  Returns the cut: keys from it
-// on are wanted, and of those equal to it the first *ties.
-template <class K, class ForEach>
-__device__ K narrow(TopShared& sh, K lo, K hi, int left, ForEach for_each, int* ties) {
+// on are wanted, and of those equal to it the first *ties.  Both histograms
+// are clear on entry.
+template <class K, int kWaves, class ForEach>
+__device__ K narrow(TopShared<kWaves>& sh, K lo, K hi, int left, ForEach for_each, int* ties) {
+  constexpr int kThreads = 64 * kWaves, kPer = kParts / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (;;) {
+  for (int round = 0;; ++round) {
     const unsigned long long span = (unsigned long long)(hi - lo);
     const int bits = span == 0 ? 0 : 64 - __clzll((long long)span);
     const int shift = max(bits - 11, 0);
-    sh.hist[tid] = 0;
-    sh.hist[tid + kTopThreads] = 0;
-    __syncthreads();
+    int* hist = sh.hist[round & 1];
     for_each([&](K k) {
-      if (k >= lo && k <= hi) atomicAdd(&sh.hist[(int)((k - lo) >> shift)], 1);
+      if (k >= lo && k <= hi) atomicAdd(&hist[(int)((k - lo) >> shift)], 1);
     });
     __syncthreads();
-    // Counts from the top: each thread two parts, then over the waves.
-    const int p1 = kParts - 1 - 2 * tid, p0 = p1 - 1;
-    const int c1 = sh.hist[p1], c0 = sh.hist[p0];
-    int inc = c1 + c0;
+    // Counts from the top: each thread kPer parts, then over the waves.
+    const int top = kParts - 1 - kPer * tid;
+    int c[kPer], mine = 0;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(inc, o);
-      if (lane >= o) inc += up;
+    for (int i = 0; i < kPer; ++i) {
+      c[i] = hist[top - i];
+      hist[top - i] = 0;  // for the round after next
+      mine += c[i];
     }
+    const int inc = wave_scan(mine);
     if (lane == 63) sh.n[wave] = inc;
     __syncthreads();
-    int above = inc - c1 - c0;
+    int above = inc - mine;
 #pragma unroll
-    for (int w = 0; w < kTopWaves; ++w)
+    for (int w = 0; w < kWaves; ++w)
       if (w < wave) above += sh.n[w];
-    if (above < left && left <= above + c1) {
-      sh.part = p1;
-      sh.above = above;
-      sh.in = c1;
-    } else if (above + c1 < left && left <= above + c1 + c0) {
-      sh.part = p0;
-      sh.above = above + c1;
-      sh.in = c0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (above < left && left <= above + c[i]) {
+        sh.part = top - i;
+        sh.above = above;
+        sh.in = c[i];
+      }
+      above += c[i];
     }
     __syncthreads();
     left -= sh.above;
     lo += (K)((K)sh.part << shift);
     if (shift == 0 || sh.in == left) {
-      *ties = shift == 0 ? left : 0x7fffffff;
+      *ties = sh.in == left ? 0x7fffffff : left;
       return lo;
     }
     hi = min(hi, (K)(lo + (K)(((K)1 << shift) - 1)));
@@ -311,8 +346,10 @@ __device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int h,
         s += (double)(x > 0 ? (float)hv[i] : (float)lv[i]) * x;
       }
     }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    s += dpp_or_0<0xB1>(s);   // quad_perm 1 0 3 2, 2 3 0 1, row_half_mirror, row_mirror
+    s += dpp_or_0<0x4E>(s);
+    s += dpp_or_0<0x141>(s);
+    s += dpp_or_0<0x140>(s);
     if (s > best) best = s;  // a NaN does not count
   }
   return best;
@@ -321,53 +358,72 @@ __device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int h,
 }  // namespace
 
 // Workgroup (h, b): the `keep` blocks with the highest scores, the lower index
-// first among equals, in index order.
-__global__ __launch_bounds__(kTopThreads) void select_top_kernel(SelectArgs a) {
-  __shared__ TopShared sh;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// first among equals, in index order.  A pass over 12,500 blocks is bound by
+// the instructions of its one CU, hence ready-made keys, four to a read.
+template <int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, int held) {
+  constexpr int kThreads = 64 * kWaves;
+  __shared__ TopShared<kWaves> sh;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  uint32_t *kept_lower = (uint32_t*)lds, *kept_upper = kept_lower + held;  // of the first blocks
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.x, b = blockIdx.y;
   const int n = blocks_of(a, b);
   const int32_t* table = a.table + (size_t)b * a.max_blocks;
-  unsigned long long* scratch = a.scratch + ((size_t)b * a.H + h) * a.max_blocks;
-  const Interval* ends = (const Interval*)scratch;
+  unsigned long long* scratch = a.scratch + ((size_t)b * a.H + h) * select_stride(a.max_blocks);
+  const Ends* ends = (const Ends*)scratch;
   int32_t* sel = a.sel + ((size_t)b * a.H + h) * a.keep;
-  const float inf = __builtin_huge_valf();
+  const uint64_t below = (1ull << lane) - 1;
 
-  // A thread holds kHeld intervals, of blocks base + i * kTopThreads + tid;
-  // lists that need more are read again in each pass.
-  Interval iv[kHeld];
-  auto hold = [&](int base) {
+  for (int i = tid; i < 2 * kParts; i += kThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) sh.open = 0;
+  auto umin = [](uint32_t x, uint32_t y) { return min(x, y); };
+  auto umax = [](uint32_t x, uint32_t y) { return max(x, y); };
+
+  // Four blocks from j on (a multiple of 4); zeros behind the last.
+  auto fetch4 = [&](int j, u32x4* l, u32x4* u) {
+    const u32x4 e0 = load16(ends + j), e1 = load16(ends + j + 2);
+    *l = u32x4{e0[0], e0[2], e1[0], e1[2]};
+    *u = u32x4{e0[1], e0[3], e1[1], e1[3]};
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int j = base + i * kTopThreads + tid;
-      iv[i] = j < n ? ends[j] : Interval{-inf, -inf};
-    }
+    for (int i = 0; i < 4; ++i)
+      if (j + i >= n) (*l)[i] = (*u)[i] = 0;
   };
-  auto for_each = [&](auto f) {
-    for (int base = 0; base < n; base += kHeld * kTopThreads) {
-      if (n > kHeld * kTopThreads) hold(base);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (base + i * kTopThreads < n) f(iv[i]);
-    }
+  auto lower4 = [&](int j) {
+    u32x4 l, u;
+    if (j < held) l = *(const u32x4*)(kept_lower + j);
+    else fetch4(j, &l, &u);
+    return l;
   };
-  hold(0);
-  auto regular = [&](const Interval& v) { return v.upper > -inf && v.lower < inf; };
+  auto upper4 = [&](int j) {
+    u32x4 l, u;
+    if (j < held) u = *(const u32x4*)(kept_upper + j);
+    else fetch4(j, &l, &u);
+    return u;
+  };
 
   uint32_t lo = ~0u, hi = 0;
   int there = 0, forced = 0;
-  for_each([&](const Interval& v) {
-    there += v.upper > -inf;
-    forced += v.lower == inf;
-    if (regular(v)) {
-      lo = min(lo, order_key(v.lower));
-      hi = max(hi, order_key(v.lower));
+  for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+    u32x4 l, u;
+    fetch4(j, &l, &u);
+    if (j < held) {
+      *(u32x4*)(kept_lower + j) = l;
+      *(u32x4*)(kept_upper + j) = u;
     }
-  });
-  lo = wave_min(lo);
-  hi = wave_max(hi);
-  there = wave_sum(there);
-  forced = wave_sum(forced);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      there += l[i] != 0;
+      forced += l[i] == ~0u;
+      lo = min(lo, l[i] - 1);      // 0 counts as the highest
+      hi = max(hi, l[i] + 1);      // ~0 counts as the lowest
+    }
+  }
+  lo = wave_reduce(lo, umin);
+  hi = wave_reduce(hi, umax);
+  there = read_lane(wave_scan(there), 63);
+  forced = read_lane(wave_scan(forced), 63);
   if (lane == 0) {
     sh.lo[wave] = lo;
     sh.hi[wave] = hi;
@@ -377,225 +433,243 @@ __global__ __launch_bounds__(kTopThreads) void select_top_kernel(SelectArgs a) {
   __syncthreads();
   there = forced = 0;
 #pragma unroll
-  for (int w = 0; w < kTopWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     lo = min(lo, (uint32_t)sh.lo[w]);
     hi = max(hi, (uint32_t)sh.hi[w]);
     there += sh.n[w];
     forced += sh.f[w];
   }
-  __syncthreads();
 
-  // Blocks whose score may be among the wanted: all, none (the forced ones
-  // fill the list), or those that reach the left-th largest lower end.
+  lo += 1;
+  hi -= 1;
+
+  // `reach`: lower ends from it on are the highest ones.  The blocks that may
+  // be wanted reach it with their upper end; those among them that do not with
+  // their lower one reach up to `rival`, and blocks that lie above that, from
+  // `sure` on, are in.  The others are undecided.
   const int left = min(a.keep, there) - forced;
-  uint32_t reach = 0;
+  uint32_t sure = 1, reach = 0, rival = 0;
   if (left <= 0) {
-    reach = ~0u;
+    sure = ~0u;  // the forced blocks fill the list
   } else if (there > a.keep) {
     int ties;
-    reach = narrow(sh, lo, hi, left, [&](auto f) {
-      for_each([&](const Interval& v) { if (regular(v)) f(order_key(v.lower)); });
-    }, &ties);
-  }
-  auto candidate = [&](const Interval& v) { return regular(v) && order_key(v.upper) >= reach; };
-  int candidates = 0;
-  for_each([&](const Interval& v) { candidates += candidate(v); });
-  candidates = wave_sum(candidates);
-  if (lane == 0) sh.f[wave] = candidates;
-  __syncthreads();
-  candidates = 0;
-#pragma unroll
-  for (int w = 0; w < kTopWaves; ++w) candidates += sh.f[w];
-
-  const uint64_t below = (1ull << lane) - 1;
-  // Calls put(i, rank) for the held intervals that `is` picks, ranked in index
-  // order from `from` on; returns the next rank.
-  auto ranked = [&](auto is, int from, auto put) {
     __syncthreads();
+    reach = narrow<uint32_t>(sh, lo, hi, left, [&](auto f) {
+#pragma unroll 1
+      for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+        const u32x4 l = lower4(j);
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const uint64_t m = __ballot(is(iv[i]));
-      if (lane == 0) sh.count[i][wave] = __popcll(m);
-    }
-    __syncthreads();
-    // The 256 counts lie in index order; the first wave adds them up.
-    if (wave == 0) {
-      int* c = &sh.count[0][0] + 4 * lane;
-      const int c0 = c[0], c1 = c[1], c2 = c[2], c3 = c[3];
-      int inc = c0 + c1 + c2 + c3;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(inc, o);
-        if (lane >= o) inc += up;
+        for (int i = 0; i < 4; ++i) f(l[i]);
       }
-      if (lane == 63) sh.n[0] = inc;
-      inc -= c1 + c2 + c3 + c0;
-      c[0] = inc;
-      c[1] = inc + c0;
-      c[2] = inc + c0 + c1;
-      c[3] = inc + c0 + c1 + c2;
+    }, &ties);
+#pragma unroll 1
+    for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+      const u32x4 l = lower4(j), u = upper4(j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (l[i] < reach) rival = max(rival, u[i]);
     }
+    rival = wave_reduce(rival, umax);
+    if (lane == 0) sh.f[wave] = (int)rival;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const bool yes = is(iv[i]);
-      const uint64_t m = __ballot(yes);
-      if (yes) put(i, from + sh.count[i][wave] + __popcll(m & below));
-    }
-    return from + sh.n[0];
-  };
-
-  if (candidates == max(left, 0)) {
-    // Everything that may be wanted is.
-    int out = 0;
-    for (int base = 0; base < n; base += kHeld * kTopThreads) {
-      if (n > kHeld * kTopThreads) hold(base);
-      out = ranked([&](const Interval& v) { return v.lower == inf || candidate(v); }, out,
-                   [&](int i, int r) { sel[r] = base + i * kTopThreads + tid; });
-    }
-    for (int i = out + tid; i < a.keep; i += kTopThreads) sel[i] = -1;
-    return;
+    for (int w = 0; w < kWaves; ++w) rival = max(rival, (uint32_t)sh.f[w]);
+    if (rival < reach) rival = 0;                  // none
+    if (ties != 0x7fffffff) rival = ~0u - 1;       // equal lower ends at the cut
+    sure = max(reach, rival + 1);
   }
-  if (candidates <= kMaxCandidates) {
-    // Listed in LDS, computed by 16 lanes each, and chosen by counting the
-    // better ones.  Forced blocks are the first and last ones.
-    int listed = 0, early = 0;
-    for (int base = 0; base < n; base += kHeld * kTopThreads) {
-      if (n > kHeld * kTopThreads) hold(base);
-      listed = ranked(candidate, listed,
-                      [&](int i, int r) { sh.block[r] = base + i * kTopThreads + tid; });
-    }
-    for (int j = tid; j < min(a.first, n); j += kTopThreads) early += ends[j].lower == inf;
-    early = wave_sum(early);
-    if (lane == 0) sh.n[wave] = early;
-    __syncthreads();
-    early = 0;
+  auto open = [&](uint32_t l, uint32_t u) { return u >= reach && l <= rival; };
+
+  if (rival != 0) {
+    // Undecided blocks: listed in LDS, computed by 16 lanes each, and chosen by
+    // counting the better ones.
+    int in = 0;
+    for (int i = tid; i < min(ceil_div(n, 32), kMaxMarked / 32); i += kThreads) sh.chosen[i] = 0;
+#pragma unroll 1
+    for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+      const u32x4 l = lower4(j), u = upper4(j);
 #pragma unroll
-    for (int w = 0; w < kTopWaves; ++w) early += sh.n[w];
-    for (int c = tid / 16; c < candidates; c += kTopThreads / 16) {
+      for (int i = 0; i < 4; ++i) {
+        in += l[i] >= sure;
+        if (open(l[i], u[i])) {
+          const int at = atomicAdd(&sh.open, 1);
+          if (at < kMaxOpen) sh.block[at] = j + i;
+        }
+      }
+    }
+    in = read_lane(wave_scan(in), 63);
+    if (lane == 0) sh.n[wave] = in;
+    __syncthreads();
+    const int opened = sh.open;
+    if (opened > kMaxOpen || n > kMaxMarked) {
+      // Too many (equal scores, very long lists): 64-bit keys of all that may
+      // be wanted in place of the intervals, and the same narrowing on them.
+#pragma unroll 1
+      for (int j = tid / 16; j < n; j += kThreads / 16) {
+        const Ends v = ends[j];
+        unsigned long long k = v.lower == ~0u ? kForced : kMissing;
+        if (v.lower != ~0u && v.upper >= reach) k = order_key(exact_score(a, b, h, table[j], tid & 15));
+        // The 16 lanes run together: all have read v before one writes.
+        if ((tid & 15) == 0) scratch[j] = k;
+      }
+      __syncthreads();
+      unsigned long long klo = ~0ull, khi = 0;
+      for (int j = tid; j < n; j += kThreads) {
+        const unsigned long long k = scratch[j];
+        if (k != kMissing && k != kForced) {
+          klo = min(klo, k);
+          khi = max(khi, k);
+        }
+      }
+#pragma unroll 1
+      for (int o = 32; o > 0; o >>= 1) {
+        klo = min(klo, (unsigned long long)__shfl_xor((long long)klo, o));
+        khi = max(khi, (unsigned long long)__shfl_xor((long long)khi, o));
+      }
+      if (lane == 0) {
+        sh.lo[wave] = klo;
+        sh.hi[wave] = khi;
+      }
+      for (int i = tid; i < 2 * kParts; i += kThreads) (&sh.hist[0][0])[i] = 0;
+      __syncthreads();
+      for (int w = 0; w < kWaves; ++w) {
+        klo = min(klo, sh.lo[w]);
+        khi = max(khi, sh.hi[w]);
+      }
+      int ties;
+      const unsigned long long cut = narrow<unsigned long long>(sh, klo, khi, left, [&](auto f) {
+        for (int j = tid; j < n; j += kThreads) f(scratch[j]);
+      }, &ties);
+      int out = 0, seen = 0;
+      for (int j0 = 0; j0 < n; j0 += kThreads) {
+        const int j = j0 + tid;
+        const unsigned long long k = j < n ? scratch[j] : kMissing;
+        const uint64_t above = __ballot(k > cut), equal = __ballot(k == cut);
+        __syncthreads();
+        if (lane == 0) {
+          sh.n[wave] = __popcll(above);
+          sh.f[wave] = __popcll(equal);
+        }
+        __syncthreads();
+        int r = out + __popcll(above & below), e = seen + __popcll(equal & below);
+        for (int w = 0; w < kWaves; ++w) {
+          if (w < wave) {
+            r += sh.n[w];
+            e += sh.f[w];
+          }
+          out += sh.n[w];
+          seen += sh.f[w];
+        }
+        if (k > cut || (k == cut && e < ties)) sel[r + min(e, ties)] = j;
+      }
+      for (int i = out + min(seen, ties) + tid; i < a.keep; i += kThreads) sel[i] = -1;
+      return;
+    }
+    in = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) in += sh.n[w];
+#pragma unroll 1
+    for (int c = tid / 16; c < opened; c += kThreads / 16) {
       const double s = exact_score(a, b, h, table[sh.block[c]], tid & 15);
       if ((tid & 15) == 0) sh.key[c] = order_key(s);
     }
     __syncthreads();
-    bool taken = false;
-    if (tid < candidates) {
-      const unsigned long long k = sh.key[tid];
+#pragma unroll 1
+    for (int c = tid; c < opened; c += kThreads) {
+      const unsigned long long k = sh.key[c];
+      const int j = sh.block[c];
       int better = 0;
-      for (int c = 0; c < candidates; ++c) better += sh.key[c] > k || (sh.key[c] == k && c < tid);
-      taken = better < left;
+      for (int i = 0; i < opened; ++i)
+        better += sh.key[i] > k || (sh.key[i] == k && sh.block[i] < j);
+      if (better < left + forced - in) atomicOr(&sh.chosen[j / 32], 1u << (j & 31));
     }
-    const uint64_t m = __ballot(taken);
-    if (lane == 0) sh.f[wave] = __popcll(m);
     __syncthreads();
-    int r = early + __popcll(m & below);
-#pragma unroll
-    for (int w = 0; w < kTopWaves; ++w)
-      if (w < wave) r += sh.f[w];
-    if (taken) sel[r] = sh.block[tid];
-    // The forced ones in front and behind.
-    int front = 0, back = early + left;
-    const int late = max(n - a.last, min(a.first, n));
-    for (int j0 = 0; j0 < min(a.first, n); j0 += 64) {
-      const bool f = j0 + lane < min(a.first, n) && ends[j0 + lane].lower == inf;
-      const uint64_t fm = __ballot(f);
-      if (f && wave == 0) sel[front + __popcll(fm & below)] = j0 + lane;
-      front += __popcll(fm);
-    }
-    for (int j0 = late; j0 < n; j0 += 64) {
-      const bool f = j0 + lane < n && ends[j0 + lane].lower == inf;
-      const uint64_t fm = __ballot(f);
-      if (f && wave == 0) sel[back + __popcll(fm & below)] = j0 + lane;
-      back += __popcll(fm);
-    }
-    for (int i = back + tid; i < a.keep; i += kTopThreads) sel[i] = -1;
-    return;
   }
 
-  // Many candidates (equal scores, long lists): 64-bit keys in place of the
-  // intervals, then the same narrowing on them.
-  for (int j = tid / 16; j < n; j += kTopThreads / 16) {
-    const Interval v = ends[j];
-    unsigned long long k = v.lower == inf ? kForced : kMissing;
-    if (candidate(v)) k = order_key(exact_score(a, b, h, table[j], tid & 15));
-    // The 16 lanes have all read v (they run together) before one writes.
-    if ((tid & 15) == 0) scratch[j] = k;
-  }
-  __syncthreads();
-  unsigned long long klo = ~0ull, khi = 0;
-  for (int j = tid; j < n; j += kTopThreads) {
-    const unsigned long long k = scratch[j];
-    if (k != kMissing && k != kForced) {
-      klo = min(klo, k);
-      khi = max(khi, k);
-    }
-  }
-  klo = wave_min(klo);
-  khi = wave_max(khi);
-  if (lane == 0) {
-    sh.lo[wave] = klo;
-    sh.hi[wave] = khi;
-  }
-  __syncthreads();
+  // Out in index order: each wave counts its run of blocks, then writes it,
+  // four blocks a lane.
+  const int run = ceil_div(ceil_div(n, kWaves), 256) * 256;
+  const int j0 = wave * run, j1 = min(j0 + run, n);
+  auto chosen4 = [&](int j) {
+    uint32_t bits = 0;
+    if (j < j1) {
+      const u32x4 l = lower4(j);
 #pragma unroll
-  for (int w = 0; w < kTopWaves; ++w) {
-    klo = min(klo, sh.lo[w]);
-    khi = max(khi, sh.hi[w]);
-  }
-  int ties;
-  const unsigned long long cut = narrow(sh, klo, khi, left, [&](auto f) {
-    for (int j = tid; j < n; j += kTopThreads) f(scratch[j]);
-  }, &ties);
-  int out = 0, seen = 0;
-  for (int j0 = 0; j0 < n; j0 += kTopThreads) {
-    const int j = j0 + tid;
-    const unsigned long long k = j < n ? scratch[j] : kMissing;
-    const uint64_t above = __ballot(k > cut), equal = __ballot(k == cut);
-    __syncthreads();
-    if (lane == 0) {
-      sh.n[wave] = __popcll(above);
-      sh.f[wave] = __popcll(equal);
+      for (int i = 0; i < 4; ++i) bits |= (uint32_t)(l[i] >= sure) << i;
+      if (rival != 0) bits |= (sh.chosen[j / 32] >> (j & 31)) & 15;
     }
-    __syncthreads();
-    int r = out + __popcll(above & below), e = seen + __popcll(equal & below);
+    return bits;
+  };
+  int mine = 0;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += 256) mine += __popc(chosen4(j + 4 * lane));
+  mine = read_lane(wave_scan(mine), 63);
+  __syncthreads();
+  if (lane == 0) sh.f[wave] = mine;
+  __syncthreads();
+  int at = 0, out = 0;
 #pragma unroll
-    for (int w = 0; w < kTopWaves; ++w) {
-      if (w < wave) {
-        r += sh.n[w];
-        e += sh.f[w];
-      }
-      out += sh.n[w];
-      seen += sh.f[w];
-    }
-    if (k > cut || (k == cut && e < ties)) sel[r + min(e, ties)] = j;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) at += sh.f[w];
+    out += sh.f[w];
   }
-  for (int i = out + min(seen, ties) + tid; i < a.keep; i += kTopThreads) sel[i] = -1;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += 256) {
+    const uint32_t bits = chosen4(j + 4 * lane);
+    const int upto = wave_scan((int)__popc(bits));
+    int r = at + upto - __popc(bits);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((bits >> i) & 1) sel[r++] = j + 4 * lane + i;
+    at += read_lane(upto, 63);
+  }
+  for (int i = out + tid; i < a.keep; i += kThreads) sel[i] = -1;
 }
 
-hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream) {
-  const int heads = a.H % 4 == 0 ? 4 : a.H % 2 == 0 ? 2 : 1;
-  auto score = [&](auto kernel) { kernel<<<kScoreGrid, 256, 0, stream>>>(a); };
-  switch (a.D) {
-    case 64:
-      heads == 4   ? score(select_score_kernel<64, 4>)
-      : heads == 2 ? score(select_score_kernel<64, 2>)
-                   : score(select_score_kernel<64, 1>);
-      break;
-    case 128:
-      heads == 4   ? score(select_score_kernel<128, 4>)
-      : heads == 2 ? score(select_score_kernel<128, 2>)
-                   : score(select_score_kernel<128, 1>);
-      break;
-    case 256:
-      heads == 4   ? score(select_score_kernel<256, 4>)
-      : heads == 2 ? score(select_score_kernel<256, 2>)
-                   : score(select_score_kernel<256, 1>);
-      break;
-    default: return hipErrorInvalidValue;
-  }
-  hipError_t e = hipGetLastError();
+namespace {
+
+template <int D, int kHeads>
+hipError_t launch_score(const SelectArgs& a, hipStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  const hipError_t e = once_per_device(done, [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(select_score_kernel<D, kHeads>),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, 4 * BoundsTile<D>::kLds);
+  });
   if (e != hipSuccess) return e;
-  select_top_kernel<<<dim3(a.H, a.B), kTopThreads, 0, stream>>>(a);
+  select_score_kernel<D, kHeads><<<kScoreGrid, 256, 4 * BoundsTile<D>::kLds, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_score_heads(const SelectArgs& a, hipStream_t stream) {
+  return a.H % 4 == 0   ? launch_score<D, 4>(a, stream)
+         : a.H % 2 == 0 ? launch_score<D, 2>(a, stream)
+                        : launch_score<D, 1>(a, stream);
+}
+
+template <int kWaves>
+hipError_t launch_top(const SelectArgs& a, hipStream_t stream) {
+  const int held = std::min((a.max_blocks + 3) / 4 * 4, kMaxHeld);
+  static std::atomic<unsigned long long> done{0};
+  const hipError_t e = once_per_device(done, [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(select_top_kernel<kWaves>),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 8);
+  });
+  if (e != hipSuccess) return e;
+  select_top_kernel<kWaves><<<dim3(a.H, a.B), 64 * kWaves, held * 8, stream>>>(a, held);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream) {
+  const hipError_t e = a.D == 64    ? launch_score_heads<64>(a, stream)
+                       : a.D == 128 ? launch_score_heads<128>(a, stream)
+                       : a.D == 256 ? launch_score_heads<256>(a, stream)
+                                    : hipErrorInvalidValue;
+  if (e != hipSuccess) return e;
+  // Few blocks: four waves, whose barriers cost less.
+  return a.max_blocks <= 4096 ? launch_top<4>(a, stream) : launch_top<16>(a, stream);
 }
 
 }  // namespace mova

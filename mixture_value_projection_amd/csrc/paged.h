@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace mova {
@@ -57,8 +59,16 @@ struct SelectArgs {
   int B, Hq, H, D;
   int keep, first, last;
   int32_t* sel;    // [B, H, keep]
-  unsigned long long* scratch;  // [B, H, max_blocks]
+  unsigned long long* scratch;  // select_scratch_words
 };
+// Words of scratch between two rows of it (16-byte aligned rows), and in all
+// (rows are read four words at a time).
+__host__ __device__ constexpr size_t select_stride(int max_blocks) {
+  return ((size_t)max_blocks + 1) / 2 * 2;
+}
+inline size_t select_scratch_words(int B, int H, int max_blocks) {
+  return B == 0 ? 0 : (size_t)B * H * select_stride(max_blocks) + 4;
+}
 hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream);
 
 struct AttentionArgs {
@@ -128,10 +138,81 @@ __device__ __forceinline__ long long block_exclusive_scan(long long x, long long
   return before + inc - x;
 }
 
+// ---- sums over a wave in registers (no LDS round trips) ----
+
+// x of the lane that the DPP control names; 0 where there is none or the row
+// is masked out.
+template <int kCtrl, int kRows = 0xf>
+__device__ __forceinline__ int dpp_or_0(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, kCtrl, kRows, 0xf, true);
+}
+template <int kCtrl, int kRows = 0xf>
+__device__ __forceinline__ double dpp_or_0(double x) {
+  int2 u = __builtin_bit_cast(int2, x);
+  u.x = dpp_or_0<kCtrl, kRows>(u.x);
+  u.y = dpp_or_0<kCtrl, kRows>(u.y);
+  return __builtin_bit_cast(double, u);
+}
+// Inclusive sum over lanes 0 .. lane (int or double).
+template <class X>
+__device__ __forceinline__ X wave_scan(X x) {
+  x += dpp_or_0<0x111>(x);       // row_shr 1, 2, 4, 8
+  x += dpp_or_0<0x112>(x);
+  x += dpp_or_0<0x114>(x);
+  x += dpp_or_0<0x118>(x);
+  x += dpp_or_0<0x142, 0xa>(x);  // row_bcast 15, 31
+  x += dpp_or_0<0x143, 0xc>(x);
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  auto step = [&](int moved) { x += __builtin_bit_cast(float, moved); };
+  step(dpp_or_0<0x111>(__builtin_bit_cast(int, x)));
+  step(dpp_or_0<0x112>(__builtin_bit_cast(int, x)));
+  step(dpp_or_0<0x114>(__builtin_bit_cast(int, x)));
+  step(dpp_or_0<0x118>(__builtin_bit_cast(int, x)));
+  step(dpp_or_0<0x142, 0xa>(__builtin_bit_cast(int, x)));
+  step(dpp_or_0<0x143, 0xc>(__builtin_bit_cast(int, x)));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+__device__ __forceinline__ int read_lane(int x, int lane) {
+  return __builtin_amdgcn_readlane(x, lane);
+}
+__device__ __forceinline__ double read_lane(double x, int lane) {
+  int2 u = __builtin_bit_cast(int2, x);
+  u.x = __builtin_amdgcn_readlane(u.x, lane);
+  u.y = __builtin_amdgcn_readlane(u.y, lane);
+  return __builtin_bit_cast(double, u);
+}
+// op over the wave of 32-bit x, in all lanes.
+template <class X, class Op>
+__device__ __forceinline__ X wave_reduce(X x, Op op) {
+  auto step = [&](auto ctrl, auto rows) {
+    const int i = __builtin_bit_cast(int, x);
+    return __builtin_bit_cast(
+        X, __builtin_amdgcn_update_dpp(i, i, decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+  };
+  using std::integral_constant;
+  x = op(x, step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{}));
+  x = op(x, step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{}));
+  x = op(x, step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{}));
+  x = op(x, step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{}));
+  x = op(x, step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{}));
+  x = op(x, step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{}));
+  return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
+// floor(x / y) for 0 <= x < 2^52 and 0 < y < 2^52: the quotient is at least
+// 1 / y > 2^-52 x / y away from the next whole number, so rounding it cannot
+// reach that.
+__device__ __forceinline__ long long floor_div(long long x, long long y) {
+  return (long long)((double)x / (double)y);
+}
+
 // A line of work over a ragged batch: request b brings cost(b) units, one
 // request after the other, and each of gridDim.x workgroups takes an equal
-// stretch [start, end) of them.  The workgroup finds the request that its
-// stretch begins in, and that request's first unit, from the lengths alone.
+// stretch [start, end) of them (2^52 units at most).  The workgroup finds the
+// request that its stretch begins in, and that request's first unit, from the
+// lengths alone.
 struct Line {
   long long stretch, start, end;
   long long first;  // first unit of request b
@@ -143,15 +224,35 @@ struct LineShared {
 };
 // For workgroups of 256 threads.  False: nothing to do.  `prefix` (null, or
 // B + 1 numbers): workgroup 0 writes the requests' first units and the stretch.
+// Up to 64 requests each wave adds up the line for itself, one request a lane;
+// above, the workgroup does.
 template <class Cost>
 __device__ __forceinline__ bool line_begin(int B, Cost cost, LineShared& sh, long long* prefix,
                                            Line* line) {
+  if (B <= 64) {
+    const int lane = threadIdx.x & 63;
+    const double mine = lane < B ? (double)cost(lane) : 0.0;
+    const double upto = wave_scan(mine), before = upto - mine;
+    const long long total = (long long)read_lane(upto, 63);
+    line->stretch = max(floor_div(total + gridDim.x - 1, gridDim.x), 1ll);
+    line->start = line->stretch * blockIdx.x;
+    line->end = min(line->start + line->stretch, total);
+    if (prefix != nullptr && blockIdx.x == 0 && threadIdx.x < 64) {
+      if (lane < B) prefix[lane] = (long long)before;
+      if (lane == 0) prefix[B] = line->stretch;
+    }
+    if (line->start >= total) return false;
+    const double at = (double)line->start;
+    line->b = __ffsll((unsigned long long)__ballot(before <= at && at < upto)) - 1;
+    line->first = (long long)read_lane(before, line->b);
+    return true;
+  }
   const int per = ceil_div(B, 256);
   const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
   long long mine = 0, total;
   for (int b = b0; b < b1; ++b) mine += cost(b);
   long long before = block_exclusive_scan<4>(mine, sh.tmp, &total);
-  line->stretch = max((total + gridDim.x - 1) / gridDim.x, 1ll);
+  line->stretch = max(floor_div(total + gridDim.x - 1, gridDim.x), 1ll);
   line->start = line->stretch * blockIdx.x;
   line->end = min(line->start + line->stretch, total);
   if (before <= line->start && line->start < before + mine) {
@@ -170,8 +271,8 @@ __device__ __forceinline__ bool line_begin(int B, Cost cost, LineShared& sh, lon
   }
   if (line->start >= total) return false;
   __syncthreads();
-  line->b = sh.b;
-  line->first = sh.first;
+  line->b = __builtin_amdgcn_readfirstlane(sh.b);
+  line->first = (long long)read_lane((double)sh.first, 0);
   return true;
 }
 
@@ -179,6 +280,32 @@ __device__ __forceinline__ bool line_begin(int B, Cost cost, LineShared& sh, lon
 __device__ __forceinline__ int request_len(const int32_t* seq_lens, int b, int max_blocks,
                                            int block_size) {
   return min(max(seq_lens[b], 0), max_blocks * block_size);
+}
+
+// Direct-to-LDS loads of 16 and 4 bytes a lane, to consecutive places.
+__device__ __forceinline__ void stream_to_lds(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, kLdsLoadNonTemporal);
+}
+__device__ __forceinline__ void word_to_lds(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 4, 0, 0);
+}
+
+// A use of x: the load behind it is waited for here and not later.
+template <class X>
+__device__ __forceinline__ void loaded(X& x) {
+  asm volatile("" : "+v"(x));
+}
+
+// Waits until at most `left` <= kMost groups of kOps vector-memory operations
+// are outstanding, and for LDS.
+template <int kMost, int kOps>
+__device__ __forceinline__ void wait_groups(int left) {
+  if constexpr (kMost == 0) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
+  } else {
+    if (left == kMost) __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(kMost * kOps));
+    else wait_groups<kMost - 1, kOps>(left);
+  }
 }
 
 }  // namespace mova

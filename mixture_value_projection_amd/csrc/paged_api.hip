@@ -68,7 +68,7 @@ int check_attention(int B, int n_heads, int n_kv_heads, int head_dim, int max_bl
 }
 
 size_t select_bytes(int B, int n_kv_heads, int max_blocks) {
-  return align256((size_t)B * n_kv_heads * max_blocks * 8);
+  return align256(8 * select_scratch_words(B, n_kv_heads, max_blocks));
 }
 
 int check_workspace(const void* workspace, size_t have, size_t need) {
