@@ -113,31 +113,6 @@ __device__ __forceinline__ int fast_div(int n, FastDiv f) {
   return (int)(((unsigned long long)(uint32_t)n * f.mul) >> f.shift);
 }
 
-// Exclusive scan of one number a thread over a workgroup of kWaves waves;
-// *total gets the sum.  `tmp` holds one number a wave and may be used again
-// after the next barrier.
-template <int kWaves>
-__device__ __forceinline__ long long block_exclusive_scan(long long x, long long* tmp,
-                                                          long long* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  long long inc = x;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const long long up = __shfl_up(inc, o);
-    if (lane >= o) inc += up;
-  }
-  if (lane == 63) tmp[wave] = inc;
-  __syncthreads();
-  long long before = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += tmp[w];
-    sum += tmp[w];
-  }
-  *total = sum;
-  return before + inc - x;
-}
-
 // ---- sums over a wave in registers (no LDS round trips) ----
 
 // x of the lane that the DPP control names; 0 where there is none or the row
@@ -199,6 +174,26 @@ __device__ __forceinline__ X wave_reduce(X x, Op op) {
   x = op(x, step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{}));
   x = op(x, step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{}));
   return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
+// Exclusive scan of one number a thread over a workgroup of kWaves waves;
+// *total gets the sum (below 2^53).  `tmp` holds one number a wave and may be
+// used again after the next barrier.
+template <int kWaves>
+__device__ __forceinline__ long long block_exclusive_scan(long long x, long long* tmp,
+                                                          long long* total) {
+  const int wave = threadIdx.x >> 6;
+  const long long inc = (long long)wave_scan((double)x);
+  if ((threadIdx.x & 63) == 63) tmp[wave] = inc;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += tmp[w];
+    sum += tmp[w];
+  }
+  *total = sum;
+  return before + inc - x;
 }
 
 // floor(x / y) for 0 <= x < 2^52 and 0 < y < 2^52: the quotient is at least

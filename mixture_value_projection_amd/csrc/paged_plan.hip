@@ -107,8 +107,8 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     s_len[b] = ok ? (int)c : -1;
     if (blockIdx.x == 0) a.seq_lens[b] = n < 0 ? 0 : (int)(ok ? c + n : c);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) taken = max(taken, __shfl_xor(taken, o));
+  // Whole numbers up to free_capacity.
+  taken = wave_reduce((int)taken, [](int x, int y) { return max(x, y); });
   if ((tid & 63) == 0) tmp[3][tid >> 6] = taken;
   __syncthreads();
   taken = max(max(tmp[3][0], tmp[3][1]), max(tmp[3][2], tmp[3][3]));
