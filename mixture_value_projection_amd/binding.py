@@ -8,6 +8,7 @@ computation runs in the library's HIP kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, NamedTuple, Optional, Tuple
 
@@ -115,6 +116,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...], device) -> None:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -531,14 +534,22 @@ def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device
     return t
 
 
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
 def _scratch(workspace: Optional[torch.Tensor], nbytes: int, what: str, device) -> torch.Tensor:
-    if nbytes == ctypes.c_size_t(-1).value:
+    if nbytes == _NO_SIZE:
         raise MovaError(-2, what)
-    if workspace is not None and workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    return workspace
+    if workspace is not None:
+        if workspace.device != device or workspace.dtype is not torch.uint8:
+            raise ValueError(f"workspace must be uint8 on {device}")
+        if workspace.numel() >= nbytes and workspace.is_contiguous():
+            return workspace
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+# The current stream's handle without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _launch(fn, name: str, device, *args) -> None:
@@ -546,19 +557,34 @@ def _launch(fn, name: str, device, *args) -> None:
     current."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs GPU tensors, got {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _stream(device))
+    index = device.index
+    stream = _raw_stream(index) if _raw_stream is not None else _stream(device)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(device))
+            rc = fn(*args, stream)
     if rc != MOVA_OK:
         raise MovaError(rc, name)
 
 
 def _dims(t: torch.Tensor, name: str, n: int, layout: str) -> Tuple[int, ...]:
-    if t.dim() != n:
+    shape = t.shape
+    if len(shape) != n:
         raise ValueError(f"{name} must be {layout}")
-    return tuple(t.shape)
+    return shape
+
+
+# Workspace sizes depend on the sizes alone, and a served model asks for the
+# same few again and again.
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(*sizes: int) -> int:
+    return load_library().mova_attention_workspace_bytes(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _select_bytes(*sizes: int) -> int:
+    return load_library().mova_block_select_workspace_bytes(*sizes)
 
 
 def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_size: int,
@@ -586,6 +612,10 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_
     _check(new_lens, "new_lens", i32, (B,), dev)
     if T < 0:
         raise ValueError("T must not be negative")
+    if seq_lens is None:
+        seq_lens = torch.empty_like(cached_lens)
+    if free_count_out is None:
+        free_count_out = torch.empty_like(free_count)
     plan = PagedPlan(_out(seq_lens, "seq_lens", i32, (B,), dev),
                      _out(cu_new, "cu_new", i32, (B + 1,), dev),
                      _out(slot_mapping, "slot_mapping", torch.int64, (T,), dev),
@@ -599,10 +629,11 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_
 
 
 def _check_pool(pool: torch.Tensor, name: str, shape, device) -> int:
-    if pool.dtype not in CACHE_DTYPES:
-        raise ValueError(f"{name} has dtype {pool.dtype}, expected bfloat16 or float8_e4m3fn")
-    _check(pool, name, pool.dtype, shape, device)
-    return CACHE_DTYPES[pool.dtype]
+    dtype = pool.dtype
+    if dtype not in CACHE_DTYPES:
+        raise ValueError(f"{name} has dtype {dtype}, expected bfloat16 or float8_e4m3fn")
+    _check(pool, name, dtype, shape, device)
+    return CACHE_DTYPES[dtype]
 
 
 def _check_scales(k_scale, v_scale, heads: int, device) -> None:
@@ -663,20 +694,19 @@ def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
     _check(k_bounds, "k_bounds", torch.bfloat16, (nb, H, 2, D), dev)
     _check(block_table, "block_table", torch.int32, (B, mb), dev)
     _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    nbytes = lib.mova_block_select_workspace_bytes(B, Hq, H, D, mb, block_size, keep)
+    nbytes = _select_bytes(B, Hq, H, D, mb, block_size, keep)
     workspace = _scratch(workspace, nbytes, "mova_block_select", dev)
     sel_blocks = _out(sel_blocks, "sel_blocks", torch.int32, (B, H, keep), dev)
     _launch(lib.mova_block_select, "mova_block_select", dev, _ptr(q), _ptr(k_bounds), nb,
             block_size, _ptr(block_table), mb, _ptr(seq_lens), B, Hq, H, D, keep, keep_first,
             keep_last, _ptr(sel_blocks), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+            workspace.numel())
     return sel_blocks
 
 
 def attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int,
                               max_blocks: int, block_size: int, keep: int = 0) -> int:
-    n = load_library().mova_attention_workspace_bytes(B, n_heads, n_kv_heads, head_dim, max_blocks,
-                                                      block_size, keep)
+    n = _attention_bytes(B, n_heads, n_kv_heads, head_dim, max_blocks, block_size, keep)
     if n == ctypes.c_size_t(-1).value:
         raise MovaError(-2, "mova_attention_workspace_bytes")
     return n
@@ -715,13 +745,16 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             raise ValueError("sel_blocks lists no blocks")
     if lse is not None:
         _check(lse, "lse", torch.float32, (B, Hq), dev)
-    nbytes = lib.mova_attention_workspace_bytes(B, Hq, H, D, mb, bs, keep)
+    nbytes = _attention_bytes(B, Hq, H, D, mb, bs, keep)
     workspace = _scratch(workspace, nbytes, "mova_attention_paged", dev)
-    out = _out(out, "out", torch.bfloat16, (B, Hq, D), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", torch.bfloat16, (B, Hq, D), dev)
     _launch(lib.mova_attention_paged, "mova_attention_paged", dev, _ptr(q), _ptr(k_cache),
             _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale), nb, bs, _ptr(block_table), mb,
             _ptr(seq_lens), _ptr(sel_blocks), keep, B, Hq, H, D, float(scale), int(window),
-            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size())
+            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel())
     return out
 
 

@@ -147,21 +147,24 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
     Ends* out = (Ends*)a.scratch + ((size_t)b * a.H + h) * select_stride(a.max_blocks);
 
-    // q+ and |q-| of query head g0 + r16 as MFMA columns.
-    Frag16 qp[kSteps], qn[kSteps];
+    // Query head g0 + r16 as an MFMA column, and its q+ and |q-|: kept, or, with
+    // wide heads, whose registers they would fill, formed at each use.
+    constexpr bool kKeep = D <= 128;
+    Frag16 q[kSteps], qp[kKeep ? kSteps : 1], qn[kKeep ? kSteps : 1];
+    auto split = [&](const Frag16& f, Frag16* pos, Frag16* neg) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = ((f.u[i] & 0x80008000u) >> 15) * 0xffffu;  // the negative ones
+        pos->u[i] = f.u[i] & ~m;
+        neg->u[i] = f.u[i] & m & 0x7fff7fffu;
+      }
+    };
     auto load_q = [&](int g0) {
       const __bf16* row = a.q + ((size_t)b * a.Hq + h * G + min(g0 + r16, G - 1)) * D + 8 * g4;
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        Frag16 f;
-        f.u = load16(row + 32 * u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // Bits of the elements whose sign is set.
-          const uint32_t neg = ((f.u[i] & 0x80008000u) >> 15) * 0xffffu;
-          qp[u].u[i] = f.u[i] & ~neg;
-          qn[u].u[i] = f.u[i] & neg & 0x7fff7fffu;
-        }
+        q[u].u = load16(row + 32 * u);
+        if constexpr (kKeep) split(q[u], &qp[u], &qn[u]);
       }
     };
     load_q(0);
@@ -175,7 +178,8 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
       if (block_at(x) >= n || page < 0 || page >= a.num_blocks) page = -1;
       const int row = max(page, 0);
       char* stage = ring + (x & (S - 1)) * T::kBytes;
-#pragma unroll
+      constexpr int kUnroll = T::kLoads > 8 ? 4 : T::kLoads;  // fewer addresses at a time
+#pragma unroll kUnroll
       for (int i = 0; i < T::kLoads; ++i) {
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
         const int c = (lane % T::kChunks) ^ rr;
@@ -213,13 +217,20 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
           lo.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow + ((4 * u + g4) ^ r16) * 16);
           hi.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow +
                                                  ((T::kChunks / 2 + 4 * u + g4) ^ r16) * 16);
-          s = mfma16x16x32(hi.h, qp[u].h, s);
+          Frag16 pos, neg;
+          if constexpr (kKeep) {
+            pos = qp[u];
+            neg = qn[u];
+          } else {
+            split(q[u], &pos, &neg);
+          }
+          s = mfma16x16x32(hi.h, pos.h, s);
           f.u = lo.u ^ 0x80008000u;
-          s = mfma16x16x32(f.h, qn[u].h, s);
+          s = mfma16x16x32(f.h, neg.h, s);
           f.u = hi.u & 0x7fff7fffu;
-          t = mfma16x16x32(f.h, qp[u].h, t);
+          t = mfma16x16x32(f.h, pos.h, t);
           f.u = lo.u & 0x7fff7fffu;
-          t = mfma16x16x32(f.h, qn[u].h, t);
+          t = mfma16x16x32(f.h, neg.h, t);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
