@@ -527,9 +527,8 @@ size_t mova_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int he
  *           log sum_p exp(scale * q . K[p]), -infinity for an empty row
  *
  * A row without keys (length 0, every block missing) gives zeros.  Products
- * accumulate in fp32; the softmax's maximum and sum are fp32, its weights are
- * rounded to bf16 for the product with V (the sum is over the unrounded ones);
- * the result is rounded once to bf16.  Results are bitwise reproducible for
+ * accumulate in fp32; the softmax's maximum and sum are fp32, its weights take
+ * part in the product with V to 16 bits; the result is rounded once to bf16.  Results are bitwise reproducible for
  * identical inputs; how a request's keys are split among workgroups, and so
  * the last bits of its row, depends on the lengths of the whole batch.
  * keep * block_size <= 2^30, scale finite.

@@ -12,7 +12,7 @@
 //
 // Work: the keys of a request, per group of key heads, are cut into tiles.
 // All tiles of the batch lie in one line, request after request, and each of
-// the kGrid workgroups (one per CU) takes an equal stretch of it, so ragged
+// the workgroups (one or two per CU) takes an equal stretch of it, so ragged
 // batches and single long requests fill the chip alike and the host needs no
 // lengths.  A request whose tiles lie in one stretch is finished there; else
 // each stretch leaves its part (m, sum, unnormalised out; fp32) in the
@@ -31,9 +31,9 @@
 // the softmax needs two lane exchanges a tile.  Their weights are then, as
 // they lie in the registers, the second operand of out^T = V^T P^T, whose
 // first operand the transposing LDS reads deliver; the sums over keys may run
-// in any order as long as both operands agree.  Weights are rounded to bf16 for this product (nearest even;
-// relative 2^-9 on average below, against bf16 outputs); maxima, sums and
-// accumulators are fp32.  8-bit elements are widened to bf16, which is exact.
+// in any order as long as both operands agree.  Weights go into this product
+// as two bf16 parts (2^-16 relative); maxima, sums and accumulators are fp32.
+// 8-bit elements are widened to bf16, which is exact.
 #include <algorithm>
 #include <atomic>
 
@@ -52,8 +52,8 @@ struct Parts {
 
 namespace {
 
-constexpr int kGrid = 256;         // one workgroup per CU
-constexpr int kRingBytes = 32768;  // keys and values in LDS per wave
+constexpr int kCus = 256;
+constexpr int kMaxGrid = 2 * kCus;  // workgroups of attention_kernel
 
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
@@ -71,17 +71,25 @@ struct Tile {
   static constexpr int kRowsPerLoad = 64 / kChunks;
   static constexpr int kLoads = kKeys / kRowsPerLoad;           // wave loads per side
   static constexpr int kSide = kKeys * kRow;                    // bytes of a side (K or V)
-  static constexpr int kStages = kRingBytes / (2 * kSide);
-  static constexpr int kLds = kRingBytes + 2 * kStages * 256;   // with the block numbers
+  // Two workgroups a CU with 16 KB of keys and values a wave, or one with 32:
+  // two hide each other's softmax (64 requests, 128 wide 130 -> 127 us; 64 wide
+  // with 8 bits 63 -> 54), where two tiles fit 16 KB; 8-bit tiles 128 wide are
+  // better off with four in the ring (129 against 133 us).
+  static constexpr int kPerCu = 4 * kSide <= 16384 && !(kFp8 && D == 128) ? 2 : 1;
+  static constexpr int kRing = 32768 / kPerCu;
+  static constexpr int kStages = kRing / (2 * kSide);
+  static constexpr int kLds = kRing + 2 * kStages * 256;        // with the block numbers
   static_assert(kStages >= 2 && kChunks <= 32 && kRowsPerLoad >= 2, "tile shape");
   // Piece c of row r lies at piece c ^ swizzle(r), so that the 8 rows of one
   // phase of the key fragments' reads, and the rows that 16 lanes of a
   // transposing read take, fall into different banks.
   static __device__ __forceinline__ int swizzle_k(int r) {
-    return (kChunks >= 8 ? r : r / (8 / kChunks)) & (kChunks - 1) & 15;
+    constexpr int kShare = kChunks >= 8 ? 1 : 8 / kChunks;
+    return (r / kShare) & (kChunks - 1) & 15;
   }
   static __device__ __forceinline__ int swizzle_v(int r) {
-    if constexpr (!kFp8) return (kChunks >= 16 ? 2 * r : 2 * (r / (16 / kChunks))) & (kChunks - 1) & 15;
+    constexpr int kShare = kChunks >= 16 ? 1 : 16 / kChunks;
+    if constexpr (!kFp8) return (2 * (r / kShare)) & (kChunks - 1) & 15;
     else if constexpr (kChunks == 4) return ((r >> 4) & 1) | ((r >> 1) & 2);
     else if constexpr (kChunks == 8) return ((r >> 1) & 1) | ((r >> 3) & 2) | (r & 4);
     else return (r & 3) | ((r >> 2) & 4) | ((r << 1) & 8);
@@ -91,7 +99,7 @@ struct Tile {
 size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
 
 Parts parts_of(const AttentionArgs& a) {
-  const size_t rows = (size_t)kGrid * 2 * heads_per_group(a.H) * std::min(a.Hq / a.H, 16);
+  const size_t rows = (size_t)kMaxGrid * 2 * heads_per_group(a.H) * std::min(a.Hq / a.H, 16);
   Parts p;
   p.prefix = (long long*)a.part;
   p.ml = a.part + prefix_floats(a.B);
@@ -160,7 +168,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   const int qtiles = ceil_div(G, 16);
   const int rows_per_b = a.H / kHeads * qtiles;
   char* ring = lds + wave * T::kLds;
-  int* pages = (int*)(ring + kRingBytes);
+  int* pages = (int*)(ring + T::kRing);
   int* listed = pages + S * 64;
 
   auto tiles_of = [&](const Span& s) { return ceil_div(s.keys, T::kKeys * kStripes); };
@@ -351,18 +359,24 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
             for (int i = 0; i < 4; ++i) o[c][i] *= keep;
         }
         m = mn;
+        // The weights in two bf16 parts, w = high + low to 2^-16: with 16-key
+        // tiles both parts fill one product's operand, against the same values
+        // twice; with 32-key tiles they are two products.
         union PFrag {
+          bf16_t e[8];
           s16x4 h[2];
           bf16x8 w;
-        } pf;
+        } high, low;
 #pragma unroll
         for (int t = 0; t < kSub; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float e = __builtin_amdgcn_exp2f(p[t][i] - safe);
             l += e;
-            pf.h[t][i] = (short)f32_to_bf16_bits(e);
+            high.e[4 * t + i] = (bf16_t)e;
+            low.e[4 * t + i] = (bf16_t)(e - (float)high.e[4 * t + i]);
           }
+        if constexpr (kSub == 1) high.h[1] = low.h[0];
         const uint32_t vt = (uint32_t)(uintptr_t)(lds_void*)(stage + T::kSide);
         constexpr int kPer = kFp8 ? 1 : kSub;  // reads a 16-column part
 #pragma unroll
@@ -387,15 +401,14 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
                 vf.u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, false));
                 vf.u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, true));
               }
-              acc = mfma16x16x32(vf.h, pf.w, acc);
-            } else if constexpr (kSub == 2) {
-              PFrag vf;
-              vf.h[0] = __builtin_bit_cast(s16x4, got[2 * i]);
-              vf.h[1] = __builtin_bit_cast(s16x4, got[2 * i + 1]);
-              acc = mfma16x16x32(vf.w, pf.w, acc);
+              acc = mfma16x16x32(vf.h, high.w, acc);
+              acc = mfma16x16x32(vf.h, low.w, acc);
             } else {
-              acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, got[i]), pf.h[0],
-                                                              acc, 0, 0, 0);
+              PFrag vf;
+              vf.h[0] = __builtin_bit_cast(s16x4, got[kSub * i]);
+              vf.h[1] = __builtin_bit_cast(s16x4, got[kSub * i + kSub - 1]);
+              acc = mfma16x16x32(vf.w, high.w, acc);
+              if constexpr (kSub == 2) acc = mfma16x16x32(vf.w, low.w, acc);
             }
           }
         }
@@ -424,7 +437,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       float* box = (float*)(lds + wave * T::kLds);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) *reinterpret_cast<f32x4*>(box + (c * 64 + lane) * 4) = o[c];
-      float* ml = (float*)(ring + kRingBytes);
+      float* ml = (float*)(ring + T::kRing);
       ml[lane] = m;
       ml[64 + lane] = l;
       __syncthreads();
@@ -432,7 +445,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 #pragma unroll 1
         for (int s = 1; s < kStripes; ++s) {
           const char* other = lds + (wave + s) * T::kLds;
-          const float* oml = (const float*)(other + kRingBytes);
+          const float* oml = (const float*)(other + T::kRing);
           const float m2 = oml[lane], l2 = oml[64 + lane];
           const float mn = fmaxf(m, m2);
           const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
@@ -477,84 +490,156 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   }
 }
 
-// Adds the parts of a request's query head that was split over stretches, and
-// writes the rows of requests without keys.  Workgroup (query head, request).
+// Adds the parts of a request's query heads that were split over stretches, and
+// writes the rows of requests without keys.  Workgroup (x, request) has
+// `at_once` query heads (1 or 4).  A head of few parts is one wave's work, with
+// one memory round trip and no barrier; one of many (a long request in few) is
+// the whole workgroup's.
+template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int heads,
-                                                             int tile_keys) {
-  __shared__ __attribute__((aligned(16))) float s_o[256 * 4];
-  __shared__ float s_e[256], s_m[4], s_l[4];
-  const int hq = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, D = a.D;
-  const size_t out_row = (size_t)b * a.Hq + hq;
+                                                             int tile_keys, int at_once) {
+  constexpr int kPer = D / 64;      // channels of a lane
+  constexpr int kFew = 32, kBatch = 8;
+  constexpr int kSlots = kMaxGrid / 256;
+  typedef __attribute__((__vector_size__(kPer * sizeof(float)))) float vec;
+  typedef __attribute__((__vector_size__(kPer * sizeof(__bf16)))) __bf16 half_vec;
+  __shared__ float s_e[kMaxGrid], s_m[4], s_l[4];
+  __shared__ vec s_o[4][64];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = ceil_div(span_of(a, b).keys, tile_keys);
-  if (n == 0) {
-    if (tid < D / 2) ((uint32_t*)(a.out + out_row * D))[tid] = 0u;
-    if (tid == 0 && a.lse != nullptr) a.lse[out_row] = -__builtin_huge_valf();
-    return;
-  }
-  const int G = a.Hq / a.H, h = hq / G, gi = hq - h * G;
+  const long long stretch = parts.prefix[a.B], before = parts.prefix[b];
+  const int G = a.Hq / a.H;
   const int qtiles = ceil_div(G, 16), cap = min(G, 16);
-  const long long stretch = parts.prefix[a.B];
-  const long long first = parts.prefix[b] + (long long)(h / heads * qtiles + gi / 16) * n;
-  const int w0 = (int)floor_div(first, stretch), w1 = (int)floor_div(first + n - 1, stretch);
-  if (w0 == w1) return;
-  const int np = w1 - w0 + 1;  // at most kGrid = 256, one a thread
-  auto part_of = [&](int i) {
+
+  auto finish = [&](int hq, vec o, float sum, float safe) {
+    const size_t row = (size_t)b * a.Hq + hq;
+    const float vs = a.v_scale != nullptr ? a.v_scale[hq / G] : 1.f;
+    const float f = sum == 0.f ? 0.f : vs / sum;
+    half_vec y;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) y[j] = (__bf16)(sum == 0.f ? 0.f : o[j] * f);
+    *reinterpret_cast<half_vec*>(a.out + row * D + kPer * lane) = y;
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[row] = sum == 0.f ? -__builtin_huge_valf()
+                              : (safe + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  };
+  // First part of the head, and how many there are.
+  auto parts_at = [&](int hq, int* w0) {
+    const int h = hq / G, gi = hq - h * G;
+    const long long first = before + (long long)(h / heads * qtiles + gi / 16) * n;
+    *w0 = (int)floor_div(first, stretch);
+    return n == 0 ? 0 : (int)floor_div(first + n - 1, stretch) - *w0 + 1;
+  };
+  auto part_of = [&](int hq, int w0, int i) {
+    const int h = hq / G, gi = hq - h * G;
     return ((size_t)((w0 + i) * 2 + (i == 0 ? 1 : 0)) * heads + h % heads) * cap + gi % 16;
   };
-  // Everything is asked for before the first wait: the thread's part's maximum
-  // and sum, and its first pieces of the outputs.
-  float m = -__builtin_huge_valf(), l = 0.f;
-  if (tid < np) {
-    const float2 v = *reinterpret_cast<const float2*>(parts.ml + 2 * part_of(tid));
-    m = v.x;
-    l = v.y;
-  }
-  constexpr int kBatch = 8;
-  const int lanes = D / 4, sub = tid / lanes, subs = 256 / lanes, c = tid % lanes;
-  f32x4 x[kBatch];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * subs;
-      if (i < np) x[k] = *reinterpret_cast<const f32x4*>(parts.o + part_of(i) * D + 4 * c);
-    }
-  };
-  load(sub);
-  float M = wave_reduce(m, [](float p, float q) { return fmaxf(p, q); });
-  if ((tid & 63) == 0) s_m[tid >> 6] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float safe = M == -__builtin_huge_valf() ? 0.f : M;
-  const float e = __builtin_amdgcn_exp2f(m - safe);
-  s_e[tid] = e;
-  // Sums in a fixed order: over the lanes, then the waves.
-  const float ls = wave_sum(l * e);
-  if ((tid & 63) == 0) s_l[tid >> 6] = ls;
-  __syncthreads();
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int i0 = sub; i0 < np; i0 += kBatch * subs) {
-    if (i0 != sub) load(i0);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * subs;
-      if (i < np) {
-        const float f = s_e[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += x[k][j] * f;
+  auto larger = [](float p, float q) { return fmaxf(p, q); };
+
+  {
+    const int hq = blockIdx.x * at_once + wave;
+    int w0;
+    const int np = wave < at_once && hq < a.Hq ? parts_at(hq, &w0) : 1;
+    if (np == 0) finish(hq, vec{}, 0.f, 0.f);
+    if (np > 1 && np <= kFew) {
+      // Everything is asked for before the first wait.
+      float m = -__builtin_huge_valf(), l = 0.f;
+      if (lane < np) {
+        const float2 v = *reinterpret_cast<const float2*>(parts.ml + 2 * part_of(hq, w0, lane));
+        m = v.x;
+        l = v.y;
       }
+      vec x[kBatch], o = {};
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k < np)
+            x[k] = *reinterpret_cast<const vec*>(parts.o + part_of(hq, w0, i0 + k) * D + kPer * lane);
+      };
+      load(0);
+      const float M = wave_reduce(m, larger);
+      const float safe = M == -__builtin_huge_valf() ? 0.f : M;
+      const float e = __builtin_amdgcn_exp2f(m - safe);
+      const float sum = wave_sum(l * e);
+      for (int i0 = 0; i0 < np; i0 += kBatch) {
+        if (i0 != 0) load(i0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k < np) {
+            const float f = __builtin_bit_cast(float, read_lane(__builtin_bit_cast(int, e), i0 + k));
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) o[j] += x[k][j] * f;
+          }
+      }
+      finish(hq, o, sum, safe);
     }
   }
-  *reinterpret_cast<f32x4*>(s_o + tid * 4) = o;
-  __syncthreads();
-  if (tid < D) {
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+
+  for (int t = 0; t < at_once; ++t) {
+    const int hq = blockIdx.x * at_once + t;
+    int w0 = 0;
+    const int np = hq < a.Hq ? parts_at(hq, &w0) : 0;  // at most kMaxGrid
+    if (np <= kFew) continue;
+    float m[kSlots], l[kSlots], M = -__builtin_huge_valf();
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      m[k] = -__builtin_huge_valf();
+      l[k] = 0.f;
+      if (tid + 256 * k < np) {
+        const float2 v =
+            *reinterpret_cast<const float2*>(parts.ml + 2 * part_of(hq, w0, tid + 256 * k));
+        m[k] = v.x;
+        l[k] = v.y;
+      }
+      M = fmaxf(M, m[k]);
+    }
+    vec x[kBatch], o = {};
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + 4 * k < np)
+          x[k] = *reinterpret_cast<const vec*>(parts.o + part_of(hq, w0, i0 + 4 * k) * D + kPer * lane);
+    };
+    load(wave);
+    M = wave_reduce(M, larger);
+    if (lane == 0) s_m[wave] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    const float safe = M == -__builtin_huge_valf() ? 0.f : M;
+    // Sums in a fixed order: a thread's, over the lanes, then the waves.
     float sum = 0.f;
-    for (int s = 0; s < subs; ++s) sum += s_o[s * D + tid];
-    const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
-    a.out[out_row * D + tid] = (__bf16)(l == 0.f ? 0.f : sum * (vs / l));
-    if (tid == 0 && a.lse != nullptr)
-      a.lse[out_row] = l == 0.f ? -__builtin_huge_valf()
-                                : (safe + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const float e = __builtin_amdgcn_exp2f(m[k] - safe);
+      s_e[tid + 256 * k] = e;
+      sum += l[k] * e;
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) s_l[wave] = sum;
+    __syncthreads();
+    for (int i0 = wave; i0 < np; i0 += 4 * kBatch) {
+      if (i0 != wave) load(i0);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + 4 * k < np) {
+          const float f = s_e[i0 + 4 * k];
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) o[j] += x[k][j] * f;
+        }
+    }
+    s_o[wave][lane] = o;
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const vec y = s_o[w][lane];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] += y[j];
+      }
+      finish(hq, o, (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), safe);
+    }
+    __syncthreads();
   }
 }
 
@@ -562,7 +647,7 @@ size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int
                                 int keep) {
   (void)max_blocks; (void)block_size; (void)keep;
   if (B == 0) return 0;
-  const size_t rows = (size_t)kGrid * 2 * heads_per_group(H) * std::min(Hq / H, 16);
+  const size_t rows = (size_t)kMaxGrid * 2 * heads_per_group(H) * std::min(Hq / H, 16);
   return prefix_floats(B) + (rows * 2 + 63) / 64 * 64 + rows * D;
 }
 
@@ -580,11 +665,13 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const Parts parts = parts_of(a);
   attention_kernel<D, kFp8, kHeads, kList>
-      <<<kGrid, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size));
+      <<<T::kPerCu * kCus, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size));
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attention_join_kernel<<<dim3(a.Hq, a.B), 256, 0, stream>>>(a, parts, kHeads,
-                                                              T::kKeys * (4 / kHeads));
+  // Few heads in the batch: a workgroup each, since they may have many parts.
+  const int at_once = (long long)a.B * a.Hq >= 1024 ? 4 : 1;
+  attention_join_kernel<D><<<dim3(ceil_div(a.Hq, at_once), a.B), 256, 0, stream>>>(
+      a, parts, kHeads, T::kKeys * (4 / kHeads), at_once);
   return hipGetLastError();
 }
 

@@ -138,10 +138,10 @@ def attention(q, k_cache, v_cache, table, lens, scale, k_scale=None, v_scale=Non
     * a logit is an fp32 sum of D exact products: off by at most
       d = (D + 4) u24 scale sum |q k|, and its softmax weight by 2 d
       relatively (numerator and sum), the exponential adding 2^-18;
-    * each weight rounded to bf16: u8 relative, so with both the sum over V is
-      off by (u8 + 2 d + 2^-18) sum p |v|, and its fp32 accumulation by less
-      than 2^-14 sum p |v| (n u24 for the n <= 2^10 terms of the tests' largest
-      running chains);
+    * each weight as two bf16 parts: u8^2 = 2^-16 relative, so with both the
+      sum over V is off by (2^-16 + 2 d + 2^-18) sum p |v|, and its fp32
+      accumulation by less than 2^-13 sum p |v| (n u24 for the n <= 2^11
+      terms, two a key, of the tests' largest running chains);
     * the result rounded to bf16: u8 |out|, plus half the smallest subnormal.
     """
     B, Hq, D = q.shape
@@ -181,7 +181,7 @@ def attention(q, k_cache, v_cache, table, lens, scale, k_scale=None, v_scale=Non
             o = p @ v * float(vs[h])
             spread = p @ v.abs() * float(vs[h])
             out[b, h * G:(h + 1) * G] = o
-            tol[b, h * G:(h + 1) * G] = (u8 * o.abs() + (u8 + 2 * d + 2.0 ** -18 + 2.0 ** -14)
+            tol[b, h * G:(h + 1) * G] = (u8 * o.abs() + (2.0 ** -16 + 2 * d + 2.0 ** -18 + 2.0 ** -13)
                                          * spread + 2.0 ** -134)
             lse[b, h * G:(h + 1) * G] = (m + torch.log(e.sum(1, keepdim=True)))[:, 0]
             tol_lse[b, h * G:(h + 1) * G] = (2 * d + 2.0 ** -16 * (1 + m.abs()))[:, 0]
