@@ -37,9 +37,8 @@ namespace mova {
 
 namespace {
 
-constexpr int kScoreGrid = 256;      // one workgroup a CU
-constexpr int kRingBytes = 32768;    // bounds in LDS per wave
-constexpr int kTileBlocks = 16;
+constexpr int kCus = 256;
+constexpr int kTileBlocks = kSelectTile;
 
 // Bound on the error of a 32-bit sum s of products with absolute sum t, in any
 // order of summation, the additions rounded or cut: at most 2 * 256 products
@@ -83,6 +82,14 @@ __device__ __forceinline__ float max16(float x) {
   return fmaxf(x, other(std::integral_constant<int, 0x140>{}));  // row_mirror
 }
 
+// Largest over the wave's lanes 16 g + r, r < 4, for all.
+__device__ __forceinline__ uint32_t tile_max(uint32_t x) {
+  x = max(x, (uint32_t)dpp_or_0<0xB1>((int)x));  // quad_perm 1 0 3 2, 2 3 0 1
+  x = max(x, (uint32_t)dpp_or_0<0x4E>((int)x));
+  return max(max((uint32_t)read_lane((int)x, 0), (uint32_t)read_lane((int)x, 16)),
+             max((uint32_t)read_lane((int)x, 32), (uint32_t)read_lane((int)x, 48)));
+}
+
 __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
   return a.num_blocks > 0
              ? ceil_div(request_len(a.seq_lens, b, a.max_blocks, a.block_size), a.block_size)
@@ -95,7 +102,8 @@ __device__ __forceinline__ int blocks_of(const SelectArgs& a, int b) {
 // MFMA rows are blocks, columns query heads (those past the group are left
 // out of the maxima).  Each wave reads through a ring of tiles in LDS, as in
 // attention.hip: with the fragments read straight into registers, one tile
-// ahead or none, the kernel took 40 and 35 us where this takes 
+// ahead or none, the kernel took 40 and 35 us where this takes 25 (3 requests
+// of 100k to 400k tokens).
 template <int D>
 struct BoundsTile {
   static constexpr int kRow = 4 * D;  // bytes of a block's bounds, lo then hi
@@ -103,8 +111,13 @@ struct BoundsTile {
   static constexpr int kRowsPerLoad = 64 / kChunks;
   static constexpr int kBytes = kTileBlocks * kRow;
   static constexpr int kLoads = kTileBlocks / kRowsPerLoad;
-  static constexpr int kStages = kRingBytes / kBytes;
-  static constexpr int kLds = kRingBytes + kStages * 256;
+  // Two workgroups a CU with 16 KB of bounds a wave, where that is two tiles,
+  // or one with 32 (128 wide: 28.9 against 31.5 us for both kernels, 32 requests
+  // of up to 30k tokens).
+  static constexpr int kPerCu = 2 * kBytes <= 16384 ? 2 : 1;
+  static constexpr int kRing = 32768 / kPerCu;
+  static constexpr int kStages = kRing / kBytes;
+  static constexpr int kLds = kRing + kStages * 256;
 };
 
 template <int D, int kHeads>
@@ -129,7 +142,7 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     return;
 
   char* ring = lds + wave * T::kLds;
-  int* fetched = (int*)(ring + kRingBytes);
+  int* fetched = (int*)(ring + T::kRing);
   int b = line.b;
   long long at = line.first;
   int n = blocks_of(a, b), tiles = tiles_of(n);
@@ -146,6 +159,8 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     const int h = hgroup * kHeads + hsub;
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
     Ends* out = (Ends*)a.scratch + ((size_t)b * a.H + h) * select_stride(a.max_blocks);
+    Ends* tops = (Ends*)a.scratch + select_tiles_at(a.B, a.H, a.max_blocks) +
+                 ((size_t)b * a.H + h) * ceil_div(a.max_blocks, kTileBlocks);
 
     // Query head g0 + r16 as an MFMA column, and its q+ and |q-|: kept, or, with
     // wide heads, whose registers they would fill, formed at each use.
@@ -257,6 +272,12 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
         else if (j < a.first || j >= n - a.last) mine = {~0u, ~0u};
         out[j] = mine;
       }
+      // The tile's largest ends, of the blocks that are neither missing nor
+      // always in.
+      const bool counts = r16 < 4 && j < n && mine.lower != ~0u;
+      const uint32_t tl = tile_max(counts ? mine.lower : 0u), tu = tile_max(counts ? mine.upper : 0u);
+      const int tile = (t0 + x) * kStripes + stripe;
+      if (lane == 0 && tile * kTileBlocks < n) tops[tile] = {tl, tu};
       }
       if (x + S < nt) {
         const int entry = fetched[(x & (S - 1)) * 64 + lane];
@@ -281,6 +302,7 @@ struct TopShared {
   uint32_t chosen[kMaxMarked / 32];
   unsigned long long key[kMaxOpen];
   int block[kMaxOpen];
+  int tiles[kMaxHeld / kTileBlocks];
   unsigned long long lo[kWaves], hi[kWaves];
   int n[kWaves], f[kWaves];
   int part, above, in, open;
@@ -414,11 +436,95 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     return u;
   };
 
+  // Long lists: as many tiles as blocks are wanted have a block whose lower end
+  // is at least the wanted-th largest of the tiles' maxima, so only the tiles
+  // that reach that with an upper end, and those with blocks that are always
+  // in, need looking at.
+  int m = n;
+  bool picked = false;
+  const int tiles = ceil_div(n, kTileBlocks);
+  if (tiles > 4 * (long long)a.keep) {
+    const Ends* tops = (const Ends*)a.scratch + select_tiles_at(a.B, a.H, a.max_blocks) +
+                       ((size_t)b * a.H + h) * ceil_div(a.max_blocks, kTileBlocks);
+    const int front = min(a.first, n), behind = max(n - a.last, front);
+    uint32_t lo = ~0u, hi = 0;
+    int filled = 0, forced = 0;
+    for (int j = tid; j < front; j += kThreads) forced += ends[j].lower == ~0u;
+    for (int j = behind + tid; j < n; j += kThreads) forced += ends[j].lower == ~0u;
+    for (int t = tid; t < tiles; t += kThreads) {
+      const uint32_t k = tops[t].lower;
+      filled += k != 0;
+      lo = min(lo, k - 1);
+      hi = max(hi, k);
+    }
+    lo = wave_reduce(lo, umin);
+    hi = wave_reduce(hi, umax);
+    filled = read_lane(wave_scan(filled), 63);
+    forced = read_lane(wave_scan(forced), 63);
+    if (lane == 0) {
+      sh.lo[wave] = lo;
+      sh.hi[wave] = hi;
+      sh.n[wave] = filled;
+      sh.f[wave] = forced;
+    }
+    __syncthreads();
+    filled = forced = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      lo = min(lo, (uint32_t)sh.lo[w]);
+      hi = max(hi, (uint32_t)sh.hi[w]);
+      filled += sh.n[w];
+      forced += sh.f[w];
+    }
+    __syncthreads();
+    const int left = a.keep - forced;
+    if (left > 0 && filled > left) {
+      int ties;
+      const uint32_t reach = narrow<uint32_t>(sh, lo + 1, hi, left, [&](auto f) {
+#pragma unroll 1
+        for (int t = tid; t < tiles; t += kThreads) f(tops[t].lower);
+      }, &ties);
+      const int run = ceil_div(ceil_div(tiles, kWaves), 64) * 64;
+      const int first = wave * run, last = min(first + run, tiles);
+      auto wanted = [&](int t) {
+        return t < last && (tops[t].upper >= reach || t * kTileBlocks < front ||
+                            (t + 1) * kTileBlocks > behind);
+      };
+      int mine = 0;
+#pragma unroll 1
+      for (int t = first; t < last; t += 64) mine += __popcll(__ballot(wanted(t + lane)));
+      __syncthreads();
+      if (lane == 0) sh.f[wave] = mine;
+      __syncthreads();
+      int at = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) at += sh.f[w];
+        all += sh.f[w];
+      }
+      picked = all * (long long)kTileBlocks <= held;
+      if (picked) {
+        m = all * kTileBlocks;
+#pragma unroll 1
+        for (int t = first; t < last; t += 64) {
+          const uint64_t yes = __ballot(wanted(t + lane));
+          if ((yes >> lane) & 1) sh.tiles[at + __popcll(yes & below)] = t + lane;
+          at += __popcll(yes);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  // Block that the i-th one looked at is.
+  auto block_of = [&](int i) {
+    return picked ? sh.tiles[i / kTileBlocks] * kTileBlocks + i % kTileBlocks : i;
+  };
+
   uint32_t lo = ~0u, hi = 0;
   int there = 0, forced = 0;
-  for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+  for (int j = 4 * tid; j < m; j += 4 * kThreads) {
     u32x4 l, u;
-    fetch4(j, &l, &u);
+    fetch4(block_of(j), &l, &u);
     if (j < held) {
       *(u32x4*)(kept_lower + j) = l;
       *(u32x4*)(kept_upper + j) = u;
@@ -467,14 +573,14 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     __syncthreads();
     reach = narrow<uint32_t>(sh, lo, hi, left, [&](auto f) {
 #pragma unroll 1
-      for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+      for (int j = 4 * tid; j < m; j += 4 * kThreads) {
         const u32x4 l = lower4(j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f(l[i]);
       }
     }, &ties);
 #pragma unroll 1
-    for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+    for (int j = 4 * tid; j < m; j += 4 * kThreads) {
       const u32x4 l = lower4(j), u = upper4(j);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -495,9 +601,9 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     // Undecided blocks: listed in LDS, computed by 16 lanes each, and chosen by
     // counting the better ones.
     int in = 0;
-    for (int i = tid; i < min(ceil_div(n, 32), kMaxMarked / 32); i += kThreads) sh.chosen[i] = 0;
+    for (int i = tid; i < min(ceil_div(m, 32), kMaxMarked / 32); i += kThreads) sh.chosen[i] = 0;
 #pragma unroll 1
-    for (int j = 4 * tid; j < n; j += 4 * kThreads) {
+    for (int j = 4 * tid; j < m; j += 4 * kThreads) {
       const u32x4 l = lower4(j), u = upper4(j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -512,7 +618,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     if (lane == 0) sh.n[wave] = in;
     __syncthreads();
     const int opened = sh.open;
-    if (opened > kMaxOpen || n > kMaxMarked) {
+    if (opened > kMaxOpen || m > kMaxMarked) {
       // Too many (equal scores, very long lists): 64-bit keys of all that may
       // be wanted in place of the intervals, and the same narrowing on them.
 #pragma unroll 1
@@ -581,7 +687,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     for (int w = 0; w < kWaves; ++w) in += sh.n[w];
 #pragma unroll 1
     for (int c = tid / 16; c < opened; c += kThreads / 16) {
-      const double s = exact_score(a, b, h, table[sh.block[c]], tid & 15);
+      const double s = exact_score(a, b, h, table[block_of(sh.block[c])], tid & 15);
       if ((tid & 15) == 0) sh.key[c] = order_key(s);
     }
     __syncthreads();
@@ -599,8 +705,8 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
 
   // Out in index order: each wave counts its run of blocks, then writes it,
   // four blocks a lane.
-  const int run = ceil_div(ceil_div(n, kWaves), 256) * 256;
-  const int j0 = wave * run, j1 = min(j0 + run, n);
+  const int run = ceil_div(ceil_div(m, kWaves), 256) * 256;
+  const int j0 = wave * run, j1 = min(j0 + run, m);
   auto chosen4 = [&](int j) {
     uint32_t bits = 0;
     if (j < j1) {
@@ -631,7 +737,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, i
     int r = at + upto - __popc(bits);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if ((bits >> i) & 1) sel[r++] = j + 4 * lane + i;
+      if ((bits >> i) & 1) sel[r++] = block_of(j + 4 * lane + i);
     at += read_lane(upto, 63);
   }
   for (int i = out + tid; i < a.keep; i += kThreads) sel[i] = -1;
@@ -647,7 +753,7 @@ hipError_t launch_score(const SelectArgs& a, hipStream_t stream) {
                                hipFuncAttributeMaxDynamicSharedMemorySize, 4 * BoundsTile<D>::kLds);
   });
   if (e != hipSuccess) return e;
-  select_score_kernel<D, kHeads><<<kScoreGrid, 256, 4 * BoundsTile<D>::kLds, stream>>>(a);
+  select_score_kernel<D, kHeads><<<BoundsTile<D>::kPerCu * kCus, 256, 4 * BoundsTile<D>::kLds, stream>>>(a);
   return hipGetLastError();
 }
 

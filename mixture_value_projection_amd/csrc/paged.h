@@ -61,13 +61,19 @@ struct SelectArgs {
   int32_t* sel;    // [B, H, keep]
   unsigned long long* scratch;  // select_scratch_words
 };
-// Words of scratch between two rows of it (16-byte aligned rows), and in all
-// (rows are read four words at a time).
+// Scratch, in 8-byte words: a word a block in 16-byte aligned rows, read four
+// words at a time; then a word a tile of kSelectTile blocks.
+constexpr int kSelectTile = 16;
 __host__ __device__ constexpr size_t select_stride(int max_blocks) {
   return ((size_t)max_blocks + 1) / 2 * 2;
 }
+__host__ __device__ constexpr size_t select_tiles_at(int B, int H, int max_blocks) {
+  return (size_t)B * H * select_stride(max_blocks) + 4;
+}
 inline size_t select_scratch_words(int B, int H, int max_blocks) {
-  return B == 0 ? 0 : (size_t)B * H * select_stride(max_blocks) + 4;
+  return B == 0 ? 0
+                : select_tiles_at(B, H, max_blocks) +
+                      (size_t)B * H * ceil_div(max_blocks, kSelectTile);
 }
 hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream);
 

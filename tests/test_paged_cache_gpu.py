@@ -238,6 +238,9 @@ SELECT = [
     ([640] * 9, 20, 4, 128, 32, 33, 1, 1),      # keep > blocks
     ([40000, 100], 4, 1, 64, 2, 1500, 2, 2),    # more blocks and candidates than are held at once
     ([17000], 2, 1, 128, 1, 90, 20, 70),        # only the forced ones
+    ([30000, 200, 3000], 8, 2, 128, 4, 16, 1, 3),  # many tiles of blocks, few wanted
+    ([60000, 59999], 4, 1, 64, 1, 20, 0, 0),
+    ([33000], 4, 2, 256, 1, 40, 17, 20),
     ([-5, 10 ** 6, 48], 6, 2, 64, 16, 6, 1, 1),  # lengths out of range
 ]
 
@@ -245,7 +248,7 @@ SELECT = [
 @pytest.mark.parametrize("lens,Hq,H,D,bs,keep,first,last", SELECT)
 def test_select(lens, Hq, H, D, bs, keep, first, last):
     rng = np.random.default_rng(len(lens) + D + keep)
-    mb = max(1, min(max(R.ceil_div(n, bs) for n in lens), 20000)) + 3
+    mb = max(1, min(max(R.ceil_div(n, bs) for n in lens), 60000)) + 3
     nb = sum(min(R.ceil_div(max(n, 0), bs), mb) for n in lens) + 2
     table = make_table(rng, lens, bs, nb, mb)
     q = torch.from_numpy(rng.standard_normal((len(lens), Hq, D), dtype=np.float32)).to(torch.bfloat16)
