@@ -526,7 +526,8 @@ size_t mova_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int he
  *   lse     float [B, n_heads] or NULL: log of the softmax's sum,
  *           log sum_p exp(scale * q . K[p]), -infinity for an empty row
  *
- * A row without keys (length 0, every block missing) gives zeros.  Products
+ * A row without keys (length 0, every block missing), or whose every logit is
+ * -infinity, gives zeros and an lse of -infinity.  Products
  * accumulate in fp32; the softmax's maximum and sum are fp32, its weights take
  * part in the product with V to 16 bits; the result is rounded once to bf16.  Results are bitwise reproducible for
  * identical inputs; how a request's keys are split among workgroups, and so

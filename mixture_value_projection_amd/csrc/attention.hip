@@ -57,7 +57,6 @@ constexpr int kMaxGrid = 2 * kCus;  // workgroups of attention_kernel
 
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
-typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 
 // Waves of a workgroup on different key heads; the others split the tiles.
 int heads_per_group(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
@@ -121,6 +120,18 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   return s;
 }
 
+// 8 e4m3 elements as bf16 (exact).
+__device__ __forceinline__ Frag16 widen_fp8(uint32_t w0, uint32_t w1) {
+  auto two = [](uint32_t w, auto upper) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                            (int)w, 1.f, decltype(upper)::value));
+  };
+  Frag16 f;
+  f.u = u32x4{two(w0, std::false_type{}), two(w0, std::true_type{}), two(w1, std::false_type{}),
+              two(w1, std::true_type{})};
+  return f;
+}
+
 // Four transposing LDS reads of 8 bytes a lane (16 lanes hand out 16 columns of
 // the 128 bytes that they address) and the wait for them, in one block: as
 // builtins, each read would first wait for every direct load in flight (the
@@ -148,7 +159,8 @@ __device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (
 
 // kHeads: key heads of a workgroup; 4 / kHeads waves share a head's tiles.
 template <int D, bool kFp8, int kHeads, bool kList>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts, FastDiv by_block) {
+__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts,
+                                                        FastDiv by_block) {
   using T = Tile<D, kFp8>;
   constexpr int kStripes = 4 / kHeads;
   constexpr int S = T::kStages;
@@ -231,7 +243,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       bool ok;
       if constexpr (kList) {
         ok = blk < a.keep && from_list >= 0 && from_list < blocks;
-        const int p = from_list * a.block_size + r;
+        const int p = (ok ? from_list : 0) * a.block_size + r;
         ok = ok && p >= sp.lo && p < sp.len;
       } else {
         ok = blk * a.block_size + r < sp.len;
@@ -325,16 +337,11 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
           } else {
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
-              const u32x4 w = *reinterpret_cast<const u32x4*>(kr + ((4 * u + g4) ^ T::swizzle_k(rr)) * 16);
+              const u32x4 w =
+                  *reinterpret_cast<const u32x4*>(kr + ((4 * u + g4) ^ T::swizzle_k(rr)) * 16);
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                Frag16 kf;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int ww = (int)w[2 * half + i];
-                  kf.u[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ww, 1.f, false));
-                  kf.u[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ww, 1.f, true));
-                }
+                const Frag16 kf = widen_fp8(w[2 * half], w[2 * half + 1]);
                 s = mfma16x16x32(kf.h, qf[2 * u + half].h, s);
               }
             }
@@ -342,7 +349,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             p[t][i] = s[i] * qs;
-            if (mask != kAll && !((mask >> (16 * t + 4 * g4 + i)) & 1)) p[t][i] = -__builtin_huge_valf();
+            if (mask != kAll && !((mask >> (16 * t + 4 * g4 + i)) & 1))
+              p[t][i] = -__builtin_huge_valf();
             top = fmaxf(top, p[t][i]);
           }
         }
@@ -386,7 +394,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = c0 + i / kPer, t = i % kPer;
-            const int rr = kFp8 ? 4 * g4 + (r16 / 2 & 3) + 16 * (r16 / 8) : 16 * t + 4 * g4 + r16 / 4;
+            const int rr =
+                kFp8 ? 4 * g4 + (r16 / 2 & 3) + 16 * (r16 / 8) : 16 * t + 4 * g4 + r16 / 4;
             const int piece = kFp8 ? c : 2 * c + (r16 & 3) / 2;
             from[i] = vt + rr * T::kRow + (piece ^ T::swizzle_v(rr)) * 16 + 8 * (r16 & 1);
           }
@@ -395,12 +404,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
           for (int i = 0; i < 4 / kPer; ++i) {
             f32x4& acc = o[c0 + i];
             if constexpr (kFp8) {
-              Frag16 vf;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                vf.u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, false));
-                vf.u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(got[i][j], 1.f, true));
-              }
+              const Frag16 vf = widen_fp8((uint32_t)got[i][0], (uint32_t)got[i][1]);
               acc = mfma16x16x32(vf.h, high.w, acc);
               acc = mfma16x16x32(vf.h, low.w, acc);
             } else {
@@ -529,7 +533,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     const int h = hq / G, gi = hq - h * G;
     const long long first = before + (long long)(h / heads * qtiles + gi / 16) * n;
     *w0 = (int)floor_div(first, stretch);
-    return n == 0 ? 0 : (int)floor_div(first + n - 1, stretch) - *w0 + 1;
+    return n == 0 ? 0 : min((int)floor_div(first + n - 1, stretch), kMaxGrid - 1) - *w0 + 1;
   };
   auto part_of = [&](int hq, int w0, int i) {
     const int h = hq / G, gi = hq - h * G;

@@ -166,12 +166,12 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     // wide heads, whose registers they would fill, formed at each use.
     constexpr bool kKeep = D <= 128;
     Frag16 q[kSteps], qp[kKeep ? kSteps : 1], qn[kKeep ? kSteps : 1];
-    auto split = [&](const Frag16& f, Frag16* pos, Frag16* neg) {
+    auto split = [&](const Frag16& f, Frag16* plus, Frag16* minus) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t m = ((f.u[i] & 0x80008000u) >> 15) * 0xffffu;  // the negative ones
-        pos->u[i] = f.u[i] & ~m;
-        neg->u[i] = f.u[i] & m & 0x7fff7fffu;
+        plus->u[i] = f.u[i] & ~m;
+        minus->u[i] = f.u[i] & m & 0x7fff7fffu;
       }
     };
     auto load_q = [&](int g0) {
@@ -212,72 +212,73 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     for (int i = 0; i < S; ++i) word_to_lds(address(i), fetched + i * 64);
     __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0_imm(0));
     asm volatile("" ::: "memory");
+    // The S turns before tile 0 only fill the ring.
     for (int x = -S; x < nt; ++x) {
       const int page = pages[0];
 #pragma unroll
       for (int i = 0; i + 1 < S; ++i) pages[i] = pages[i + 1];
       if (x >= 0) {
-      wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
-      asm volatile("" ::: "memory");
-      const char* stage = ring + (x & (S - 1)) * T::kBytes;
-      float lowest[4], highest[4];
+        wait_groups<S - 1, kGroupLoads>(min(S - 1, nt - 1 - x));
+        asm volatile("" ::: "memory");
+        const char* stage = ring + (x & (S - 1)) * T::kBytes;
+        float lowest[4], highest[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lowest[i] = highest[i] = -__builtin_huge_valf();
-      for (int g0 = 0; g0 < G; g0 += 16) {
-        if (G > 16) load_q(g0);
-        f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, t = s;
+        for (int i = 0; i < 4; ++i) lowest[i] = highest[i] = -__builtin_huge_valf();
+        for (int g0 = 0; g0 < G; g0 += 16) {
+          if (G > 16) load_q(g0);
+          f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, t = s;
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-          Frag16 lo, hi, f;
-          lo.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow + ((4 * u + g4) ^ r16) * 16);
-          hi.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow +
-                                                 ((T::kChunks / 2 + 4 * u + g4) ^ r16) * 16);
-          Frag16 pos, neg;
-          if constexpr (kKeep) {
-            pos = qp[u];
-            neg = qn[u];
-          } else {
-            split(q[u], &pos, &neg);
+          for (int u = 0; u < kSteps; ++u) {
+            Frag16 lo, hi, f;
+            lo.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow + ((4 * u + g4) ^ r16) * 16);
+            hi.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow +
+                                                   ((T::kChunks / 2 + 4 * u + g4) ^ r16) * 16);
+            Frag16 plus, minus;
+            if constexpr (kKeep) {
+              plus = qp[u];
+              minus = qn[u];
+            } else {
+              split(q[u], &plus, &minus);
+            }
+            s = mfma16x16x32(hi.h, plus.h, s);
+            f.u = lo.u ^ 0x80008000u;
+            s = mfma16x16x32(f.h, minus.h, s);
+            f.u = hi.u & 0x7fff7fffu;
+            t = mfma16x16x32(f.h, plus.h, t);
+            f.u = lo.u & 0x7fff7fffu;
+            t = mfma16x16x32(f.h, minus.h, t);
           }
-          s = mfma16x16x32(hi.h, pos.h, s);
-          f.u = lo.u ^ 0x80008000u;
-          s = mfma16x16x32(f.h, neg.h, s);
-          f.u = hi.u & 0x7fff7fffu;
-          t = mfma16x16x32(f.h, pos.h, t);
-          f.u = lo.u & 0x7fff7fffu;
-          t = mfma16x16x32(f.h, neg.h, t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e = t[i] * kErrorRel + kErrorAbs;
+            const bool enclosed = fabsf(s[i]) + t[i] < 3e38f;
+            float lower = enclosed ? s[i] - e : -__builtin_huge_valf();
+            float upper = enclosed ? s[i] + e : __builtin_huge_valf();
+            if (g0 + r16 >= G) lower = upper = -__builtin_huge_valf();
+            lowest[i] = fmaxf(lowest[i], lower);
+            highest[i] = fmaxf(highest[i], upper);
+          }
         }
+        Ends mine = {0u, 0u};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = t[i] * kErrorRel + kErrorAbs;
-          const bool enclosed = fabsf(s[i]) + t[i] < 3e38f;
-          float lower = enclosed ? s[i] - e : -__builtin_huge_valf();
-          float upper = enclosed ? s[i] + e : __builtin_huge_valf();
-          if (g0 + r16 >= G) lower = upper = -__builtin_huge_valf();
-          lowest[i] = fmaxf(lowest[i], lower);
-          highest[i] = fmaxf(highest[i], upper);
+          const Ends v = {order_key(max16(lowest[i])), order_key(max16(highest[i]))};
+          if (r16 == i) mine = v;
         }
-      }
-      Ends mine = {0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Ends v = {order_key(max16(lowest[i])), order_key(max16(highest[i]))};
-        if (r16 == i) mine = v;
-      }
-      const int i = 4 * g4 + (r16 & 3);
-      const int j = ((t0 + x) * kStripes + stripe) * kTileBlocks + i;
-      const int p = __shfl(page, i);
-      if (r16 < 4 && j < n) {
-        if (p < 0) mine = {0u, 0u};
-        else if (j < a.first || j >= n - a.last) mine = {~0u, ~0u};
-        out[j] = mine;
-      }
-      // The tile's largest ends, of the blocks that are neither missing nor
-      // always in.
-      const bool counts = r16 < 4 && j < n && mine.lower != ~0u;
-      const uint32_t tl = tile_max(counts ? mine.lower : 0u), tu = tile_max(counts ? mine.upper : 0u);
-      const int tile = (t0 + x) * kStripes + stripe;
-      if (lane == 0 && tile * kTileBlocks < n) tops[tile] = {tl, tu};
+        const int i = 4 * g4 + (r16 & 3);
+        const int j = ((t0 + x) * kStripes + stripe) * kTileBlocks + i;
+        const int p = __shfl(page, i);
+        if (r16 < 4 && j < n) {
+          if (p < 0) mine = {0u, 0u};
+          else if (j < a.first || j >= n - a.last) mine = {~0u, ~0u};
+          out[j] = mine;
+        }
+        // The tile's largest ends, of the blocks that are neither missing nor
+        // always in.
+        const bool counts = r16 < 4 && j < n && mine.lower != ~0u;
+        const Ends most = {tile_max(counts ? mine.lower : 0u), tile_max(counts ? mine.upper : 0u)};
+        const int tile = (t0 + x) * kStripes + stripe;
+        if (lane == 0 && tile * kTileBlocks < n) tops[tile] = most;
       }
       if (x + S < nt) {
         const int entry = fetched[(x & (S - 1)) * 64 + lane];
@@ -291,12 +292,15 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
 
 namespace {
 
+// Eight waves: with four the passes over long lists take longer, with sixteen
+// the barriers (39 us for both kernels against 42 and 41, 3 requests of 100k to
+// 400k tokens).
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kParts = 2048;          // of a histogram
 constexpr int kMaxHeld = 14336;       // blocks whose ends LDS holds, a multiple of 4
 constexpr int kMaxOpen = 1024;        // undecided blocks computed in LDS
 constexpr int kMaxMarked = 65536;     // blocks with a mark in LDS
 
-template <int kWaves>
 struct TopShared {
   int hist[2][kParts];
   uint32_t chosen[kMaxMarked / 32];
@@ -312,9 +316,9 @@ struct TopShared {
 // for_each(f) hands to f one after the other.  Returns the cut: keys from it
 // on are wanted, and of those equal to it the first *ties.  Both histograms
 // are clear on entry.
-template <class K, int kWaves, class ForEach>
-__device__ K narrow(TopShared<kWaves>& sh, K lo, K hi, int left, ForEach for_each, int* ties) {
-  constexpr int kThreads = 64 * kWaves, kPer = kParts / kThreads;
+template <class K, class ForEach>
+__device__ K narrow(TopShared& sh, K lo, K hi, int left, ForEach for_each, int* ties) {
+  constexpr int kPer = kParts / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int round = 0;; ++round) {
     const unsigned long long span = (unsigned long long)(hi - lo);
@@ -393,10 +397,8 @@ __device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int h,
 // Workgroup (h, b): the `keep` blocks with the highest scores, the lower index
 // first among equals, in index order.  A pass over 12,500 blocks is bound by
 // the instructions of its one CU, hence ready-made keys, four to a read.
-template <int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void select_top_kernel(SelectArgs a, int held) {
-  constexpr int kThreads = 64 * kWaves;
-  __shared__ TopShared<kWaves> sh;
+__global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int held) {
+  __shared__ TopShared sh;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   uint32_t *kept_lower = (uint32_t*)lds, *kept_upper = kept_lower + held;  // of the first blocks
   const int tid = threadIdx.x, lane = tid & 63;
@@ -764,16 +766,15 @@ hipError_t launch_score_heads(const SelectArgs& a, hipStream_t stream) {
                         : launch_score<D, 1>(a, stream);
 }
 
-template <int kWaves>
 hipError_t launch_top(const SelectArgs& a, hipStream_t stream) {
   const int held = std::min((a.max_blocks + 3) / 4 * 4, kMaxHeld);
   static std::atomic<unsigned long long> done{0};
   const hipError_t e = once_per_device(done, [&] {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(select_top_kernel<kWaves>),
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(select_top_kernel),
                                hipFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld * 8);
   });
   if (e != hipSuccess) return e;
-  select_top_kernel<kWaves><<<dim3(a.H, a.B), 64 * kWaves, held * 8, stream>>>(a, held);
+  select_top_kernel<<<dim3(a.H, a.B), kThreads, held * 8, stream>>>(a, held);
   return hipGetLastError();
 }
 
@@ -784,9 +785,7 @@ hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream) {
                        : a.D == 128 ? launch_score_heads<128>(a, stream)
                        : a.D == 256 ? launch_score_heads<256>(a, stream)
                                     : hipErrorInvalidValue;
-  if (e != hipSuccess) return e;
-  // Few blocks: four waves, whose barriers cost less.
-  return a.max_blocks <= 4096 ? launch_top<4>(a, stream) : launch_top<16>(a, stream);
+  return e == hipSuccess ? launch_top(a, stream) : e;
 }
 
 }  // namespace mova
