@@ -162,24 +162,20 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
     Ends* tops = (Ends*)a.scratch + select_tiles_at(a.B, a.H, a.max_blocks) +
                  ((size_t)b * a.H + h) * ceil_div(a.max_blocks, kTileBlocks);
 
-    // Query head g0 + r16 as an MFMA column, and its q+ and |q-|: kept, or, with
-    // wide heads, whose registers they would fill, formed at each use.
-    constexpr bool kKeep = D <= 128;
-    Frag16 q[kSteps], qp[kKeep ? kSteps : 1], qn[kKeep ? kSteps : 1];
-    auto split = [&](const Frag16& f, Frag16* plus, Frag16* minus) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t m = ((f.u[i] & 0x80008000u) >> 15) * 0xffffu;  // the negative ones
-        plus->u[i] = f.u[i] & ~m;
-        minus->u[i] = f.u[i] & m & 0x7fff7fffu;
-      }
-    };
+    // q+ and |q-| of query head g0 + r16 as MFMA columns.
+    Frag16 qp[kSteps], qn[kSteps];
     auto load_q = [&](int g0) {
       const __bf16* row = a.q + ((size_t)b * a.Hq + h * G + min(g0 + r16, G - 1)) * D + 8 * g4;
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        q[u].u = load16(row + 32 * u);
-        if constexpr (kKeep) split(q[u], &qp[u], &qn[u]);
+        Frag16 f;
+        f.u = load16(row + 32 * u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = ((f.u[i] & 0x80008000u) >> 15) * 0xffffu;  // the negative ones
+          qp[u].u[i] = f.u[i] & ~m;
+          qn[u].u[i] = f.u[i] & m & 0x7fff7fffu;
+        }
       }
     };
     load_q(0);
@@ -225,7 +221,12 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) lowest[i] = highest[i] = -__builtin_huge_valf();
         for (int g0 = 0; g0 < G; g0 += 16) {
-          if (G > 16) load_q(g0);
+          if (G > 16) {
+            load_q(g0);
+            // Waited for here: a group of up to 16 has no such wait.
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) loaded(qp[u].u), loaded(qn[u].u);
+          }
           f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f}, t = s;
 #pragma unroll
           for (int u = 0; u < kSteps; ++u) {
@@ -233,20 +234,13 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
             lo.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow + ((4 * u + g4) ^ r16) * 16);
             hi.u = *reinterpret_cast<const u32x4*>(stage + r16 * T::kRow +
                                                    ((T::kChunks / 2 + 4 * u + g4) ^ r16) * 16);
-            Frag16 plus, minus;
-            if constexpr (kKeep) {
-              plus = qp[u];
-              minus = qn[u];
-            } else {
-              split(q[u], &plus, &minus);
-            }
-            s = mfma16x16x32(hi.h, plus.h, s);
+            s = mfma16x16x32(hi.h, qp[u].h, s);
             f.u = lo.u ^ 0x80008000u;
-            s = mfma16x16x32(f.h, minus.h, s);
+            s = mfma16x16x32(f.h, qn[u].h, s);
             f.u = hi.u & 0x7fff7fffu;
-            t = mfma16x16x32(f.h, plus.h, t);
+            t = mfma16x16x32(f.h, qp[u].h, t);
             f.u = lo.u & 0x7fff7fffu;
-            t = mfma16x16x32(f.h, minus.h, t);
+            t = mfma16x16x32(f.h, qn[u].h, t);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
