@@ -48,7 +48,8 @@ __device__ __forceinline__ int clamp_int(long long v) {
 
 }  // namespace
 
-__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
+__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a,
+                                                                  FastDiv by_block) {
   // Per request: first token row, blocks handed out before it, blocks given
   // back before it, and its stored length (-1: it gets no slots).
   extern __shared__ int plan_lds[];
@@ -60,16 +61,26 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
 
   const int tid = threadIdx.x;
   const int bs = a.block_size;
-  const long long most = (long long)a.max_blocks * bs;
+  const int most = a.max_blocks * bs;  // at most 2^30
+  // Blocks that n <= most tokens fill.
+  auto blocks = [&](int n) { return fast_div(n + bs - 1, by_block); };
   const int per = ceil_div(a.B, kPlanThreads);
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   const int count = min(max(*a.free_count, 0), a.free_capacity);
 
+  // The thread's first request stays in registers (up to 256 requests it is the
+  // only one).
+  const int fresh0 = b0 < b1 ? a.fresh[b0] : 0, cached0 = b0 < b1 ? a.cached[b0] : 0;
+  auto fresh = [&](int b) { return b == b0 ? fresh0 : a.fresh[b]; };
+  auto cached = [&](int b) {
+    return min(max(b == b0 ? cached0 : a.cached[b], 0), most);
+  };
+
   long long rows = 0, back = 0;
   for (int b = b0; b < b1; ++b) {
-    const int n = a.fresh[b];
+    const int n = fresh(b);
     if (n >= 0) rows += n;
-    else back += (min((long long)max(a.cached[b], 0), most) + bs - 1) / bs;
+    else back += blocks(cached(b));
   }
   long long all_rows, all_back, all_need;
   const long long row0 = block_exclusive_scan<kPlanThreads / 64>(rows, tmp[0], &all_rows);
@@ -77,35 +88,35 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   const int have = (int)min((long long)count + all_back, (long long)a.free_capacity);
 
   // Needs of the requests whose tokens fit their table row and the T rows.
-  auto need_of = [&](long long c, int n, long long row_end) -> long long {
-    if (n < 0 || c + n > most || row_end > a.T) return -1;
-    return (c + n + bs - 1) / bs - (c + bs - 1) / bs;
+  auto need_of = [&](int c, int n, long long row_end) -> long long {
+    if (n < 0 || n > most - c || row_end > a.T) return -1;
+    return blocks(c + n) - blocks(c);
   };
   long long need = 0, at = row0;
   for (int b = b0; b < b1; ++b) {
-    const int n = a.fresh[b];
+    const int n = fresh(b);
     at += max(n, 0);
-    need += max(need_of(min((long long)max(a.cached[b], 0), most), n, at), 0ll);
+    need += max(need_of(cached(b), n, at), 0ll);
   }
   const long long need0 = block_exclusive_scan<kPlanThreads / 64>(need, tmp[2], &all_need);
 
   long long upto = need0, taken = 0, given = back0;
   at = row0;
   for (int b = b0; b < b1; ++b) {
-    const int n = a.fresh[b];
-    const long long c = min((long long)max(a.cached[b], 0), most);
+    const int n = fresh(b);
+    const int c = cached(b);
     s_row[b] = clamp_int(at);
     s_need[b] = clamp_int(upto);
     s_back[b] = clamp_int(given);
     if (blockIdx.x == 0) a.cu_new[b] = clamp_int(at);
     at += max(n, 0);
-    if (n < 0) given += (c + bs - 1) / bs;
+    if (n < 0) given += blocks(c);
     const long long mine = need_of(c, n, at);
     upto += max(mine, 0ll);
     const bool ok = mine == 0 || (mine > 0 && upto <= have);
     if (mine > 0 && ok) taken = upto;
-    s_len[b] = ok ? (int)c : -1;
-    if (blockIdx.x == 0) a.seq_lens[b] = n < 0 ? 0 : (int)(ok ? c + n : c);
+    s_len[b] = ok ? c : -1;
+    if (blockIdx.x == 0) a.seq_lens[b] = n < 0 ? 0 : ok ? c + n : c;
   }
   // Whole numbers up to free_capacity.
   taken = wave_reduce((int)taken, [](int x, int y) { return max(x, y); });
@@ -137,7 +148,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
       const int c = s_len[b];
       if (c >= 0) {
         p = c + (t - s_row[b]);
-        const int j = p / bs, old = (c + bs - 1) / bs;
+        const int j = fast_div(p, by_block), old = blocks(c);
         const int page = j < old ? a.table[(size_t)b * a.max_blocks + j] : popped(s_need[b] + j - old);
         slot = (long long)page * bs + (p - j * bs);
       }
@@ -147,7 +158,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   }
   for (int i = g; i < (int)taken; i += step) {
     const int b = last_at_most(s_need, a.B, i);
-    const int old = (s_len[b] + bs - 1) / bs;
+    const int old = blocks(s_len[b]);
     a.table[(size_t)b * a.max_blocks + old + (i - s_need[b])] = popped(i);
   }
   for (int j = g; j < have - count; j += step) a.free_blocks[count + j] = returned(j);
@@ -159,7 +170,8 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
   // come back in one call.
   const long long items = std::max<long long>(a.T, (long long)a.B * a.max_blocks / 16);
   const int grid = (int)std::min<long long>(std::max<long long>((items + 255) / 256, 1), 128);
-  paged_plan_kernel<<<grid, kPlanThreads, (size_t)a.B * 16, stream>>>(a);
+  paged_plan_kernel<<<grid, kPlanThreads, (size_t)a.B * 16, stream>>>(
+      a, make_fast_div(a.block_size));
   return hipGetLastError();
 }
 

@@ -374,6 +374,29 @@ def test_attention(lens, Hq, H, D, bs, dtype):
     check_attention(a, "listed blocks in a window", sel=sel, window=max(max(lens) // 3, 1))
 
 
+def test_large_batches():
+    """More requests than a wave has lanes, many of them empty: the shares of
+    the workgroups begin anywhere in them."""
+    rng = np.random.default_rng(8)
+    for B, H, G, D, bs in [(2048, 1, 2, 64, 4), (1500, 4, 1, 64, 8), (65, 2, 3, 128, 16)]:
+        lens = rng.integers(0, 40, B) * (rng.random(B) < 0.7)
+        lens[-1] = 700
+        a = make_attention(B, list(lens), H * G, H, D, bs, torch.bfloat16)
+        say(f"batch of {B}")
+        check_attention(a, f"batch of {B}")
+        kb = torch.zeros(a["k"].shape[0], H, 2, D, dtype=torch.bfloat16)
+        kb[:, :, 0], kb[:, :, 1] = a["k"].float().amin(1), a["k"].float().amax(1)
+        check_select(a["q"], kb, bs, a["table"], lens, 3, 1, 1, f"batch of {B}")
+
+
+def test_one_request_over_all_workgroups():
+    """A single row of work (one key head) split into as many parts as there
+    are workgroups, and one with a group of query heads above a tile."""
+    for Hq, H, D, bs in [(4, 1, 64, 16), (33, 1, 64, 16), (2, 2, 128, 64)]:
+        a = make_attention(3, [40000], Hq, H, D, bs, torch.bfloat16)
+        check_attention(a, f"Hq={Hq} H={H}")
+
+
 def test_attention_bad_tables_and_lengths():
     lens = [300, 200, 150, 10 ** 6, -4]
     a = make_attention(1, lens, 8, 2, 128, 16, torch.bfloat16, mb=20)
