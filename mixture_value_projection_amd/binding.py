@@ -527,13 +527,6 @@ class PagedPlan(NamedTuple):
     free_count: torch.Tensor    # int32 [1]
 
 
-def _out(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype, shape, device)
-    return t
-
-
 _NO_SIZE = ctypes.c_size_t(-1).value
 
 
@@ -614,18 +607,29 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_
         raise ValueError("T must not be negative")
     if seq_lens is None:
         seq_lens = torch.empty_like(cached_lens)
+    else:
+        _check(seq_lens, "seq_lens", i32, (B,), dev)
+    if cu_new is None:
+        cu_new = cached_lens.new_empty(B + 1)
+    else:
+        _check(cu_new, "cu_new", i32, (B + 1,), dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
+    else:
+        _check(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
+    if positions is None:
+        positions = cached_lens.new_empty(T)
+    else:
+        _check(positions, "positions", i32, (T,), dev)
     if free_count_out is None:
         free_count_out = torch.empty_like(free_count)
-    plan = PagedPlan(_out(seq_lens, "seq_lens", i32, (B,), dev),
-                     _out(cu_new, "cu_new", i32, (B + 1,), dev),
-                     _out(slot_mapping, "slot_mapping", torch.int64, (T,), dev),
-                     _out(positions, "positions", i32, (T,), dev),
-                     _out(free_count_out, "free_count_out", i32, (1,), dev))
+    else:
+        _check(free_count_out, "free_count_out", i32, (1,), dev)
     _launch(lib.mova_paged_plan, "mova_paged_plan", dev, _ptr(cached_lens), _ptr(new_lens), B, T,
             block_size, mb, _ptr(block_table), _ptr(free_blocks), cap, _ptr(free_count),
-            _ptr(plan.free_count), _ptr(plan.seq_lens), _ptr(plan.cu_new),
-            _ptr(plan.slot_mapping), _ptr(plan.positions))
-    return plan
+            _ptr(free_count_out), _ptr(seq_lens), _ptr(cu_new), _ptr(slot_mapping),
+            _ptr(positions))
+    return PagedPlan(seq_lens, cu_new, slot_mapping, positions, free_count_out)
 
 
 def _check_pool(pool: torch.Tensor, name: str, shape, device) -> int:
@@ -696,7 +700,10 @@ def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
     _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
     nbytes = _select_bytes(B, Hq, H, D, mb, block_size, keep)
     workspace = _scratch(workspace, nbytes, "mova_block_select", dev)
-    sel_blocks = _out(sel_blocks, "sel_blocks", torch.int32, (B, H, keep), dev)
+    if sel_blocks is None:
+        sel_blocks = block_table.new_empty((B, H, keep))
+    else:
+        _check(sel_blocks, "sel_blocks", torch.int32, (B, H, keep), dev)
     _launch(lib.mova_block_select, "mova_block_select", dev, _ptr(q), _ptr(k_bounds), nb,
             block_size, _ptr(block_table), mb, _ptr(seq_lens), B, Hq, H, D, keep, keep_first,
             keep_last, _ptr(sel_blocks), _ptr(workspace),
