@@ -376,22 +376,23 @@ int mova_ffn_moe_forward(const void* x, const void* router_w, const float* route
  *   k_cache, v_cache  [num_blocks, block_size, n_kv_heads, head_dim], bf16 or
  *                     8-bit e4m3 (cache_dtype); slot s is row s % block_size
  *                     of block s / block_size
- *   k_scale, v_scale  float [n_kv_heads]: an 8-bit element e of key head h
- *                     stands for e * scale[h]; NULL = 1.  Must be NULL for
- *                     bf16 pools.
+ *   k_scale, v_scale  float [n_kv_heads], positive: an 8-bit element e of key
+ *                     head h stands for e * scale[h]; NULL = 1.  Must be NULL
+ *                     for bf16 pools.
  *   block_table       int32 [B, max_blocks]: the pool block of each run of
  *                     block_size positions of each request, any order
  *   seq_lens          int32 [B]: tokens of each request, the newest included.
  *                     On the device, never read by the host: it counts as 0
  *                     below 0 and as max_blocks * block_size above that.
  * Table entries outside [0, num_blocks) -- e.g. -1 -- stand for blocks that
- * are not there: their keys take no part.  Entries behind a request's last
- * block are not read.  Any block_size > 0 is taken.
+ * are not there: their keys take no part.  What lies behind a request's last
+ * block does not matter.  Any block_size > 0 is taken.
  * Domain: B <= 2048, max_blocks * block_size <= 2^30; pools that are read have
  * at most 2^31 - 1 slots; head_dim 64, 128 or 256, n_heads a multiple of
  * n_kv_heads, n_kv_heads * head_dim <= 16384, n_heads * head_dim <= 131072.
  * int32 and float arrays are 4-byte aligned, slot_mapping 8-byte, tensors 16,
- * workspaces 256.  Errors as for mova_value_forward; T == 0 (store) and B == 0
+ * workspaces 256.  `stream` belongs to the current device.  Errors as for
+ * mova_value_forward; T == 0 (store) and B == 0
  * (selection, attention) return MOVA_OK and enqueue nothing.
  */
 enum mova_cache_dtype {
