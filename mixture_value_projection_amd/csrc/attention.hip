@@ -197,7 +197,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   for (long long pos = line.start; pos < line.end;) {
     while (pos >= at + (long long)n * rows_per_b) {
       at += (long long)n * rows_per_b;
-      sp = span_of(a, ++b);
+      if (++b >= a.B) return;
+      sp = span_of(a, b);
       n = tiles_of(sp);
     }
     const int row = (int)floor_div(pos - at, n);

@@ -149,7 +149,8 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
   for (long long pos = line.start; pos < line.end;) {
     while (pos >= at + (long long)tiles * groups) {
       at += (long long)tiles * groups;
-      n = blocks_of(a, ++b);
+      if (++b >= a.B) return;
+      n = blocks_of(a, b);
       tiles = tiles_of(n);
     }
     const int hgroup = (int)floor_div(pos - at, tiles);
@@ -309,7 +310,8 @@ struct TopShared {
 // Narrows [lo, hi] around the left-th largest of the keys in it, which
 // for_each(f) hands to f one after the other.  Returns the cut: keys from it
 // on are wanted, and of those equal to it the first *ties.  Both histograms
-// are clear on entry.
+// are clear on entry.  A round leaves at most 2^-11 of the range, so there are
+// at most six.
 template <class K, class ForEach>
 __device__ K narrow(TopShared& sh, K lo, K hi, int left, ForEach for_each, int* ties) {
   constexpr int kPer = kParts / kThreads;
@@ -334,6 +336,10 @@ __device__ K narrow(TopShared& sh, K lo, K hi, int left, ForEach for_each, int* 
     }
     const int inc = wave_scan(mine);
     if (lane == 63) sh.n[wave] = inc;
+    if (tid == 0) {  // ends the search should the part below not be found
+      sh.part = sh.above = 0;
+      sh.in = left;
+    }
     __syncthreads();
     int above = inc - mine;
 #pragma unroll
@@ -673,7 +679,8 @@ __global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int 
           out += sh.n[w];
           seen += sh.f[w];
         }
-        if (k > cut || (k == cut && e < ties)) sel[r + min(e, ties)] = j;
+        const int to = r + min(e, ties);
+        if ((k > cut || (k == cut && e < ties)) && to < a.keep) sel[to] = j;
       }
       for (int i = out + min(seen, ties) + tid; i < a.keep; i += kThreads) sel[i] = -1;
       return;
@@ -733,7 +740,7 @@ __global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int 
     int r = at + upto - __popc(bits);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if ((bits >> i) & 1) sel[r++] = block_of(j + 4 * lane + i);
+      if ((bits >> i) & 1 && r < a.keep) sel[r++] = block_of(j + 4 * lane + i);
     at += read_lane(upto, 63);
   }
   for (int i = out + tid; i < a.keep; i += kThreads) sel[i] = -1;

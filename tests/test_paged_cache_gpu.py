@@ -637,3 +637,40 @@ def test_two_streams_at_once():
     for i in range(2):
         for o in outs[i]:
             assert torch.equal(o.cpu(), want[i])
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured sparse steps over one workspace, replayed in turns with
+    eager calls on it between them."""
+    a = [make_attention(s, lens, 16, 4, 128, 16, torch.bfloat16)
+         for s, lens in ((1, [3000, 40, 900]), (2, [77, 2500, 0]))]
+    dev = [{k: (v.to(DEV) if torch.is_tensor(v) else v) for k, v in x.items()} for x in a]
+    tabs = [(i32(x["table"]), i32(x["lens"])) for x in a]
+    kb = []
+    for x in dev:
+        t = torch.empty(x["k"].shape[0], 4, 2, 128, dtype=torch.bfloat16, device=DEV)
+        t[:, :, 0], t[:, :, 1] = x["k"].float().amin(1), x["k"].float().amax(1)
+        kb.append(t)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+
+    def step(i, ws):
+        sel = binding.block_select(dev[i]["q"], kb[i], 16, *tabs[i], 6, workspace=ws)
+        return sel, binding.attention_paged(dev[i]["q"], dev[i]["k"], dev[i]["v"], *tabs[i],
+                                            128 ** -0.5, sel_blocks=sel, workspace=ws)
+
+    want = [[t.clone() for t in step(i, None)] for i in range(2)]
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(i, ws))
+        graphs.append(g)
+    for r in range(4):
+        for i in (0, 1, 1, 0):
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(outs[i], want[i])), (r, i)
+            step(1 - i, ws)
+            torch.cuda.synchronize()
