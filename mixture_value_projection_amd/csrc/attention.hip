@@ -16,7 +16,8 @@
 // batches and single long requests fill the chip alike and the host needs no
 // lengths.  A request whose tiles lie in one stretch is finished there; else
 // each stretch leaves its part (m, sum, unnormalised out; fp32) in the
-// workspace and attention_join_kernel adds them.
+// workspace and attention_join_kernel adds them.  Where no row can have more
+// than a few tiles the line is one of whole rows (`whole`).
 //
 // A workgroup's four waves take four key heads at the same positions (rows of
 // 4 x head_dim elements are contiguous), or stripes of the tiles when there
@@ -160,7 +161,7 @@ __device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (
 // kHeads: key heads of a workgroup; 4 / kHeads waves share a head's tiles.
 template <int D, bool kFp8, int kHeads, bool kList>
 __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts,
-                                                        FastDiv by_block) {
+                                                        FastDiv by_block, int whole) {
   using T = Tile<D, kFp8>;
   constexpr int kStripes = 4 / kHeads;
   constexpr int S = T::kStages;
@@ -183,9 +184,11 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   int* pages = (int*)(ring + T::kRing);
   int* listed = pages + S * 64;
 
+  // Units of the line that a request brings: its tiles, or its rows.
   auto tiles_of = [&](const Span& s) { return ceil_div(s.keys, T::kKeys * kStripes); };
+  auto units_of = [&](int n) { return (long long)(whole ? 1 : n) * rows_per_b; };
   Line line;
-  if (!line_begin(a.B, [&](int b) { return (long long)tiles_of(span_of(a, b)) * rows_per_b; }, s_line,
+  if (!line_begin(a.B, [&](int b) { return units_of(whole ? 0 : tiles_of(span_of(a, b))); }, s_line,
                   parts.prefix, &line))
     return;
 
@@ -195,16 +198,16 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   Span sp = span_of(a, b);
   int n = tiles_of(sp);
   for (long long pos = line.start; pos < line.end;) {
-    while (pos >= at + (long long)n * rows_per_b) {
-      at += (long long)n * rows_per_b;
+    while (pos >= at + units_of(n)) {
+      at += units_of(n);
       if (++b >= a.B) return;
       sp = span_of(a, b);
       n = tiles_of(sp);
     }
-    const int row = (int)floor_div(pos - at, n);
-    const int t0 = (int)(pos - at - (long long)row * n);
-    const int t1 = (int)min((long long)n, t0 + (line.end - pos));
-    pos += t1 - t0;
+    const int row = whole ? (int)(pos - at) : (int)floor_div(pos - at, n);
+    const int t0 = whole ? 0 : (int)(pos - at - (long long)row * n);
+    const int t1 = whole ? n : (int)min((long long)n, t0 + (line.end - pos));
+    pos += whole ? 1 : t1 - t0;
     const int hgroup = row / qtiles, qt = row - hgroup * qtiles;
     const int h = hgroup * kHeads + hsub;
     const int nt = t1 - t0;
@@ -669,14 +672,26 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   });
   if (e != hipSuccess) return e;
   const Parts parts = parts_of(a);
+  // Few tiles a row at most (short contexts, windows, short lists): every row
+  // is one workgroup's, and there is nothing to join.  A workgroup alone takes
+  // 0.9 us a tile, splitting and joining 4 to 5 us in all, and the more rows
+  // there are the less a split is for.  32 query heads over 8 of 128, split
+  // and whole: 1 request of 64 tokens 8.8 and 7.9 us, of 128 9.0 and 11.4; 16 of
+  // 32..96 about 9.7 and 10; 64 of up to 192 16.9 and 15.9, of up to 256 18.7
+  // and 19.7; 256 of up to 512 72.6 and 62.7.
+  const int tile_keys = T::kKeys * (4 / kHeads);
+  long long keys = (long long)(kList ? a.keep : a.max_blocks) * a.block_size;
+  if (!kList && a.window > 0) keys = std::min<long long>(keys, a.window);
+  const long long rows = (long long)a.B * (a.H / kHeads) * ceil_div(a.Hq / a.H, 16);
+  const int whole = keys <= std::min(4 + rows / 16, 32ll) * tile_keys;
   attention_kernel<D, kFp8, kHeads, kList>
-      <<<T::kPerCu * kCus, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size));
+      <<<T::kPerCu * kCus, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size), whole);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || whole) return e;
   // Few heads in the batch: a workgroup each, since they may have many parts.
   const int at_once = (long long)a.B * a.Hq >= 1024 ? 4 : 1;
   attention_join_kernel<D><<<dim3(ceil_div(a.Hq, at_once), a.B), 256, 0, stream>>>(
-      a, parts, kHeads, T::kKeys * (4 / kHeads), at_once);
+      a, parts, kHeads, tile_keys, at_once);
   return hipGetLastError();
 }
 

@@ -389,6 +389,26 @@ def test_large_batches():
         check_select(a["q"], kb, bs, a["table"], lens, 3, 1, 1, f"batch of {B}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("B,Hq,H,D,bs,longest", [
+    (1, 8, 8, 128, 16, 64), (3, 12, 3, 64, 16, 500), (70, 8, 4, 128, 16, 120), (70, 8, 4, 128, 16, 160),
+    (300, 4, 2, 64, 8, 900), (5, 40, 2, 256, 16, 90)])
+def test_rows_split_or_whole(B, Hq, H, D, bs, longest, dtype):
+    """Batches on either side of where rows stop being split: by the table's
+    width, by a window and by the list's length; the same keys in a wider
+    table give the same result to rounding."""
+    rng = np.random.default_rng(B + longest)
+    lens = rng.integers(0, longest + 1, B)
+    lens[0] = longest
+    a = make_attention(B, list(lens), Hq, H, D, bs, dtype)
+    check_attention(a, "narrow table")
+    wide = dict(a, table=np.concatenate([a["table"], np.full((B, 4000), -1)], axis=1))
+    check_attention(wide, "wide table")
+    check_attention(wide, "window", window=min(40, longest))
+    sel = rng.integers(-1, R.ceil_div(longest, bs) + 1, (B, H, 2))
+    check_attention(wide, "short lists", sel=sel)
+
+
 def test_one_request_over_all_workgroups():
     """A single row of work (one key head) split into as many parts as there
     are workgroups, and one with a group of query heads above a tile."""
