@@ -79,6 +79,10 @@ struct Tile {
   static constexpr int kRing = 32768 / kPerCu;
   static constexpr int kStages = kRing / (2 * kSide);
   static constexpr int kLds = kRing + 2 * kStages * 256;        // with the block numbers
+  // The non-temporal hint, where a row fills a 128-byte cache line (64 requests:
+  // 144 -> 127 us); two heads' waves share the line of a shorter row, and the
+  // hint would have it read twice (64 wide with 8 bits: 44 us without, 53 with).
+  static constexpr bool kStream = kRow >= 128;
   static_assert(kStages >= 2 && kChunks <= 32 && kRowsPerLoad >= 2, "tile shape");
   // Piece c of row r lies at piece c ^ swizzle(r), so that the 8 rows of one
   // phase of the key fragments' reads, and the rows that 16 lanes of a
@@ -261,9 +265,10 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
         const size_t off = (size_t)(uint32_t)__shfl(slot, rr) * row_bytes + (size_t)h * T::kRow;
         const int c = lane % T::kChunks;
-        stream_to_lds((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16, stage + i * 1024);
-        stream_to_lds((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
-                      stage + T::kSide + i * 1024);
+        piece_to_lds<T::kStream>((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16,
+                                 stage + i * 1024);
+        piece_to_lds<T::kStream>((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
+                                 stage + T::kSide + i * 1024);
       }
       word_to_lds(table_address(block_of(x + S, next_list)), pages + (x & (S - 1)) * 64);
       if constexpr (kList) word_to_lds(list_address(x + 2 * S), listed + (x & (S - 1)) * 64);

@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
       for (int i = 0; i < T::kLoads; ++i) {
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
         const int c = (lane % T::kChunks) ^ rr;
-        stream_to_lds((const char*)a.bounds +
+        piece_to_lds<true>((const char*)a.bounds +
                           ((size_t)(uint32_t)__shfl(row, rr) * a.H + h) * T::kRow + c * 16,
                       stage + i * 1024);
       }

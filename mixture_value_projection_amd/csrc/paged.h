@@ -283,9 +283,14 @@ __device__ __forceinline__ int request_len(const int32_t* seq_lens, int b, int m
   return min(max(seq_lens[b], 0), max_blocks * block_size);
 }
 
-// Direct-to-LDS loads of 16 and 4 bytes a lane, to consecutive places.
-__device__ __forceinline__ void stream_to_lds(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, kLdsLoadNonTemporal);
+// Direct-to-LDS loads of 16 (kStream: with the non-temporal hint) and 4 bytes a
+// lane, to consecutive places.
+template <bool kStream>
+__device__ __forceinline__ void piece_to_lds(const void* from, void* to) {
+  if constexpr (kStream)
+    __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, kLdsLoadNonTemporal);
+  else
+    __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, 0);
 }
 __device__ __forceinline__ void word_to_lds(const void* from, void* to) {
   __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 4, 0, 0);
