@@ -196,8 +196,8 @@ __global__ __launch_bounds__(256) void select_score_kernel(SelectArgs a) {
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
         const int c = (lane % T::kChunks) ^ rr;
         piece_to_lds<true>((const char*)a.bounds +
-                          ((size_t)(uint32_t)__shfl(row, rr) * a.H + h) * T::kRow + c * 16,
-                      stage + i * 1024);
+                               ((size_t)(uint32_t)__shfl(row, rr) * a.H + h) * T::kRow + c * 16,
+                           stage + i * 1024);
       }
       word_to_lds(address(x + S), fetched + (x & (S - 1)) * 64);
       return page;
