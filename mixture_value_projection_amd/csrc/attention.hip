@@ -111,8 +111,10 @@ Parts parts_of(const AttentionArgs& a) {
   return p;
 }
 
-// Keys request b reads, [lo, lo + keys) or, with a list, keep * block_size
-// listed positions.
+// Keys request b reads, [lo, lo + keys) or, with a list, those of its first
+// entries, as many as the request has blocks: all there is where each block is
+// listed once and ahead of the entries that name none.  What is listed behind
+// them belongs to the row's last tile.
 struct Span {
   int len, lo;
   int keys;
@@ -121,7 +123,8 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   Span s;
   s.len = a.num_blocks > 0 ? request_len(a.seq_lens, b, a.max_blocks, a.block_size) : 0;
   s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
-  s.keys = a.sel != nullptr ? (s.len > 0 ? a.keep * a.block_size : 0) : s.len - s.lo;
+  s.keys = a.sel != nullptr ? min(a.keep, ceil_div(s.len, a.block_size)) * a.block_size
+                            : s.len - s.lo;
   return s;
 }
 
@@ -214,7 +217,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
     pos += whole ? 1 : t1 - t0;
     const int hgroup = row / qtiles, qt = row - hgroup * qtiles;
     const int h = hgroup * kHeads + hsub;
-    const int nt = t1 - t0;
+    int nt = t1 - t0;
+    const bool all = nt == n;
     const int blocks = ceil_div(sp.len, a.block_size);
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
     const int32_t* list = kList ? a.sel + ((size_t)b * a.H + h) * a.keep : nullptr;
@@ -230,6 +234,24 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       *blk = fast_div(p, by_block);
       *r = p - *blk * a.block_size;
     };
+    if (kList && t1 == n && blocks < a.keep && n > 0) {
+      // Entries behind those of the span: most often none names a block.
+      int last = -1, l = lane;
+      loaded(l);  // no register of the main loop for what follows from it
+#pragma unroll 1
+      for (int i = blocks; i < a.keep; i += 256) {
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = list[min(i + 64 * k + l, a.keep - 1)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (const uint64_t there = __ballot(e[k] >= 0 && e[k] < blocks))
+            last = min(i + 64 * k + 63 - __clzll((long long)there), a.keep - 1);
+      }
+      if (last >= 0)
+        nt = __builtin_amdgcn_readfirstlane(
+            max(nt, ceil_div((last + 1) * a.block_size, T::kKeys * kStripes) - t0));
+    }
     auto list_address = [&](int x) {
       int blk, r;
       locate(x, &blk, &r);
@@ -323,14 +345,16 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         if (mask != kAll) {
           // Values that take no part become zeros: their weight is zero, but
           // what lies there may be infinite or NaN.
+          const uint32_t own = mask >> (lane / T::kChunks);
 #pragma unroll
           for (int i = 0; i < T::kLoads; ++i)
-            if (!((mask >> (i * T::kRowsPerLoad + lane / T::kChunks)) & 1))
+            if (!((own >> (i * T::kRowsPerLoad)) & 1))
               *reinterpret_cast<u32x4*>(stage + T::kSide + i * 1024 + lane * 16) =
                   u32x4{0u, 0u, 0u, 0u};
         }
         float p[kSub][4];
         float top = -__builtin_huge_valf();
+        const uint32_t of_lane = mask >> (4 * g4);
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
           f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -358,7 +382,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             p[t][i] = s[i] * qs;
-            if (mask != kAll && !((mask >> (16 * t + 4 * g4 + i)) & 1))
+            if (mask != kAll && !((of_lane >> (16 * t + i)) & 1))
               p[t][i] = -__builtin_huge_valf();
             top = fmaxf(top, p[t][i]);
           }
@@ -477,7 +501,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       if (stripe != 0) continue;
     }
     if (!has_row) continue;
-    if (nt == n) {
+    if (all) {
       const float f = l == 0.f ? 0.f : vs / l;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
@@ -507,17 +531,19 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 // writes the rows of requests without keys.  Workgroup (x, request) has
 // `at_once` query heads (1 or 4).  A head of few parts is one wave's work, with
 // one memory round trip and no barrier; one of many (a long request in few) is
-// the whole workgroup's.
+// several workgroups', a slice of its channels each.
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int heads,
                                                              int tile_keys, int at_once) {
   constexpr int kPer = D / 64;      // channels of a lane
   constexpr int kFew = 32, kBatch = 8;
+  constexpr int kSlice = 32;        // channels of a workgroup of a head of many parts
   constexpr int kSlots = kMaxGrid / 256;
   typedef __attribute__((__vector_size__(kPer * sizeof(float)))) float vec;
   typedef __attribute__((__vector_size__(kPer * sizeof(__bf16)))) __bf16 half_vec;
+  typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
   __shared__ float s_e[kMaxGrid], s_m[4], s_l[4];
-  __shared__ vec s_o[4][64];
+  __shared__ f32x4 s_o[4][8];
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = ceil_div(span_of(a, b).keys, tile_keys);
@@ -525,17 +551,22 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   const int G = a.Hq / a.H;
   const int qtiles = ceil_div(G, 16), cap = min(G, 16);
 
+  auto scale_of = [&](int hq, float sum) {
+    return (a.v_scale != nullptr ? a.v_scale[hq / G] : 1.f) / sum;
+  };
+  auto write_lse = [&](int hq, float sum, float safe) {
+    if (a.lse != nullptr)
+      a.lse[(size_t)b * a.Hq + hq] =
+          sum == 0.f ? -__builtin_huge_valf()
+                     : (safe + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  };
   auto finish = [&](int hq, vec o, float sum, float safe) {
-    const size_t row = (size_t)b * a.Hq + hq;
-    const float vs = a.v_scale != nullptr ? a.v_scale[hq / G] : 1.f;
-    const float f = sum == 0.f ? 0.f : vs / sum;
+    const float f = scale_of(hq, sum);
     half_vec y;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) y[j] = (__bf16)(sum == 0.f ? 0.f : o[j] * f);
-    *reinterpret_cast<half_vec*>(a.out + row * D + kPer * lane) = y;
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[row] = sum == 0.f ? -__builtin_huge_valf()
-                              : (safe + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+    *reinterpret_cast<half_vec*>(a.out + ((size_t)b * a.Hq + hq) * D + kPer * lane) = y;
+    if (lane == 0) write_lse(hq, sum, safe);
   };
   // First part of the head, and how many there are.
   auto parts_at = [&](int hq, int* w0) {
@@ -550,7 +581,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   };
   auto larger = [](float p, float q) { return fmaxf(p, q); };
 
-  {
+  if (blockIdx.z == 0) {
     const int hq = blockIdx.x * at_once + wave;
     int w0;
     const int np = wave < at_once && hq < a.Hq ? parts_at(hq, &w0) : 1;
@@ -607,14 +638,17 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
       }
       M = fmaxf(M, m[k]);
     }
-    vec x[kBatch], o = {};
-    auto load = [&](int i0) {
+    // A wave's load is a slice of eight parts.
+    const int sub = 8 * wave + lane / 8;
+    f32x4 x[kBatch];
+    auto load = [&](int c, int i0) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (i0 + 4 * k < np)
-          x[k] = *reinterpret_cast<const vec*>(parts.o + part_of(hq, w0, i0 + 4 * k) * D + kPer * lane);
+        if (i0 + 32 * k + sub < np)
+          x[k] = *reinterpret_cast<const f32x4*>(
+              parts.o + part_of(hq, w0, i0 + 32 * k + sub) * D + c + 4 * (lane & 7));
     };
-    load(wave);
+    load(kSlice * blockIdx.z, 0);
     M = wave_reduce(M, larger);
     if (lane == 0) s_m[wave] = M;
     __syncthreads();
@@ -631,28 +665,36 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     sum = wave_sum(sum);
     if (lane == 0) s_l[wave] = sum;
     __syncthreads();
-    for (int i0 = wave; i0 < np; i0 += 4 * kBatch) {
-      if (i0 != wave) load(i0);
+    sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    for (int c = kSlice * blockIdx.z; c < D; c += kSlice * gridDim.z) {
+      f32x4 o = {};
+      for (int i0 = 0; i0 < np; i0 += 32 * kBatch) {
+        if (i0 != 0 || c != (int)(kSlice * blockIdx.z)) load(c, i0);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (i0 + 4 * k < np) {
-          const float f = s_e[i0 + 4 * k];
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + 32 * k + sub < np) {
+            const float f = s_e[i0 + 32 * k + sub];
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) o[j] += x[k][j] * f;
-        }
-    }
-    s_o[wave][lane] = o;
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const vec y = s_o[w][lane];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] += y[j];
+            for (int j = 0; j < 4; ++j) o[j] += x[k][j] * f;
+          }
       }
-      finish(hq, o, (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), safe);
+#pragma unroll
+      for (int step = 8; step < 64; step *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], step);
+      if (lane < 8) s_o[wave][lane] = o;
+      __syncthreads();
+      if (tid < 8) {
+        o = (s_o[0][tid] + s_o[1][tid]) + (s_o[2][tid] + s_o[3][tid]);
+        const float f = scale_of(hq, sum);
+        bf16x4 y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = (__bf16)(sum == 0.f ? 0.f : o[j] * f);
+        *reinterpret_cast<bf16x4*>(a.out + ((size_t)b * a.Hq + hq) * D + c + 4 * tid) = y;
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (tid == 0 && blockIdx.z == 0) write_lse(hq, sum, safe);
   }
 }
 
@@ -685,7 +727,7 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   // 32..96 about 9.7 and 10; 64 of up to 192 16.9 and 15.9, of up to 256 18.7
   // and 19.7; 256 of up to 512 72.6 and 62.7.
   const int tile_keys = T::kKeys * (4 / kHeads);
-  long long keys = (long long)(kList ? a.keep : a.max_blocks) * a.block_size;
+  long long keys = (long long)(kList ? std::min(a.keep, a.max_blocks) : a.max_blocks) * a.block_size;
   if (!kList && a.window > 0) keys = std::min<long long>(keys, a.window);
   const long long rows = (long long)a.B * (a.H / kHeads) * ceil_div(a.Hq / a.H, 16);
   const int whole = keys <= std::min(4 + rows / 16, 32ll) * tile_keys;
@@ -693,9 +735,12 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
       <<<T::kPerCu * kCus, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size), whole);
   e = hipGetLastError();
   if (e != hipSuccess || whole) return e;
-  // Few heads in the batch: a workgroup each, since they may have many parts.
-  const int at_once = (long long)a.B * a.Hq >= 1024 ? 4 : 1;
-  attention_join_kernel<D><<<dim3(ceil_div(a.Hq, at_once), a.B), 256, 0, stream>>>(
+  // Few heads in the batch may have many parts each: a workgroup a head, and
+  // as many as keep the launch short a slice.
+  const int heads = a.B * a.Hq;
+  const int at_once = heads >= 1024 ? 4 : 1;
+  const int slices = std::clamp(1024 / heads, 1, D / 32);
+  attention_join_kernel<D><<<dim3(ceil_div(a.Hq, at_once), a.B, slices), 256, 0, stream>>>(
       a, parts, kHeads, tile_keys, at_once);
   return hipGetLastError();
 }

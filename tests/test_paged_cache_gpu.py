@@ -417,6 +417,55 @@ def test_one_request_over_all_workgroups():
         check_attention(a, f"Hq={Hq} H={H}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("lens,Hq,H,D,bs", [
+    ([20000], 6, 2, 256, 32), ([9000, 5], 8, 8, 64, 16), ([14000], 5, 1, 128, 16),
+    ([12, 30000] + [7] * 62, 32, 8, 128, 16)])
+def test_rows_of_many_parts(lens, Hq, H, D, bs, dtype):
+    """Long requests by themselves, where several workgroups join a head, and
+    one among so many heads that a workgroup joins four."""
+    say(f"many parts {lens[:4]} D={D} {dtype}")
+    check_attention(make_attention(D + len(lens), lens, Hq, H, D, bs, dtype), "many parts")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("lens,Hq,H,D,bs,keep", [
+    ([100, 1, 0, 37], 8, 4, 128, 16, 90), ([700, 64, 3], 6, 3, 64, 8, 600),
+    ([500, 20], 20, 1, 128, 32, 70), ([130, 90, 257], 8, 2, 256, 64, 300),
+    ([40] * 80, 4, 4, 64, 16, 20)])
+def test_lists_longer_than_the_request(lens, Hq, H, D, bs, keep, dtype):
+    """Lists with more entries than the request has blocks: each block once and
+    nothing behind, the same from the list's end, a single block as the last
+    entry or somewhere between, blocks listed again and again, and nothing."""
+    rng = np.random.default_rng(keep)
+    B = len(lens)
+    a = make_attention(keep, lens, Hq, H, D, bs, dtype)
+    blocks = [R.ceil_div(n, bs) for n in lens]
+
+    def lists(fill):
+        sel = np.full((B, H, keep), -1)
+        for b, n in enumerate(blocks):
+            for h in range(H if n else 0):
+                fill(sel[b, h], n)
+        return sel
+
+    def at(row, where, what):
+        row[where] = what
+
+    cases = {
+        "front": lists(lambda row, n: at(row, slice(0, n), rng.permutation(n))),
+        "end": lists(lambda row, n: at(row, slice(keep - n, keep), rng.permutation(n))),
+        "last": lists(lambda row, n: at(row, keep - 1, rng.integers(n))),
+        "between": lists(lambda row, n: at(row, rng.integers(keep), rng.integers(n))),
+        "again": lists(lambda row, n: at(row, slice(0, keep), rng.integers(0, n, keep))),
+        "nothing": lists(lambda row, n: None),
+    }
+    for what, sel in cases.items():
+        say(f"lists of {keep}, {what}")
+        check_attention(a, what, sel=sel)
+        check_attention(a, what + " in a window", sel=sel, window=30)
+
+
 def test_attention_bad_tables_and_lengths():
     lens = [300, 200, 150, 10 ** 6, -4]
     a = make_attention(1, lens, 8, 2, 128, 16, torch.bfloat16, mb=20)
