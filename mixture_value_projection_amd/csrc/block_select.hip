@@ -365,29 +365,44 @@ __device__ K narrow(TopShared& sh, K lo, K hi, int left, ForEach for_each, int* 
   }
 }
 
-// 64-bit score of a block, in each of 16 lanes that work on it.
+// Lanes that work on a block's 64-bit score: 16 a query head, and four heads at
+// a time where the group has them.
+__device__ __forceinline__ int exact_lanes(int G) { return G >= 4 ? 64 : 16; }
+
+// 64-bit score of a block, in all of the exact_lanes(G) lanes that work on it;
+// l is the number of the lane among them.  What two heads of a lane need is
+// asked for together.
 __device__ __forceinline__ double exact_score(const SelectArgs& a, int b, int h, int page, int l) {
+  typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
   const int G = a.Hq / a.H;
+  const int step = exact_lanes(G) / 16;
   const __bf16* lo = a.bounds + ((size_t)page * a.H + h) * 2 * a.D;
+  const __bf16* q = a.q + ((size_t)b * a.Hq + h * G) * a.D;
   double best = -__builtin_huge_val();
-  for (int g = 0; g < G; ++g) {
-    const __bf16* q = a.q + ((size_t)b * a.Hq + h * G + g) * a.D;
-    double s = 0;
-    for (int d = 4 * l; d < a.D; d += 64) {
-      typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
-      const bf16x4 qv = *(const bf16x4*)(q + d), lv = *(const bf16x4*)(lo + d),
-                   hv = *(const bf16x4*)(lo + a.D + d);
+  for (int g = l / 16; g < G; g += 2 * step) {
+    const __bf16 *q0 = q + (size_t)g * a.D, *q1 = q + (size_t)min(g + step, G - 1) * a.D;
+    double s0 = 0, s1 = 0;
+    for (int d = 4 * (l & 15); d < a.D; d += 64) {
+      const bf16x4 lv = *(const bf16x4*)(lo + d), hv = *(const bf16x4*)(lo + a.D + d),
+                   v0 = *(const bf16x4*)(q0 + d), v1 = *(const bf16x4*)(q1 + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const double x = (double)(float)qv[i];
-        s += (double)(x > 0 ? (float)hv[i] : (float)lv[i]) * x;
+        const double x0 = (double)(float)v0[i], x1 = (double)(float)v1[i];
+        s0 += (double)(x0 > 0 ? (float)hv[i] : (float)lv[i]) * x0;
+        s1 += (double)(x1 > 0 ? (float)hv[i] : (float)lv[i]) * x1;
       }
     }
-    s += dpp_or_0<0xB1>(s);   // quad_perm 1 0 3 2, 2 3 0 1, row_half_mirror, row_mirror
-    s += dpp_or_0<0x4E>(s);
-    s += dpp_or_0<0x141>(s);
-    s += dpp_or_0<0x140>(s);
-    if (s > best) best = s;  // a NaN does not count
+    // quad_perm 1 0 3 2, 2 3 0 1, row_half_mirror, row_mirror
+    s0 += dpp_or_0<0xB1>(s0), s1 += dpp_or_0<0xB1>(s1);
+    s0 += dpp_or_0<0x4E>(s0), s1 += dpp_or_0<0x4E>(s1);
+    s0 += dpp_or_0<0x141>(s0), s1 += dpp_or_0<0x141>(s1);
+    s0 += dpp_or_0<0x140>(s0), s1 += dpp_or_0<0x140>(s1);
+    if (s0 > best) best = s0;  // a NaN does not count
+    if (s1 > best) best = s1;
+  }
+  if (step == 4) {
+    best = fmax(best, __shfl_xor(best, 16));
+    best = fmax(best, __shfl_xor(best, 32));
   }
   return best;
 }
@@ -600,8 +615,9 @@ __global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int 
   auto open = [&](uint32_t l, uint32_t u) { return u >= reach && l <= rival; };
 
   if (rival != 0) {
-    // Undecided blocks: listed in LDS, computed by 16 lanes each, and chosen by
+    // Undecided blocks: listed in LDS, computed in 64 bits, and chosen by
     // counting the better ones.
+    const int lanes = exact_lanes(a.Hq / a.H), sub = tid & (lanes - 1);
     int in = 0;
     for (int i = tid; i < min(ceil_div(m, 32), kMaxMarked / 32); i += kThreads) sh.chosen[i] = 0;
 #pragma unroll 1
@@ -624,12 +640,12 @@ __global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int 
       // Too many (equal scores, very long lists): 64-bit keys of all that may
       // be wanted in place of the intervals, and the same narrowing on them.
 #pragma unroll 1
-      for (int j = tid / 16; j < n; j += kThreads / 16) {
+      for (int j = tid / lanes; j < n; j += kThreads / lanes) {
         const Ends v = ends[j];
         unsigned long long k = v.lower == ~0u ? kForced : kMissing;
-        if (v.lower != ~0u && v.upper >= reach) k = order_key(exact_score(a, b, h, table[j], tid & 15));
-        // The 16 lanes run together: all have read v before one writes.
-        if ((tid & 15) == 0) scratch[j] = k;
+        if (v.lower != ~0u && v.upper >= reach) k = order_key(exact_score(a, b, h, table[j], sub));
+        // A block's lanes run together: all have read v before one writes.
+        if (sub == 0) scratch[j] = k;
       }
       __syncthreads();
       unsigned long long klo = ~0ull, khi = 0;
@@ -689,9 +705,9 @@ __global__ __launch_bounds__(kThreads) void select_top_kernel(SelectArgs a, int 
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) in += sh.n[w];
 #pragma unroll 1
-    for (int c = tid / 16; c < opened; c += kThreads / 16) {
-      const double s = exact_score(a, b, h, table[block_of(sh.block[c])], tid & 15);
-      if ((tid & 15) == 0) sh.key[c] = order_key(s);
+    for (int c = tid / lanes; c < opened; c += kThreads / lanes) {
+      const double s = exact_score(a, b, h, table[block_of(sh.block[c])], sub);
+      if (sub == 0) sh.key[c] = order_key(s);
     }
     __syncthreads();
 #pragma unroll 1
