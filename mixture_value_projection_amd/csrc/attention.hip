@@ -47,8 +47,8 @@ namespace mova {
 // tile of request b, prefix[B] the tiles of a stretch.
 struct Parts {
   long long* prefix;
-  float* ml;  // [two a workgroup][heads per group][rows][2]
-  float* o;   // [two a workgroup][heads per group][rows][D]
+  float* ml;  // [two a workgroup][tracks per group][rows][2]
+  float* o;   // [two a workgroup][tracks per group][rows][D]
 };
 
 namespace {
@@ -59,8 +59,10 @@ constexpr int kMaxGrid = 2 * kCus;  // workgroups of attention_kernel
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 
-// Waves of a workgroup on different key heads; the others split the tiles.
-int heads_per_group(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
+// A track is a key head with up to 16 of the query heads that share it.
+int tracks_of(int Hq, int H) { return H * ceil_div(Hq / H, 16); }
+// Waves of a workgroup on different tracks; the others split the tiles.
+int tracks_per_group(int tracks) { return tracks % 4 == 0 ? 4 : tracks % 2 == 0 ? 2 : 1; }
 
 template <int D, bool kFp8>
 struct Tile {
@@ -103,7 +105,7 @@ struct Tile {
 size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
 
 Parts parts_of(const AttentionArgs& a) {
-  const size_t rows = (size_t)kMaxGrid * 2 * heads_per_group(a.H) * std::min(a.Hq / a.H, 16);
+  const size_t rows = (size_t)kMaxGrid * 2 * tracks_per_group(tracks_of(a.Hq, a.H)) * std::min(a.Hq / a.H, 16);
   Parts p;
   p.prefix = (long long*)a.part;
   p.ml = a.part + prefix_floats(a.B);
@@ -179,12 +181,14 @@ __device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (
 
 }  // namespace
 
-// kHeads: key heads of a workgroup; 4 / kHeads waves share a head's tiles.
-template <int D, bool kFp8, int kHeads, bool kList>
+// kTracks: tracks of a workgroup; 4 / kTracks waves share a track's tiles.
+// kShared: tracks of one key head lie side by side and read the same rows.
+template <int D, bool kFp8, int kTracks, bool kShared, bool kList>
 __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts,
                                                         FastDiv by_block, Pad pad, int whole) {
   using T = Tile<D, kFp8>;
-  constexpr int kStripes = 4 / kHeads;
+  constexpr int kStripes = 4 / kTracks;
+  constexpr bool kStream = T::kStream && !kShared;
   constexpr int S = T::kStages;
   constexpr int kSub = T::kKeys / 16;      // 16-key parts of a tile
   constexpr int kCols = D / 16;
@@ -197,10 +201,10 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int hsub = wave / kStripes, stripe = wave % kStripes;
+  const int tsub = wave / kStripes, stripe = wave % kStripes;
   const int G = a.Hq / a.H;
   const int qtiles = ceil_div(G, 16);
-  const int rows_per_b = a.H / kHeads * qtiles;
+  const int rows_per_b = a.H * qtiles / kTracks;
   char* ring = lds + wave * T::kLds;
   int* pages = (int*)(ring + T::kRing);
   int* listed = pages + S * 64;
@@ -233,8 +237,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
     const int t1 = whole ? n : min(n, t0 + share);
     pos += whole ? 1 : share;
     if (kList && !whole && t0 >= n) continue;  // the padding of a row
-    const int hgroup = row / qtiles, qt = row - hgroup * qtiles;
-    const int h = hgroup * kHeads + hsub;
+    const int track = row * kTracks + tsub;
+    const int h = track / qtiles, qt = track - h * qtiles;
     int nt = t1 - t0;
     const bool all = nt == n;
     const int blocks = ceil_div(sp.len, a.block_size);
@@ -305,9 +309,9 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
         const size_t off = (size_t)(uint32_t)__shfl(slot, rr) * row_bytes + (size_t)h * T::kRow;
         const int c = lane % T::kChunks;
-        piece_to_lds<T::kStream>((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16,
+        piece_to_lds<kStream>((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16,
                                  stage + i * 1024);
-        piece_to_lds<T::kStream>((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
+        piece_to_lds<kStream>((const char*)a.v_cache + off + (c ^ T::swizzle_v(rr)) * 16,
                                  stage + T::kSide + i * 1024);
       }
       word_to_lds(table_address(block_of(x + S, next_list)), pages + (x & (S - 1)) * 64);
@@ -363,10 +367,9 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         if (mask != kAll) {
           // Values that take no part become zeros: their weight is zero, but
           // what lies there may be infinite or NaN.
-          const uint32_t own = mask >> (lane / T::kChunks);
 #pragma unroll
           for (int i = 0; i < T::kLoads; ++i)
-            if (!((own >> (i * T::kRowsPerLoad)) & 1))
+            if (!((mask >> (i * T::kRowsPerLoad + lane / T::kChunks)) & 1))
               *reinterpret_cast<u32x4*>(stage + T::kSide + i * 1024 + lane * 16) =
                   u32x4{0u, 0u, 0u, 0u};
         }
@@ -533,7 +536,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
                                : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
     } else {
       const int cap = min(G, 16);
-      const size_t part = ((size_t)(blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kHeads + hsub) * cap + r16;
+      const size_t part = ((size_t)(blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kTracks + tsub) * cap + r16;
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
         *reinterpret_cast<f32x4*>(parts.o + part * D + 16 * c + 4 * g4) = o[c];
@@ -547,14 +550,16 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 
 // Adds the parts of a request's query heads that were split over stretches, and
 // writes the rows of requests without keys.  Workgroup (x, request) has
-// `at_once` query heads (1 or 4).  A head of few parts is one wave's work, with
+// kAtOnce query heads (1 or 4).  A head of few parts is one wave's work, with
 // one memory round trip and no barrier; one of many (a long request in few) is
 // several workgroups', a slice of its channels each.
-template <int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int heads,
-                                                             int tile_keys, Pad pad, int at_once) {
+template <int D, int kAtOnce>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int tracks,
+                                                             int tile_keys, Pad pad) {
   constexpr int kPer = D / 64;      // channels of a lane
   constexpr int kFew = 32, kBatch = 8;
+  // (Four heads a workgroup: rarely many parts, and registers are waves at once.)
+  constexpr int kManyBatch = kAtOnce == 1 ? 8 : 1;
   constexpr int kSlice = 32;        // channels of a workgroup of a head of many parts
   constexpr int kSlots = kMaxGrid / 256;
   typedef __attribute__((__vector_size__(kPer * sizeof(float)))) float vec;
@@ -590,20 +595,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   // First part of the head, and how many there are.
   auto parts_at = [&](int hq, int* w0) {
     const int h = hq / G, gi = hq - h * G;
-    const long long first = before + (long long)(h / heads * qtiles + gi / 16) * units;
+    const long long first = before + (long long)((h * qtiles + gi / 16) / tracks) * units;
     *w0 = (int)floor_div(first, stretch);
     return n == 0 ? 0 : min((int)floor_div(first + n - 1, stretch), kMaxGrid - 1) - *w0 + 1;
   };
   auto part_of = [&](int hq, int w0, int i) {
     const int h = hq / G, gi = hq - h * G;
-    return ((size_t)((w0 + i) * 2 + (i == 0 ? 1 : 0)) * heads + h % heads) * cap + gi % 16;
+    return ((size_t)((w0 + i) * 2 + (i == 0 ? 1 : 0)) * tracks + (h * qtiles + gi / 16) % tracks) * cap +
+           gi % 16;
   };
   auto larger = [](float p, float q) { return fmaxf(p, q); };
 
   if (blockIdx.z == 0) {
-    const int hq = blockIdx.x * at_once + wave;
+    const int hq = blockIdx.x * kAtOnce + wave;
     int w0;
-    const int np = wave < at_once && hq < a.Hq ? parts_at(hq, &w0) : 1;
+    const int np = wave < kAtOnce && hq < a.Hq ? parts_at(hq, &w0) : 1;
     if (np == 0) finish(hq, vec{}, 0.f, 0.f);
     if (np > 1 && np <= kFew) {
       // Everything is asked for before the first wait.
@@ -639,8 +645,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     }
   }
 
-  for (int t = 0; t < at_once; ++t) {
-    const int hq = blockIdx.x * at_once + t;
+  for (int t = 0; t < kAtOnce; ++t) {
+    const int hq = blockIdx.x * kAtOnce + t;
     int w0 = 0;
     const int np = hq < a.Hq ? parts_at(hq, &w0) : 0;  // at most kMaxGrid
     if (np <= kFew) continue;
@@ -659,10 +665,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     }
     // A wave's load is a slice of eight parts.
     const int sub = 8 * wave + lane / 8;
-    f32x4 x[kBatch];
+    f32x4 x[kManyBatch];
     auto load = [&](int c, int i0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
+      for (int k = 0; k < kManyBatch; ++k)
         if (i0 + 32 * k + sub < np)
           x[k] = *reinterpret_cast<const f32x4*>(
               parts.o + part_of(hq, w0, i0 + 32 * k + sub) * D + c + 4 * (lane & 7));
@@ -687,10 +693,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
     sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
     for (int c = kSlice * blockIdx.z; c < D; c += kSlice * gridDim.z) {
       f32x4 o = {};
-      for (int i0 = 0; i0 < np; i0 += 32 * kBatch) {
+      for (int i0 = 0; i0 < np; i0 += 32 * kManyBatch) {
         if (i0 != 0 || c != (int)(kSlice * blockIdx.z)) load(c, i0);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
+        for (int k = 0; k < kManyBatch; ++k)
           if (i0 + 32 * k + sub < np) {
             const float f = s_e[i0 + 32 * k + sub];
 #pragma unroll
@@ -721,19 +727,19 @@ size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int
                                 int keep) {
   (void)max_blocks; (void)block_size; (void)keep;
   if (B == 0) return 0;
-  const size_t rows = (size_t)kMaxGrid * 2 * heads_per_group(H) * std::min(Hq / H, 16);
+  const size_t rows = (size_t)kMaxGrid * 2 * tracks_per_group(tracks_of(Hq, H)) * std::min(Hq / H, 16);
   return prefix_floats(B) + (rows * 2 + 63) / 64 * 64 + rows * D;
 }
 
 namespace {
 
-template <int D, bool kFp8, int kHeads, bool kList>
+template <int D, bool kFp8, int kTracks, bool kShared, bool kList>
 hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   using T = Tile<D, kFp8>;
   static std::atomic<unsigned long long> done{0};
   hipError_t e = once_per_device(done, [&] {
     return hipFuncSetAttribute(
-        reinterpret_cast<const void*>(attention_kernel<D, kFp8, kHeads, kList>),
+        reinterpret_cast<const void*>(attention_kernel<D, kFp8, kTracks, kShared, kList>),
         hipFuncAttributeMaxDynamicSharedMemorySize, 4 * T::kLds);
   });
   if (e != hipSuccess) return e;
@@ -745,10 +751,10 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   // and whole: 1 request of 64 tokens 8.8 and 7.9 us, of 128 9.0 and 11.4; 16 of
   // 32..96 about 9.7 and 10; 64 of up to 192 16.9 and 15.9, of up to 256 18.7
   // and 19.7; 256 of up to 512 72.6 and 62.7.
-  const int tile_keys = T::kKeys * (4 / kHeads);
+  const int tile_keys = T::kKeys * (4 / kTracks);
   long long keys = (long long)(kList ? std::min(a.keep, a.max_blocks) : a.max_blocks) * a.block_size;
   if (!kList && a.window > 0) keys = std::min<long long>(keys, a.window);
-  const long long rows = (long long)a.B * (a.H / kHeads) * ceil_div(a.Hq / a.H, 16);
+  const long long rows = (long long)a.B * (tracks_of(a.Hq, a.H) / kTracks);
   const int whole = keys <= std::min(4 + rows / 16, 32ll) * tile_keys;
   const int grid = T::kPerCu * kCus;
   Pad pad = {};
@@ -757,27 +763,38 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
     pad.to = (int)std::min<long long>((rows * pad.most + grid - 1) / grid, pad.most);
     pad.by = make_fast_div(pad.to);
   }
-  attention_kernel<D, kFp8, kHeads, kList><<<grid, 256, 4 * T::kLds, stream>>>(
+  attention_kernel<D, kFp8, kTracks, kShared, kList><<<grid, 256, 4 * T::kLds, stream>>>(
       a, parts, make_fast_div(a.block_size), pad, whole);
   e = hipGetLastError();
   if (e != hipSuccess || whole) return e;
   // Few heads in the batch may have many parts each: a workgroup a head, and
   // as many as keep the launch short a slice.
   const int heads = a.B * a.Hq;
-  const int at_once = heads >= 1024 ? 4 : 1;
-  const int slices = std::clamp(1024 / heads, 1, D / 32);
-  attention_join_kernel<D><<<dim3(ceil_div(a.Hq, at_once), a.B, slices), 256, 0, stream>>>(
-      a, parts, kHeads, tile_keys, pad, at_once);
+  if (heads >= 1024) {
+    attention_join_kernel<D, 4><<<dim3(ceil_div(a.Hq, 4), a.B), 256, 0, stream>>>(
+        a, parts, kTracks, tile_keys, pad);
+  } else {
+    const int slices = std::clamp(1024 / heads, 1, D / 32);
+    attention_join_kernel<D, 1><<<dim3(a.Hq, a.B, slices), 256, 0, stream>>>(a, parts, kTracks,
+                                                                            tile_keys, pad);
+  }
   return hipGetLastError();
 }
 
+template <int D, bool kFp8, int kTracks, bool kShared>
+hipError_t launch_list(const AttentionArgs& a, hipStream_t stream) {
+  return a.sel != nullptr ? launch_cfg<D, kFp8, kTracks, kShared, true>(a, stream)
+                          : launch_cfg<D, kFp8, kTracks, kShared, false>(a, stream);
+}
+
 template <int D, bool kFp8>
-hipError_t launch_heads(const AttentionArgs& a, hipStream_t stream) {
-  const bool list = a.sel != nullptr;
-  switch (heads_per_group(a.H)) {
-    case 4: return list ? launch_cfg<D, kFp8, 4, true>(a, stream) : launch_cfg<D, kFp8, 4, false>(a, stream);
-    case 2: return list ? launch_cfg<D, kFp8, 2, true>(a, stream) : launch_cfg<D, kFp8, 2, false>(a, stream);
-    default: return list ? launch_cfg<D, kFp8, 1, true>(a, stream) : launch_cfg<D, kFp8, 1, false>(a, stream);
+hipError_t launch_tracks(const AttentionArgs& a, hipStream_t stream) {
+  const int tracks = tracks_of(a.Hq, a.H);
+  const bool shared = tracks > a.H;
+  switch (tracks_per_group(tracks)) {
+    case 4: return shared ? launch_list<D, kFp8, 4, true>(a, stream) : launch_list<D, kFp8, 4, false>(a, stream);
+    case 2: return shared ? launch_list<D, kFp8, 2, true>(a, stream) : launch_list<D, kFp8, 2, false>(a, stream);
+    default: return launch_list<D, kFp8, 1, false>(a, stream);
   }
 }
 
@@ -786,9 +803,9 @@ hipError_t launch_heads(const AttentionArgs& a, hipStream_t stream) {
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream) {
   const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
-    case 64: return fp8 ? launch_heads<64, true>(a, stream) : launch_heads<64, false>(a, stream);
-    case 128: return fp8 ? launch_heads<128, true>(a, stream) : launch_heads<128, false>(a, stream);
-    case 256: return fp8 ? launch_heads<256, true>(a, stream) : launch_heads<256, false>(a, stream);
+    case 64: return fp8 ? launch_tracks<64, true>(a, stream) : launch_tracks<64, false>(a, stream);
+    case 128: return fp8 ? launch_tracks<128, true>(a, stream) : launch_tracks<128, false>(a, stream);
+    case 256: return fp8 ? launch_tracks<256, true>(a, stream) : launch_tracks<256, false>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -419,6 +419,23 @@ def test_one_request_over_all_workgroups():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("lens,Hq,H,D,bs", [
+    ([3000, 1, 0, 700], 64, 1, 128, 16), ([900, 333], 32, 1, 64, 16), ([5000], 17, 1, 256, 32),
+    ([40, 1200], 96, 2, 64, 8), ([2500, 60], 40, 1, 128, 64), ([800, 9], 99, 3, 128, 16),
+    ([700] * 9, 96, 3, 256, 16), ([30] * 5, 128, 4, 128, 16), ([100, 2000], 256, 2, 64, 24)])
+def test_wide_groups(lens, Hq, H, D, bs, dtype):
+    """Groups of more than 16 query heads: several tracks read a key head, side
+    by side in a workgroup where their number allows."""
+    say(f"wide group {lens[:3]} Hq={Hq} H={H} D={D} {dtype}")
+    a = make_attention(Hq + D, lens, Hq, H, D, bs, dtype)
+    check_attention(a, "all keys")
+    check_attention(a, "window", window=50)
+    mb = a["table"].shape[1]
+    sel = np.random.default_rng(Hq).integers(-1, mb + 1, (len(lens), H, 12))
+    check_attention(a, "listed blocks", sel=sel)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("lens,Hq,H,D,bs", [
     ([20000], 6, 2, 256, 32), ([9000, 5], 8, 8, 64, 16), ([14000], 5, 1, 128, 16),
     ([12, 30000] + [7] * 62, 32, 8, 128, 16)])
 def test_rows_of_many_parts(lens, Hq, H, D, bs, dtype):

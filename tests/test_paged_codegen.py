@@ -5,7 +5,7 @@
   for all of them stands between the products of a tile.
 * Both contract on the matrix units, attention's values through transposing
   LDS reads, and read the cache with the non-temporal hint where a row fills a
-  cache line.
+  cache line and no two waves read it.
 """
 import os
 import re
@@ -49,13 +49,14 @@ def test_rings_stay_in_flight(attention, scores):
 
 
 def test_attention_reads_values_transposed(attention):
-    assert len(attention) == 36  # head_dim x dtype x heads of a workgroup x list
+    assert len(attention) == 60  # head_dim x dtype x (tracks of a workgroup, shared) x list
     for name, ins in attention.items():
-        fp8 = re.search(r"ILi\d+ELb1E", name) is not None
+        D, fp8, shared = (int(x) for x in
+                          re.search(r"ILi(\d+)ELb([01])ELi\dELb([01])E", name).groups())
         assert any(i.startswith("ds_read_b64_tr_b8" if fp8 else "ds_read_b64_tr_b16") for i in ins)
         assert any(i.startswith("v_mfma_f32_16x16x32_bf16") for i in ins), name
         hinted = [bool(re.search(r" nt\b", i)) for i in ins if i.startswith("global_load_lds_dwordx4")]
-        assert hinted and set(hinted) == {not (fp8 and "ILi64E" in name)}, name
+        assert hinted and set(hinted) == {not shared and not (fp8 and D == 64)}, name
 
 
 def test_no_packed_fp32(attention, scores):
