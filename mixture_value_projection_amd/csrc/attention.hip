@@ -367,7 +367,8 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         if (mask != kAll) {
           // Values that take no part become zeros: their weight is zero, but
           // what lies there may be infinite or NaN.
-#pragma unroll
+          constexpr int kUnroll = T::kLoads > 4 ? 1 : T::kLoads;  // a register each
+#pragma unroll kUnroll
           for (int i = 0; i < T::kLoads; ++i)
             if (!((mask >> (i * T::kRowsPerLoad + lane / T::kChunks)) & 1))
               *reinterpret_cast<u32x4*>(stage + T::kSide + i * 1024 + lane * 16) =
