@@ -74,10 +74,10 @@ struct Tile {
   static constexpr int kLoads = kKeys / kRowsPerLoad;           // wave loads per side
   static constexpr int kSide = kKeys * kRow;                    // bytes of a side (K or V)
   // Two workgroups a CU with 16 KB of keys and values a wave, or one with 32:
-  // two hide each other's softmax (64 requests, 128 wide 130 -> 127 us; 64 wide
-  // with 8 bits 63 -> 54), where two tiles fit 16 KB; 8-bit tiles 128 wide are
-  // better off with four in the ring (129 against 133 us).
-  static constexpr int kPerCu = 4 * kSide <= 16384 && !(kFp8 && D == 128) ? 2 : 1;
+  // two hide each other's softmax and beginnings (64 requests, 128 wide 130 ->
+  // 127 us; 8 bits, 64 wide 63 -> 54, 3 heads of 128 41.5 -> 35.3), where two
+  // tiles fit 16 KB.
+  static constexpr int kPerCu = 4 * kSide <= 16384 ? 2 : 1;
   static constexpr int kRing = 32768 / kPerCu;
   static constexpr int kStages = kRing / (2 * kSide);
   static constexpr int kLds = kRing + 2 * kStages * 256;        // with the block numbers
@@ -156,6 +156,18 @@ __device__ __forceinline__ Frag16 widen_fp8(uint32_t w0, uint32_t w1) {
   return f;
 }
 
+// Largest of the lanes i, i + 16, i + 32 and i + 48, in all of them: exchanges of
+// rows of 16 and of halves in registers.
+__device__ __forceinline__ float max_over_groups(float x) {
+  uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto rows = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = fmaxf(__builtin_bit_cast(float, (uint32_t)rows[0]), __builtin_bit_cast(float, (uint32_t)rows[1]));
+  u = __builtin_bit_cast(uint32_t, x);
+  const auto halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)halves[0]),
+               __builtin_bit_cast(float, (uint32_t)halves[1]));
+}
+
 // Four transposing LDS reads of 8 bytes a lane (16 lanes hand out 16 columns of
 // the 128 bytes that they address) and the wait for them, in one block: as
 // builtins, each read would first wait for every direct load in flight (the
@@ -218,7 +230,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
                   parts.prefix, &line))
     return;
 
-  const size_t row_bytes = (size_t)a.H * T::kRow;
+  const uint32_t row_bytes = (uint32_t)a.H * T::kRow;
   int b = line.b;
   long long at = line.first;  // first tile of request b
   Span sp = span_of(a, b);
@@ -304,10 +316,14 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       const uint32_t mask = (uint32_t)__ballot(ok) & (uint32_t)((1ull << T::kKeys) - 1);
       const int slot = ok ? page * a.block_size + r : 0;
       char* stage = ring + (x & (S - 1)) * 2 * T::kSide;
+      uint32_t row_slot[T::kLoads];  // exchanged together, before the first load
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i)
+        row_slot[i] = (uint32_t)__shfl(slot, i * T::kRowsPerLoad + lane / T::kChunks);
 #pragma unroll
       for (int i = 0; i < T::kLoads; ++i) {
         const int rr = i * T::kRowsPerLoad + lane / T::kChunks;
-        const size_t off = (size_t)(uint32_t)__shfl(slot, rr) * row_bytes + (size_t)h * T::kRow;
+        const size_t off = (size_t)row_slot[i] * row_bytes + (size_t)h * T::kRow;
         const int c = lane % T::kChunks;
         piece_to_lds<kStream>((const char*)a.k_cache + off + (c ^ T::swizzle_k(rr)) * 16,
                                  stage + i * 1024);
@@ -376,7 +392,6 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         }
         float p[kSub][4];
         float top = -__builtin_huge_valf();
-        const uint32_t of_lane = mask >> (4 * g4);
 #pragma unroll
         for (int t = 0; t < kSub; ++t) {
           f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -402,15 +417,21 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[t][i] = s[i] * qs;
-            if (mask != kAll && !((of_lane >> (16 * t + i)) & 1))
-              p[t][i] = -__builtin_huge_valf();
-            top = fmaxf(top, p[t][i]);
-          }
+          for (int i = 0; i < 4; ++i) p[t][i] = s[i] * qs;
         }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        if (mask != kAll) {
+          const uint32_t of_lane = mask >> (4 * g4);
+#pragma unroll
+          for (int t = 0; t < kSub; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!((of_lane >> (16 * t + i)) & 1)) p[t][i] = -__builtin_huge_valf();
+        }
+#pragma unroll
+        for (int t = 0; t < kSub; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, p[t][i]);
+        top = max_over_groups(top);
         const float mn = fmaxf(m, top);
         const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
         if (__any(mn > m)) {
