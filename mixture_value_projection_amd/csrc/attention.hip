@@ -755,8 +755,15 @@ size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int
 
 namespace {
 
+// Keys of a row at most.
+long long most_keys(const AttentionArgs& a) {
+  if (a.sel != nullptr) return (long long)std::min(a.keep, a.max_blocks) * a.block_size;
+  const long long keys = (long long)a.max_blocks * a.block_size;
+  return a.window > 0 ? std::min<long long>(keys, a.window) : keys;
+}
+
 template <int D, bool kFp8, int kTracks, bool kShared, bool kList>
-hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
+hipError_t launch_cfg(const AttentionArgs& a, bool whole, hipStream_t stream) {
   using T = Tile<D, kFp8>;
   static std::atomic<unsigned long long> done{0};
   hipError_t e = once_per_device(done, [&] {
@@ -766,18 +773,8 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
   });
   if (e != hipSuccess) return e;
   const Parts parts = parts_of(a);
-  // Few tiles a row at most (short contexts, windows, short lists): every row
-  // is one workgroup's, and there is nothing to join.  A workgroup alone takes
-  // 0.9 us a tile, splitting and joining 4 to 5 us in all, and the more rows
-  // there are the less a split is for.  32 query heads over 8 of 128, split
-  // and whole: 1 request of 64 tokens 8.8 and 7.9 us, of 128 9.0 and 11.4; 16 of
-  // 32..96 about 9.7 and 10; 64 of up to 192 16.9 and 15.9, of up to 256 18.7
-  // and 19.7; 256 of up to 512 72.6 and 62.7.
   const int tile_keys = T::kKeys * (4 / kTracks);
-  long long keys = (long long)(kList ? std::min(a.keep, a.max_blocks) : a.max_blocks) * a.block_size;
-  if (!kList && a.window > 0) keys = std::min<long long>(keys, a.window);
   const long long rows = (long long)a.B * (tracks_of(a.Hq, a.H) / kTracks);
-  const int whole = keys <= std::min(4 + rows / 16, 32ll) * tile_keys;
   const int grid = T::kPerCu * kCus;
   Pad pad = {};
   if (kList) {
@@ -804,19 +801,41 @@ hipError_t launch_cfg(const AttentionArgs& a, hipStream_t stream) {
 }
 
 template <int D, bool kFp8, int kTracks, bool kShared>
-hipError_t launch_list(const AttentionArgs& a, hipStream_t stream) {
-  return a.sel != nullptr ? launch_cfg<D, kFp8, kTracks, kShared, true>(a, stream)
-                          : launch_cfg<D, kFp8, kTracks, kShared, false>(a, stream);
+hipError_t launch_list(const AttentionArgs& a, bool whole, hipStream_t stream) {
+  return a.sel != nullptr ? launch_cfg<D, kFp8, kTracks, kShared, true>(a, whole, stream)
+                          : launch_cfg<D, kFp8, kTracks, kShared, false>(a, whole, stream);
 }
 
+// Few tiles a row at most (short contexts, windows, short lists): every row is
+// one workgroup's, and there is nothing to join.  Splitting and joining take
+// 4 to 5 us in all, a tile of a workgroup alone 0.9, and the more rows there
+// are the less a split is for.  While every row of a single track has a
+// workgroup at once, its four waves take stripes of the row, else four tracks.
+// 32 query heads over 8 of 128, us of (four tracks split / four tracks whole /
+// stripes whole): 1 request of up to 64 tokens 8.8 / 7.5 / 5.8, of 256 9.6 / -
+// / 8.0, of 512 11.3 / - / 11.0; 16 of 384 12.9 / - / 10.0; 64 of 256 18.7 /
+// 19.7 / 12.1, of 768 31.6 / - / 28.7; 256 of 64 - / 12.3 / 19.7, of 512 72.6 /
+// 62.7 / 65.8.  With 8 bits 64 of 512 20.0 / - / 13.9.  256-wide tiles are twice
+// the bytes and have half the workgroups.
 template <int D, bool kFp8>
 hipError_t launch_tracks(const AttentionArgs& a, hipStream_t stream) {
-  const int tracks = tracks_of(a.Hq, a.H);
+  using T = Tile<D, kFp8>;
+  const int tracks = tracks_of(a.Hq, a.H), group = tracks_per_group(tracks);
+  const long long rows = (long long)a.B * tracks, keys = most_keys(a);
+  const bool whole = keys <= std::min(4 + rows / group / 16, 32ll) * T::kKeys * (4 / group);
+  const long long at_once = T::kPerCu * kCus;
+  if (keys <= std::min(5 + rows / 16, 12ll) / (3 - T::kPerCu) * T::kKeys * 4 &&
+      (rows <= at_once || (!whole && rows <= 2 * at_once)))
+    return launch_list<D, kFp8, 1, false>(a, true, stream);
   const bool shared = tracks > a.H;
-  switch (tracks_per_group(tracks)) {
-    case 4: return shared ? launch_list<D, kFp8, 4, true>(a, stream) : launch_list<D, kFp8, 4, false>(a, stream);
-    case 2: return shared ? launch_list<D, kFp8, 2, true>(a, stream) : launch_list<D, kFp8, 2, false>(a, stream);
-    default: return launch_list<D, kFp8, 1, false>(a, stream);
+  switch (group) {
+    case 4:
+      return shared ? launch_list<D, kFp8, 4, true>(a, whole, stream)
+                    : launch_list<D, kFp8, 4, false>(a, whole, stream);
+    case 2:
+      return shared ? launch_list<D, kFp8, 2, true>(a, whole, stream)
+                    : launch_list<D, kFp8, 2, false>(a, whole, stream);
+    default: return launch_list<D, kFp8, 1, false>(a, whole, stream);
   }
 }
 

@@ -392,7 +392,10 @@ def test_large_batches():
 @pytest.mark.parametrize("dtype", [torch.bfloat16, FP8], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("B,Hq,H,D,bs,longest", [
     (1, 8, 8, 128, 16, 64), (3, 12, 3, 64, 16, 500), (70, 8, 4, 128, 16, 120), (70, 8, 4, 128, 16, 160),
-    (300, 4, 2, 64, 8, 900), (5, 40, 2, 256, 16, 90)])
+    (300, 4, 2, 64, 8, 900), (5, 40, 2, 256, 16, 90), (1, 32, 8, 128, 16, 320),
+    (1, 32, 8, 128, 16, 400), (64, 16, 4, 256, 16, 300), (64, 16, 4, 256, 16, 500),
+    (130, 32, 8, 128, 32, 200), (130, 32, 8, 128, 32, 640), (33, 64, 1, 64, 16, 700),
+    (17, 96, 2, 128, 16, 500), (260, 8, 4, 64, 8, 1000)])
 def test_rows_split_or_whole(B, Hq, H, D, bs, longest, dtype):
     """Batches on either side of where rows stop being split: by the table's
     width, by a window and by the list's length; the same keys in a wider
