@@ -17,11 +17,12 @@
 // lengths.  A request whose tiles lie in one stretch is finished there; else
 // each stretch leaves its part (m, sum, unnormalised out; fp32) in the
 // workspace and attention_join_kernel adds them.  Where no row can have more
-// than a few tiles the line is one of whole rows (`whole`).
+// than a few tiles the line is one of whole rows (`whole`).  With a list, the
+// tiles are those of as many of its entries as the request has blocks.
 //
-// A workgroup's four waves take four key heads at the same positions (rows of
-// 4 x head_dim elements are contiguous), or stripes of the tiles when there
-// are fewer heads.  Each wave is a pipeline of its own: a ring of tiles in
+// A workgroup's four waves take four tracks (a key head with up to 16 of its
+// query heads) at the same positions (rows of 4 x head_dim elements are
+// contiguous), or stripes of the tiles where there are fewer.  Each wave is a pipeline of its own: a ring of tiles in
 // LDS, filled by direct-to-LDS loads with kStages - 1 tiles in flight while
 // one is used; no barrier but at the ends.  The block table (and the list of
 // chosen blocks) is fetched the same way, kStages tiles ahead of the tile
