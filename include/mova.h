@@ -528,9 +528,13 @@ size_t mova_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int he
  *           log sum_p exp(scale * q . K[p]), -infinity for an empty row
  *
  * A row without keys (length 0, every block missing), or whose every logit is
- * -infinity, gives zeros and an lse of -infinity.  Products
- * accumulate in fp32; the softmax's maximum and sum are fp32, its weights take
- * part in the product with V to 16 bits; the result is rounded once to bf16.  Results are bitwise reproducible for
+ * -infinity, gives zeros and an lse of -infinity.  Products accumulate in fp32;
+ * the softmax's maximum and sum are fp32, its weights take part in the product
+ * with V to 2^-16; the result is rounded once to bf16.  An infinite value of a
+ * key that takes part makes its channel infinite (NaN with one of the other
+ * sign, or where the key's weight is below 2^-70 of the row's largest and
+ * rounds to 0); finite values may be as large as bf16 holds, where sums of
+ * them pass 2^112 with weights to 2^-15.  Results are bitwise reproducible for
  * identical inputs; how a request's keys are split among workgroups, and so
  * the last bits of its row, depends on the lengths of the whole batch.
  * keep * block_size <= 2^30, scale finite.

@@ -145,6 +145,15 @@ __device__ __forceinline__ int padded(int n, Pad pad) {
   return min(fast_div(n + pad.to - 1, pad.by) * pad.to, pad.most);
 }
 
+// Sums of weighted values above kMostSum (or not finite) are formed once more,
+// with weights relative to 2^kLift times the largest.  The second pass cannot
+// overflow, as a row has at most 2^30 keys, nor can the sums of its parts with
+// those of the others (at most 4 * 2 * kMaxGrid of them, each up to kMostSum).
+// And a weight's second part, 0 or negative for many, is kept at 2^-22 of the
+// weight or more, so that its product with an infinite value is that infinity.
+// (The first part is cut rather than rounded for that, which costs it a bit.)
+constexpr float kMostSum = 0x1p112f, kLift = 31.f, kLeastPart = 0x1p-22f;
+
 // 8 e4m3 elements as bf16 (exact).
 __device__ __forceinline__ Frag16 widen_fp8(uint32_t w0, uint32_t w1) {
   auto two = [](uint32_t w, auto upper) {
@@ -236,6 +245,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
   long long at = line.first;  // first tile of request b
   Span sp = span_of(a, b);
   int n = tiles_of(sp);
+  bool again = false;  // the second pass over a row's share
   for (long long pos = line.start; pos < line.end;) {
     while (pos >= at + units_of(n)) {
       at += units_of(n);
@@ -432,7 +442,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         for (int t = 0; t < kSub; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) top = fmaxf(top, p[t][i]);
-        top = max_over_groups(top);
+        top = max_over_groups(top) + (again ? kLift : 0.f);
         const float mn = fmaxf(m, top);
         const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
         if (__any(mn > m)) {
@@ -458,8 +468,10 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
           for (int i = 0; i < 4; ++i) {
             const float e = __builtin_amdgcn_exp2f(p[t][i] - safe);
             l += e;
-            high.e[4 * t + i] = (bf16_t)e;
-            low.e[4 * t + i] = (bf16_t)(e - (float)high.e[4 * t + i]);
+            const uint32_t bits = __builtin_bit_cast(uint32_t, e) & (again ? 0xffff0000u : ~0u);
+            high.e[4 * t + i] = (bf16_t)__builtin_bit_cast(float, bits);
+            const float rest = e - (float)high.e[4 * t + i];
+            low.e[4 * t + i] = (bf16_t)(kFp8 ? rest : fmaxf(rest, e * (again ? kLeastPart : -1.f)));
           }
         if constexpr (kSub == 1) high.h[1] = low.h[0];
         const uint32_t vt = (uint32_t)(uintptr_t)(lds_void*)(stage + T::kSide);
@@ -512,6 +524,18 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
     // The four lanes of a query head hold its sum in parts.
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    if constexpr (!kFp8) {  // (8-bit values are at most 448)
+      float most = 0.f;     // NaN counts as the largest
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_maximum(most, fabsf(o[c][i]));
+      again = !again && __any(has_row && !(most < kMostSum) && l > 0.f && l < __builtin_huge_valf());
+      if (again) {
+        pos -= whole ? 1 : share;
+        continue;
+      }
+    }
     if constexpr (kStripes > 1) {
       // Stripes of a head meet in its first wave, through the ring.
       __syncthreads();
