@@ -536,6 +536,13 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         continue;
       }
     }
+    if (__any(l == 0.f)) {
+      // No weight: nothing, also where a value is infinite or NaN.
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[c][i] = l == 0.f ? 0.f : o[c][i];
+    }
     if constexpr (kStripes > 1) {
       // Stripes of a head meet in its first wave, through the ring.
       __syncthreads();

@@ -128,3 +128,16 @@ def test_just_below_the_second_pass(D):
     size = torch.from_numpy(2.0 ** rng.integers(100, 122, a["v"].shape[0]))[:, None, None, None]
     a["v"] = (a["v"].double() * size).to(torch.bfloat16)
     each_form(a, 2, "between")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, C.FP8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("lens,Hq,H,D,bs", SHAPES)
+def test_every_logit_minus_infinity(lens, Hq, H, D, bs, dtype):
+    """Rows whose every logit is -infinity give zeros, whatever their values."""
+    for v in (1.0, math.inf, math.nan):  # (the 8-bit type has NaN for infinity)
+        a = C.make_attention(14, lens, Hq, H, D, bs, dtype)
+        a["q"][:, :, 0] = -math.inf
+        a["k"][:, :, :, 0] = torch.ones(1).to(dtype)
+        a["v"][:] = torch.tensor(v).to(dtype)
+        out, lse = C.run_attention(a)
+        assert (out == 0).all() and (lse == -math.inf).all(), v
