@@ -77,25 +77,27 @@ __global__ __launch_bounds__(256, 6) void kv_store_kernel(StoreArgs a, int bound
   const int width = a.H * a.D;
   const int groups = ceil_div(width, 512);
   if ((int)blockIdx.x >= bounds_groups) {
-    const long long item = (long long)(blockIdx.x - bounds_groups) * 4 + wave;
-    const int t = (int)(item / groups);
-    if (t >= a.T) return;
-    const int c = ((int)(item - (long long)t * groups) * 64 + lane) * 8;
-    const long long s = a.slots[t];
-    if (s < 0 || s >= a.num_slots || c >= width) return;
-    const int head = c / a.D;
-    const size_t from = (size_t)t * width + c, to = (size_t)s * width + c;
-    Frag16 x, y;
-    if (a.k != nullptr) x.u = load16(a.k + from);
-    if (a.v != nullptr) y.u = load16(a.v + from);
-    Stored<kFp8> e;
-    if (a.k != nullptr) {
-      e.take(x, a.k_scale == nullptr ? 1.f : a.k_scale[head]);
-      e.store(a.k_cache, to);
-    }
-    if (a.v != nullptr) {
-      e.take(y, a.v_scale == nullptr ? 1.f : a.v_scale[head]);
-      e.store(a.v_cache, to);
+    const int items = a.T * groups;  // at most 2^29
+    const int step = ((int)gridDim.x - bounds_groups) * 4;
+    for (int item = ((int)blockIdx.x - bounds_groups) * 4 + wave; item < items; item += step) {
+      const int t = item / groups;
+      const int c = ((item - t * groups) * 64 + lane) * 8;
+      const long long s = a.slots[t];
+      if (s < 0 || s >= a.num_slots || c >= width) continue;
+      const int head = c / a.D;
+      const size_t from = (size_t)t * width + c, to = (size_t)s * width + c;
+      Frag16 x, y;
+      if (a.k != nullptr) x.u = load16(a.k + from);
+      if (a.v != nullptr) y.u = load16(a.v + from);
+      Stored<kFp8> e;
+      if (a.k != nullptr) {
+        e.take(x, a.k_scale == nullptr ? 1.f : a.k_scale[head]);
+        e.store(a.k_cache, to);
+      }
+      if (a.v != nullptr) {
+        e.take(y, a.v_scale == nullptr ? 1.f : a.v_scale[head]);
+        e.store(a.v_cache, to);
+      }
     }
     return;
   }
@@ -208,7 +210,9 @@ __global__ __launch_bounds__(256, 6) void kv_store_kernel(StoreArgs a, int bound
 
 hipError_t launch_kv_store(const StoreArgs& a, hipStream_t stream) {
   const int groups = ceil_div(a.H * a.D, 512);
-  const unsigned copy = (unsigned)(((long long)a.T * groups + 3) / 4);
+  // A launch has fewer than 2^32 threads: of very large calls a wave copies
+  // several pieces (at most 2^21 workgroups here, and 2^23 for the bounds).
+  const int copy = std::min((int)(((long long)a.T * groups + 3) / 4), 1 << 21);
   // A workgroup a token while there are few, so that a decode step's blocks
   // are worked on at once; prompts have about one run in block_size tokens.
   const int tokens = std::min(std::max(1, ceil_div(a.T, 256)), 64);
