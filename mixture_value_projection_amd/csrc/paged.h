@@ -61,19 +61,18 @@ struct SelectArgs {
   int32_t* sel;    // [B, H, keep]
   unsigned long long* scratch;  // select_scratch_words
 };
-// Scratch, in 8-byte words: a word a block in 16-byte aligned rows, read four
-// words at a time; then a word a tile of kSelectTile blocks.
+// Scratch, in 8-byte words: a word a block, in rows that hold whole tiles of
+// kSelectTile blocks (the choice reads whole tiles); then a word a tile.
 constexpr int kSelectTile = 16;
 __host__ __device__ constexpr size_t select_stride(int max_blocks) {
-  return ((size_t)max_blocks + 1) / 2 * 2;
+  return ((size_t)max_blocks + kSelectTile - 1) / kSelectTile * kSelectTile;
 }
 __host__ __device__ constexpr size_t select_tiles_at(int B, int H, int max_blocks) {
-  return (size_t)B * H * select_stride(max_blocks) + 4;
+  return (size_t)B * H * select_stride(max_blocks);
 }
 inline size_t select_scratch_words(int B, int H, int max_blocks) {
-  return B == 0 ? 0
-                : select_tiles_at(B, H, max_blocks) +
-                      (size_t)B * H * ceil_div(max_blocks, kSelectTile);
+  return select_tiles_at(B, H, max_blocks) +
+         (size_t)B * H * (select_stride(max_blocks) / kSelectTile);
 }
 hipError_t launch_block_select(const SelectArgs& a, hipStream_t stream);
 
