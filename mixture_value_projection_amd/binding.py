@@ -561,10 +561,20 @@ def _launch(fn, name: str, device, *args) -> None:
         raise MovaError(rc, name)
 
 
+_INT_MAX = 0x7fffffff
+
+
+def _fits(*sizes: int) -> None:
+    """The C ABI takes sizes as int, and ctypes would cut longer ones."""
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX:
+        raise ValueError(f"sizes must fit 32 bits, got {sizes}")
+
+
 def _dims(t: torch.Tensor, name: str, n: int, layout: str) -> Tuple[int, ...]:
     shape = t.shape
     if len(shape) != n:
         raise ValueError(f"{name} must be {layout}")
+    _fits(*shape)
     return shape
 
 
@@ -603,6 +613,7 @@ def paged_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, T: int, block_
     _check(free_count, "free_count", i32, (1,), dev)
     _check(cached_lens, "cached_lens", i32, (B,), dev)
     _check(new_lens, "new_lens", i32, (B,), dev)
+    _fits(T, block_size)
     if T < 0:
         raise ValueError("T must not be negative")
     if seq_lens is None:
@@ -698,6 +709,7 @@ def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
     _check(k_bounds, "k_bounds", torch.bfloat16, (nb, H, 2, D), dev)
     _check(block_table, "block_table", torch.int32, (B, mb), dev)
     _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _fits(block_size, keep, keep_first, keep_last)
     nbytes = _select_bytes(B, Hq, H, D, mb, block_size, keep)
     workspace = _scratch(workspace, nbytes, "mova_block_select", dev)
     if sel_blocks is None:
@@ -713,6 +725,7 @@ def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
 
 def attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int,
                               max_blocks: int, block_size: int, keep: int = 0) -> int:
+    _fits(B, n_heads, n_kv_heads, head_dim, max_blocks, block_size, keep)
     n = _attention_bytes(B, n_heads, n_kv_heads, head_dim, max_blocks, block_size, keep)
     if n == ctypes.c_size_t(-1).value:
         raise MovaError(-2, "mova_attention_workspace_bytes")
@@ -760,8 +773,9 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _check(out, "out", torch.bfloat16, (B, Hq, D), dev)
     _launch(lib.mova_attention_paged, "mova_attention_paged", dev, _ptr(q), _ptr(k_cache),
             _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale), nb, bs, _ptr(block_table), mb,
-            _ptr(seq_lens), _ptr(sel_blocks), keep, B, Hq, H, D, float(scale), int(window),
-            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel())
+            _ptr(seq_lens), _ptr(sel_blocks), keep, B, Hq, H, D, float(scale),
+            max(-1, min(int(window), _INT_MAX)), _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel())
     return out
 
 
