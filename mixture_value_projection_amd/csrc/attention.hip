@@ -131,20 +131,6 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   return s;
 }
 
-// Tiles that a row of n takes up in the line.  With lists that is a multiple of
-// `to`, a workgroup's share if all were full, so that one row shorter than its
-// list does not have the stretches of all later ones run across two rows (32
-// requests, a few of them short of their 64 blocks: 53.3 us unpadded, 50.7 so,
-// for selection and attention).
-struct Pad {
-  FastDiv by;
-  int to;
-  int most;  // tiles of a full list
-};
-__device__ __forceinline__ int padded(int n, Pad pad) {
-  return min(fast_div(n + pad.to - 1, pad.by) * pad.to, pad.most);
-}
-
 // Sums of weighted values above kMostSum (or not finite) are formed once more,
 // with weights relative to 2^kLift times the largest.  The second pass cannot
 // overflow, as a row has at most 2^30 keys, nor can the sums of its parts with
@@ -207,7 +193,7 @@ __device__ __forceinline__ void read4_transposed(i32x2 (&v)[4], const uint32_t (
 // kShared: tracks of one key head lie side by side and read the same rows.
 template <int D, bool kFp8, int kTracks, bool kShared, bool kList>
 __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts parts,
-                                                        FastDiv by_block, Pad pad, int whole) {
+                                                        FastDiv by_block, int whole) {
   using T = Tile<D, kFp8>;
   constexpr int kStripes = 4 / kTracks;
   constexpr bool kStream = T::kStream && !kShared;
@@ -233,8 +219,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 
   // Units of the line that a request brings: its tiles, or its rows.
   auto tiles_of = [&](const Span& s) { return ceil_div(s.keys, T::kKeys * kStripes); };
-  auto row_units = [&](int n) { return whole ? 1 : kList ? padded(n, pad) : n; };
-  auto units_of = [&](int n) { return (long long)row_units(n) * rows_per_b; };
+  auto units_of = [&](int n) { return (long long)(whole ? 1 : n) * rows_per_b; };
   Line line;
   if (!line_begin(a.B, [&](int b) { return units_of(whole ? 0 : tiles_of(span_of(a, b))); }, s_line,
                   parts.prefix, &line))
@@ -253,13 +238,10 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
       sp = span_of(a, b);
       n = tiles_of(sp);
     }
-    const int units = row_units(n);
-    const int row = whole ? (int)(pos - at) : (int)floor_div(pos - at, units);
-    const int t0 = whole ? 0 : (int)(pos - at - (long long)row * units);
-    const int share = (int)min((long long)(units - t0), line.end - pos);
-    const int t1 = whole ? n : min(n, t0 + share);
-    pos += whole ? 1 : share;
-    if (kList && !whole && t0 >= n) continue;  // the padding of a row
+    const int row = whole ? (int)(pos - at) : (int)floor_div(pos - at, n);
+    const int t0 = whole ? 0 : (int)(pos - at - (long long)row * n);
+    const int t1 = whole ? n : (int)min((long long)n, t0 + (line.end - pos));
+    pos += whole ? 1 : t1 - t0;
     const int track = row * kTracks + tsub;
     const int h = track / qtiles, qt = track - h * qtiles;
     int nt = t1 - t0;
@@ -532,7 +514,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
         for (int i = 0; i < 4; ++i) most = __builtin_elementwise_maximum(most, fabsf(o[c][i]));
       again = !again && __any(has_row && !(most < kMostSum) && l > 0.f && l < __builtin_huge_valf());
       if (again) {
-        pos -= whole ? 1 : share;
+        pos -= whole ? 1 : t1 - t0;
         continue;
       }
     }
@@ -609,7 +591,7 @@ __global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a, Parts p
 // several workgroups', a slice of its channels each.
 template <int D, int kAtOnce>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts, int tracks,
-                                                             int tile_keys, Pad pad) {
+                                                             int tile_keys) {
   constexpr int kPer = D / 64;      // channels of a lane
   constexpr int kFew = 32, kBatch = 8;
   // (Four heads a workgroup: rarely many parts, and registers are waves at once.)
@@ -624,7 +606,6 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = ceil_div(span_of(a, b).keys, tile_keys);
-  const int units = a.sel != nullptr ? padded(n, pad) : n;
   const long long stretch = parts.prefix[a.B], before = parts.prefix[b];
   const int G = a.Hq / a.H;
   const int qtiles = ceil_div(G, 16), cap = min(G, 16);
@@ -649,7 +630,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   // First part of the head, and how many there are.
   auto parts_at = [&](int hq, int* w0) {
     const int h = hq / G, gi = hq - h * G;
-    const long long first = before + (long long)((h * qtiles + gi / 16) / tracks) * units;
+    const long long first = before + (long long)((h * qtiles + gi / 16) / tracks) * n;
     *w0 = (int)floor_div(first, stretch);
     return n == 0 ? 0 : min((int)floor_div(first + n - 1, stretch), kMaxGrid - 1) - *w0 + 1;
   };
@@ -806,16 +787,8 @@ hipError_t launch_cfg(const AttentionArgs& a, bool whole, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const Parts parts = parts_of(a);
   const int tile_keys = T::kKeys * (4 / kTracks);
-  const long long rows = (long long)a.B * (tracks_of(a.Hq, a.H) / kTracks);
-  const int grid = T::kPerCu * kCus;
-  Pad pad = {};
-  if (kList) {
-    pad.most = ceil_div(a.keep * a.block_size, tile_keys);
-    pad.to = (int)std::min<long long>((rows * pad.most + grid - 1) / grid, pad.most);
-    pad.by = make_fast_div(pad.to);
-  }
-  attention_kernel<D, kFp8, kTracks, kShared, kList><<<grid, 256, 4 * T::kLds, stream>>>(
-      a, parts, make_fast_div(a.block_size), pad, whole);
+  attention_kernel<D, kFp8, kTracks, kShared, kList>
+      <<<T::kPerCu * kCus, 256, 4 * T::kLds, stream>>>(a, parts, make_fast_div(a.block_size), whole);
   e = hipGetLastError();
   if (e != hipSuccess || whole) return e;
   // Few heads in the batch may have many parts each: a workgroup a head, and
@@ -823,11 +796,11 @@ hipError_t launch_cfg(const AttentionArgs& a, bool whole, hipStream_t stream) {
   const int heads = a.B * a.Hq;
   if (heads >= 1024) {
     attention_join_kernel<D, 4><<<dim3(ceil_div(a.Hq, 4), a.B), 256, 0, stream>>>(
-        a, parts, kTracks, tile_keys, pad);
+        a, parts, kTracks, tile_keys);
   } else {
     const int slices = std::clamp(1024 / heads, 1, D / 32);
     attention_join_kernel<D, 1><<<dim3(a.Hq, a.B, slices), 256, 0, stream>>>(a, parts, kTracks,
-                                                                            tile_keys, pad);
+                                                                            tile_keys);
   }
   return hipGetLastError();
 }
