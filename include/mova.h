@@ -403,7 +403,8 @@ enum mova_cache_dtype {
 /*
  * Block tables and slot maps of one step.  Request b has cached_lens[b]
  * tokens in the cache, in its first ceil(cached_lens[b] / block_size) table
- * entries.
+ * entries.  Those have to be blocks of the pool, none of them in two rows: the
+ * call computes slots from them and gives them back as they stand, -1 included.
  *
  *   new_lens[b] >= 0: it gets that many new tokens; their rows are
  *     [cu_new[b], cu_new[b + 1]) of the step's packed tokens.

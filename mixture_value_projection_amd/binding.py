@@ -699,7 +699,8 @@ def block_select(q: torch.Tensor, k_bounds: torch.Tensor, block_size: int,
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """mova_block_select: int32 [B, n_kv_heads, keep] positions in each
     request's block table of the blocks whose keys can reach the highest
-    logits, ascending, -1 behind the last."""
+    logits, ascending, -1 behind the last.  ``workspace`` (optional uint8 tensor)
+    is reused when large enough; else one is allocated."""
     lib = load_library()
     B, Hq, D = _dims(q, "q", 3, "[B, n_heads, head_dim]")
     nb, H = _dims(k_bounds, "k_bounds", 4, "[num_blocks, n_kv_heads, 2, head_dim]")[:2]
@@ -744,7 +745,9 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
     ``window`` > 0 keeps the last ``window`` positions, ``sel_blocks`` (int32
     [B, n_kv_heads, keep], as from ``block_select``) the listed blocks;
-    ``lse`` (float32 [B, n_heads]) receives the log-sum-exp of the logits."""
+    ``lse`` (float32 [B, n_heads]) receives the log-sum-exp of the logits.
+    ``workspace`` (optional uint8 tensor) is reused when large enough
+    (``attention_workspace_bytes``); else one is allocated."""
     lib = load_library()
     B, Hq, D = _dims(q, "q", 3, "[B, n_heads, head_dim]")
     nb, bs, H, _ = _dims(k_cache, "k_cache", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")

@@ -22,11 +22,11 @@
 //
 // A workgroup's four waves take four tracks (a key head with up to 16 of its
 // query heads) at the same positions (rows of 4 x head_dim elements are
-// contiguous), or stripes of the tiles where there are fewer.  Each wave is a pipeline of its own: a ring of tiles in
-// LDS, filled by direct-to-LDS loads with kStages - 1 tiles in flight while
-// one is used; no barrier but at the ends.  The block table (and the list of
-// chosen blocks) is fetched the same way, kStages tiles ahead of the tile
-// whose addresses need it.
+// contiguous), or stripes of the tiles where there are fewer.  Each wave is a
+// pipeline of its own: a ring of tiles in LDS, filled by direct-to-LDS loads
+// with kStages - 1 tiles in flight while one is used; no barrier but at the
+// ends.  The block table (and the list of chosen blocks) is fetched the same
+// way, kStages tiles ahead of the tile whose addresses need it.
 //
 // A tile's logits are MFMA products K Q^T (16 keys x 16 query heads, heads
 // past the group are zero), so a lane holds four keys of one query head and
@@ -34,8 +34,11 @@
 // they lie in the registers, the second operand of out^T = V^T P^T, whose
 // first operand the transposing LDS reads deliver; the sums over keys may run
 // in any order as long as both operands agree.  Weights go into this product
-// as two bf16 parts (2^-16 relative); maxima, sums and accumulators are fp32.
-// 8-bit elements are widened to bf16, which is exact.
+// as two bf16 parts (2^-16 relative), and the others of the softmax stay fp32.
+// Against the 64-bit result rounded to bf16 that leaves 0.2 % of the elements
+// one step off (64 requests of 500 to 8000 tokens; 0.05 % with fp32 weights); a
+// third part cost 8-bit caches 1.4 % of their time.  8-bit elements are widened
+// to bf16, which is exact.
 #include <algorithm>
 #include <atomic>
 
@@ -75,16 +78,17 @@ struct Tile {
   static constexpr int kLoads = kKeys / kRowsPerLoad;           // wave loads per side
   static constexpr int kSide = kKeys * kRow;                    // bytes of a side (K or V)
   // Two workgroups a CU with 16 KB of keys and values a wave, or one with 32:
-  // two hide each other's softmax and beginnings (64 requests, 128 wide 130 ->
-  // 127 us; 8 bits, 64 wide 63 -> 54, 3 heads of 128 41.5 -> 35.3), where two
-  // tiles fit 16 KB.
+  // two hide each other's softmax and beginnings, where two tiles fit 16 KB (64
+  // requests of 500 to 8000 tokens: 8 heads of 128 122.0 -> 121.5 us, of 64 66.5
+  // -> 66.0; 8 bits, 8 heads of 64 52.8 -> 44.4, 3 heads of 128 39.4 -> 32.9).
   static constexpr int kPerCu = 4 * kSide <= 16384 ? 2 : 1;
   static constexpr int kRing = 32768 / kPerCu;
   static constexpr int kStages = kRing / (2 * kSide);
   static constexpr int kLds = kRing + 2 * kStages * 256;        // with the block numbers
-  // The non-temporal hint, where a row fills a 128-byte cache line (64 requests:
-  // 144 -> 127 us); two heads' waves share the line of a shorter row, and the
-  // hint would have it read twice (64 wide with 8 bits: 44 us without, 53 with).
+  // The non-temporal hint, where a row fills a 128-byte cache line (the same
+  // batch, 8 heads of 128: 138 -> 121 us, of 64: 75 -> 66); two heads' waves share
+  // the line of a shorter row, and the hint would have it read twice (64 wide with
+  // 8 bits: 44 us without, 53 with).
   static constexpr bool kStream = kRow >= 128;
   static_assert(kStages >= 2 && kChunks <= 32 && kRowsPerLoad >= 2, "tile shape");
   // Piece c of row r lies at piece c ^ swizzle(r), so that the 8 rows of one
@@ -758,9 +762,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   }
 }
 
-size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int block_size,
-                                int keep) {
-  (void)max_blocks; (void)block_size; (void)keep;
+size_t attention_scratch_floats(int B, int Hq, int H, int D) {
   if (B == 0) return 0;
   const size_t rows = (size_t)kMaxGrid * 2 * tracks_per_group(tracks_of(Hq, H)) * std::min(Hq / H, 16);
   return prefix_floats(B) + (rows * 2 + 63) / 64 * 64 + rows * D;

@@ -16,7 +16,7 @@
 // product of the absolute values the error that 32-bit sums can have made.
 // That is a few percent of the matrix units, where 64-bit products of every
 // block kept the vector units busy for twice the time that the bounds take to
-// read (3 requests of 100k to 400k tokens: 42 us; 96 MB of bounds).  The blocks
+// read (3 requests of 100k to 400k tokens: 42 us; 125 MB of bounds).  The blocks
 // of the batch form one line in tiles of 16, cut into equal stretches as in
 // attention.hip.
 //

@@ -97,8 +97,7 @@ struct AttentionArgs {
   float* part;  // scratch of attention_scratch_floats
 };
 // Floats of scratch; depends on the sizes alone.
-size_t attention_scratch_floats(int B, int Hq, int H, int D, int max_blocks, int block_size,
-                                int keep);
+size_t attention_scratch_floats(int B, int Hq, int H, int D);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
 // ---- device helpers ---------------------------------------------------------

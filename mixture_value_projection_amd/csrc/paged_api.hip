@@ -172,8 +172,7 @@ size_t mova_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int he
                                       int max_blocks, int block_size, int keep) {
   if (check_attention(B, n_heads, n_kv_heads, head_dim, max_blocks, block_size, keep) != MOVA_OK)
     return (size_t)-1;
-  return align256(4 * attention_scratch_floats(B, n_heads, n_kv_heads, head_dim, max_blocks,
-                                               block_size, keep));
+  return align256(4 * attention_scratch_floats(B, n_heads, n_kv_heads, head_dim));
 }
 
 int mova_attention_paged(const void* q, const void* k_cache, const void* v_cache, int cache_dtype,
