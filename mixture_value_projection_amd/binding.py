@@ -574,7 +574,8 @@ def _dims(t: torch.Tensor, name: str, n: int, layout: str) -> Tuple[int, ...]:
     shape = t.shape
     if len(shape) != n:
         raise ValueError(f"{name} must be {layout}")
-    _fits(*shape)
+    if max(shape) > _INT_MAX:
+        raise ValueError(f"{name}'s sizes must fit 32 bits, got {tuple(shape)}")
     return shape
 
 
