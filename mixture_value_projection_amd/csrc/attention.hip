@@ -825,14 +825,14 @@ hipError_t launch_list(const AttentionArgs& a, bool whole, hipStream_t stream) {
 // 62.7 / 65.8.  With 8 bits 64 of 512 20.0 / - / 13.9.  256-wide tiles are twice
 // the bytes and have half the workgroups.
 //
-// Rows that need a second round of workgroups are striped while they are short,
-// the longer the fuller that round is.  Us of (four tracks split / stripes whole)
+// Rows that wait for a workgroup to come free are striped while they are short,
+// the longer the more of them there are.  Us of (four tracks split / stripes whole)
 // for lengths of 1/8 to the whole of the limit, and all at it: 72 requests of 300
 // 20.1 / 19.3 and 26.8 / 23.8; 65 of 768 27.0 / 36.7 and 44.3 / 48.6, 96 of 768
 // 32.8 / 37.5 and 58.0 / 53.4, 104 of 640 32.0 / 32.9 and 55.5 / 47.5, 128 of 768
-// 40.4 / 40.3 and 71.5 / 65.6.  256 wide,
-// 112 of 384 25.8 / 28.7 and 39.7 / 35.5; 8 bits, 65 of 1000 23.1 / 30.6 and 33.5
-// / 36.8, 112 of 1000 31.0 / 31.3 and 51.5 / 43.7.
+// 40.4 / 40.3 and 71.5 / 65.6.  256 wide, 112 of 384 25.8 / 28.7 and 39.7 / 35.5;
+// 8 bits, 65 of 1000 23.1 / 30.6 and 33.5 / 36.8, 112 of 1000 31.0 / 31.3 and 51.5
+// / 43.7.
 template <int D, bool kFp8>
 hipError_t launch_tracks(const AttentionArgs& a, hipStream_t stream) {
   using T = Tile<D, kFp8>;
@@ -841,8 +841,8 @@ hipError_t launch_tracks(const AttentionArgs& a, hipStream_t stream) {
   const bool whole = keys <= std::min(4 + rows / group / 16, 32ll) * T::kKeys * (4 / group);
   const long long at_once = T::kPerCu * kCus;
   auto striped = [](long long tiles) { return tiles / (3 - T::kPerCu) * T::kKeys * 4; };  // keys
-  const bool second = rows <= 2 * at_once && keys <= striped(5 + 8 * (rows - at_once) / at_once);
-  if (keys <= striped(std::min(5 + rows / 16, 12ll)) && (rows <= at_once || (!whole && second)))
+  const bool waiting = rows <= 2 * at_once && keys <= striped(5 + 8 * (rows - at_once) / at_once);
+  if (keys <= striped(std::min(5 + rows / 16, 12ll)) && (rows <= at_once || (!whole && waiting)))
     return launch_list<D, kFp8, 1, false>(a, true, stream);
   const bool shared = tracks > a.H;
   switch (group) {

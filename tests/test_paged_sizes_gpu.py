@@ -130,10 +130,10 @@ def test_select_over_more_than_65536_blocks(n, keep, first, last):
 @pytest.mark.parametrize("B,Hq,H,D,bs,longest", [
     (300, 4, 2, 64, 8, 768), (300, 4, 2, 64, 8, 776), (180, 12, 4, 128, 16, 512),
     (180, 12, 4, 128, 16, 528), (90, 8, 4, 256, 16, 256), (90, 8, 4, 256, 16, 272)])
-def test_second_round_of_rows(B, Hq, H, D, bs, longest, dtype):
+def test_more_rows_than_workgroups(B, Hq, H, D, bs, longest, dtype):
     """Batches of more rows than have a workgroup at once, on either side of the
     length (of bf16 keys) up to which each is one workgroup's."""
     rng = np.random.default_rng(longest)
     lens = rng.integers(0, longest + 1, B)
     lens[B // 2] = longest
-    C.check_attention(C.make_attention(B, list(lens), Hq, H, D, bs, dtype), "second round")
+    C.check_attention(C.make_attention(B, list(lens), Hq, H, D, bs, dtype), "more rows")
