@@ -370,7 +370,10 @@ int mova_ffn_moe_forward(const void* x, const void* router_w, const float* route
  * (mova_paged_plan), their keys, and values for an 8-bit pool, stored
  * (mova_kv_store_paged), the blocks worth reading chosen (mova_block_select,
  * optional), and one new token per request attending over the cache
- * (mova_attention_paged).
+ * (mova_attention_paged), or several (mova_attention_chunk_paged).  Between the
+ * steps, rows of the block table are forked and given back and the pool's
+ * blocks moved together (mova_paged_fork, mova_paged_free, mova_paged_compact,
+ * mova_paged_copy).
  *
  * Shared layouts
  *   k_cache, v_cache  [num_blocks, block_size, n_kv_heads, head_dim], bf16 or
@@ -547,6 +550,167 @@ int mova_attention_paged(const void* q, const void* k_cache, const void* v_cache
                          int n_heads, int n_kv_heads, int head_dim, float scale, int window,
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
                          hipStream_t stream);
+
+/* Bytes of workspace of mova_attention_chunk_paged; (size_t)-1 outside the
+ * domain. */
+size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_heads,
+                                            int head_dim, int max_blocks, int block_size);
+
+/*
+ * Several new tokens per request (a prompt, a chunk of one, drafts to be
+ * verified) attending over the cache that already holds them:
+ *
+ *   out[t, i] = sum_p softmax_p( scale * q[t, i] . K[p, h] ) V[p, h],
+ *               h = i / (n_heads / n_kv_heads)
+ *
+ * Rows [cu_new[b], cu_new[b + 1]) of q and out are request b's.  Its row number
+ * j stands at position cached_lens[b] + j and sees the positions up to its own,
+ * with window > 0 only the last `window` of them.  A row whose position is not
+ * below seq_lens[b] has no token in the cache: zeros, and an lse of -infinity.
+ * With mova_paged_plan's cached_lens, seq_lens and cu_new, those are the rows
+ * of requests that it did not admit.  Rows ahead of cu_new[0] and from
+ * cu_new[B] on are not written.
+ *
+ *   q, out      bf16  [T, n_heads, head_dim]
+ *   cached_lens int32 [B]      tokens ahead of the new ones, kept within
+ *               [0, max_blocks * block_size]
+ *   seq_lens    int32 [B]      tokens with the new ones
+ *   cu_new      int32 [B + 1]  not decreasing, kept within [0, T]
+ *   lse         float [T, n_heads] or NULL
+ *
+ * Rows without keys, infinite logits and infinite or NaN values that take part
+ * or do not: as for mova_attention_paged, an infinite value gives NaN where its
+ * key's weight is below 2^-126 of the row's largest.  Products accumulate in
+ * fp32 and the softmax's maximum and sum are fp32.  Results are bitwise
+ * reproducible for identical inputs; how a row's keys are split, and so its
+ * last bits, depends on the lengths of the whole batch.  T <= 2^24, scale
+ * finite.  out and lse overlap no input.
+ */
+int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v_cache,
+                               int cache_dtype, const float* k_scale, const float* v_scale,
+                               int num_blocks, int block_size, const int32_t* block_table,
+                               int max_blocks, const int32_t* cached_lens, const int32_t* seq_lens,
+                               const int32_t* cu_new, int T, int B, int n_heads, int n_kv_heads,
+                               int head_dim, float scale, int window, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Upkeep of the cache's blocks.  Several rows of the block table may hold the
+ * same block: shares int32 [num_blocks] counts a block's holders beyond the
+ * first, 0 for every block at first.  mova_paged_plan knows nothing of it and
+ * need not: the blocks that it hands out have one holder, and rows whose blocks
+ * may be shared are ended with mova_paged_free instead of a negative
+ * new_lens.  num_blocks <= 2^20; int32 arrays are 4-byte aligned.  Blocks
+ * outside [0, num_blocks) in a table row are passed over.  Lengths are kept
+ * within [0, max_blocks * block_size].  Outputs overlap no input and no other
+ * output unless said so.  All results are the same for the same inputs.
+ */
+
+/*
+ * Further rows of the block table that begin with a parent's tokens: pair i
+ * gives row children[i] the first fork_lens[i] tokens of row parents[i] (all of
+ * them for NULL; kept within [0, cached_lens[parents[i]]]).  The blocks that
+ * these tokens fill are shared, their share counts go up by one, and for tokens
+ * that fill a last one in part a block is taken from the top of the free stack
+ * (as mova_paged_plan takes them) and named in copy_dst[i], with the parent's
+ * block in copy_src[i]: mova_paged_copy then copies it, once in each layer's
+ * pools.
+ *
+ * A pair gets nothing (its child's row and length stay) when a row number lies
+ * outside [0, B) -- -1 pads a list --, the child is a parent in this call or the
+ * child of an earlier pair, or when the pairs up to and with it need more blocks
+ * than the stack has and it needs one.  The child's row has to hold no blocks.
+ *
+ *   parents, children int32 [n], fork_lens int32 [n] or NULL
+ *   block_table  int32 [B, max_blocks]  in / out
+ *   free_blocks  int32 [free_capacity], not changed; free_count int32 [1];
+ *                free_count_out int32 [1], not the same address
+ *   shares       int32 [num_blocks]     in / out
+ *   seq_lens     int32 [B]  out: cached_lens, for the children the tokens they
+ *                got; not the address of cached_lens
+ *   copy_src, copy_dst int32 [n] out: -1 where nothing is to be copied
+ *
+ * n <= 2048.
+ */
+int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
+                    int n, const int32_t* cached_lens, int B, int block_size, int max_blocks,
+                    int32_t* block_table, const int32_t* free_blocks, int free_capacity,
+                    const int32_t* free_count, int32_t* free_count_out, int32_t* shares,
+                    int num_blocks, int32_t* seq_lens, int32_t* copy_src, int32_t* copy_dst,
+                    hipStream_t stream);
+
+/*
+ * Rows given back in whole or from some token on: row b keeps its first
+ * keep_lens[b] tokens (0: the request ends; at or above cached_lens[b]: it stays
+ * as it is) and lets go of the blocks behind them.  A block with a share count
+ * loses one; the last holder's goes on the free stack.  Blocks freed by the call
+ * are pushed in descending order, so that the lowest is on top; those beyond
+ * free_capacity are dropped.
+ *
+ * A row is not cut inside a block that others hold too (by the counts as they
+ * come in), as its next token would be written into theirs: it stays as it is.
+ * Such a row can be forked at that length instead, which copies the block.
+ *
+ *   free_blocks  int32 [free_capacity]  in / out, above *free_count only
+ *   shares       int32 [num_blocks]     in / out
+ *   seq_lens     int32 [B]  out: the tokens kept; not the address of
+ *                cached_lens or keep_lens
+ *
+ * The block table itself stays: what lies behind a row's last block does not
+ * matter.
+ */
+int mova_paged_free(const int32_t* cached_lens, const int32_t* keep_lens, int B, int block_size,
+                    int max_blocks, const int32_t* block_table, int32_t* free_blocks,
+                    int free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                    int32_t* shares, int num_blocks, int32_t* seq_lens, hipStream_t stream);
+
+/* Bytes of workspace of mova_paged_compact; (size_t)-1 outside the domain. */
+size_t mova_paged_compact_workspace_bytes(int num_blocks);
+
+/*
+ * The blocks in use moved together, so that the pool's upper part is free: with
+ * `used` blocks not on the free stack and edge = max(limit, used), the i-th used
+ * block at or above the edge goes to the i-th free block below it (both in
+ * ascending order).  limit = 0 moves everything below `used`.
+ *
+ *   cached_lens  int32 [B]: which entries of a row are in use
+ *   block_table_out int32 [B, max_blocks] out: the entries in use renamed, one
+ *                that names a free block -1; may be block_table
+ *   free_blocks_out int32 [free_capacity] out: the free blocks in descending
+ *                order, the lowest on top, behind them as free_blocks; may be
+ *                free_blocks.  *free_count_out: how many (each block counts
+ *                once); not the address of free_count
+ *   shares_out   int32 [num_blocks] out: counts at the blocks' new places, 0 for
+ *                free ones; may be shares
+ *   remap        int32 [num_blocks] out: a block's new place, -1 for a free one,
+ *                for whoever else holds block numbers
+ *   move_src, move_dst int32 [num_blocks / 2] out: the moves for
+ *                mova_paged_copy, -1 behind the last; *move_count of them
+ *   workspace    mova_paged_compact_workspace_bytes bytes, 256-byte aligned
+ *
+ * The contents have to be copied, in each layer's pools, before the freed blocks
+ * are handed out again.
+ */
+int mova_paged_compact(const int32_t* cached_lens, int B, int block_size, int max_blocks,
+                       const int32_t* block_table, int32_t* block_table_out,
+                       const int32_t* free_blocks, int32_t* free_blocks_out, int free_capacity,
+                       const int32_t* free_count, int32_t* free_count_out, const int32_t* shares,
+                       int32_t* shares_out, int num_blocks, int limit, int32_t* remap,
+                       int32_t* move_src, int32_t* move_dst, int32_t* move_count, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Blocks copied within the pools: block copy_dst[i] becomes as block copy_src[i]
+ * in k_cache, v_cache and k_bounds, each of which may be NULL (not all).  Pairs
+ * with a block outside [0, num_blocks) and those behind *copy_count (int32 [1],
+ * NULL: n) are passed over.  A copy_dst that is listed twice, or is another
+ * pair's copy_src, races: its contents are unspecified.  Domain as
+ * mova_kv_store_paged, block_size <= 2^18.
+ */
+int mova_paged_copy(const int32_t* copy_src, const int32_t* copy_dst, int n,
+                    const int32_t* copy_count, void* k_cache, void* v_cache, void* k_bounds,
+                    int cache_dtype, int num_blocks, int block_size, int n_kv_heads, int head_dim,
+                    hipStream_t stream);
 
 /*
  * Kernel-choice overrides, for tests and measurements only.  A production

@@ -84,6 +84,23 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mova_attention_paged.restype = i
     lib.mova_attention_paged.argtypes = [vp, vp, vp, i, vp, vp, i, i, vp, i, vp, vp, i, i, i, i, i,
                                          f, i, vp, vp, vp, sz, vp]
+    lib.mova_attention_chunk_workspace_bytes.restype = sz
+    lib.mova_attention_chunk_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.mova_attention_chunk_paged.restype = i
+    lib.mova_attention_chunk_paged.argtypes = [vp, vp, vp, i, vp, vp, i, i, vp, i, vp, vp, vp, i, i,
+                                               i, i, i, f, i, vp, vp, vp, sz, vp]
+    lib.mova_paged_copy.restype = i
+    lib.mova_paged_copy.argtypes = [vp, vp, i, vp, vp, vp, vp, i, i, i, i, i, vp]
+    lib.mova_paged_fork.restype = i
+    lib.mova_paged_fork.argtypes = [vp, vp, vp, i, vp, i, i, i, vp, vp, i, vp, vp, vp, i, vp, vp,
+                                    vp, vp]
+    lib.mova_paged_free.restype = i
+    lib.mova_paged_free.argtypes = [vp, vp, i, i, i, vp, vp, i, vp, vp, vp, i, vp, vp]
+    lib.mova_paged_compact_workspace_bytes.restype = sz
+    lib.mova_paged_compact_workspace_bytes.argtypes = [i]
+    lib.mova_paged_compact.restype = i
+    lib.mova_paged_compact.argtypes = [vp, i, i, i, vp, vp, vp, vp, i, vp, vp, vp, vp, i, i, vp, vp,
+                                       vp, vp, vp, sz, vp]
     lib.mova_debug_override.restype = i
     lib.mova_debug_override.argtypes = [i, i]
     lib.mova_debug_override_get.restype = i
@@ -781,6 +798,252 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             max(-1, min(int(window), _INT_MAX)), _ptr(out), _ptr(lse), _ptr(workspace),
             workspace.numel())
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_bytes(*sizes: int) -> int:
+    return load_library().mova_attention_chunk_workspace_bytes(*sizes)
+
+
+def attention_chunk_workspace_bytes(T: int, B: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                    max_blocks: int, block_size: int) -> int:
+    _fits(T, B, n_heads, n_kv_heads, head_dim, max_blocks, block_size)
+    n = _chunk_bytes(T, B, n_heads, n_kv_heads, head_dim, max_blocks, block_size)
+    if n == _NO_SIZE:
+        raise MovaError(-2, "mova_attention_chunk_workspace_bytes")
+    return n
+
+
+def attention_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_table: torch.Tensor, cached_lens: torch.Tensor,
+                          seq_lens: torch.Tensor, cu_new: torch.Tensor, scale: float,
+                          k_scale: Optional[torch.Tensor] = None,
+                          v_scale: Optional[torch.Tensor] = None, window: int = 0,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """mova_attention_chunk_paged: the new tokens of each request attending
+    over the paged cache that already holds them; returns bf16 [T, n_heads,
+    head_dim].
+
+    Rows ``cu_new[b]`` up to ``cu_new[b + 1]`` of ``q`` are request b's, at
+    positions from ``cached_lens[b]`` on; each sees the positions up to its
+    own (``window`` > 0: the last ``window`` of them).  Rows at or past
+    ``seq_lens[b]`` give zeros; rows that belong to no request are not
+    written.  With ``paged_plan``: its ``cached_lens`` argument and the
+    ``seq_lens`` and ``cu_new`` that it returns.  ``lse`` (float32 [T,
+    n_heads]) receives the log-sum-exp of the logits; ``workspace`` (optional
+    uint8 tensor) is reused when large enough
+    (``attention_chunk_workspace_bytes``); else one is allocated."""
+    lib = load_library()
+    T, Hq, D = _dims(q, "q", 3, "[T, n_heads, head_dim]")
+    nb, bs, H, _ = _dims(k_cache, "k_cache", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")
+    B, mb = _dims(block_table, "block_table", 2, "[B, max_blocks]")
+    dev = q.device
+    _check(q, "q", torch.bfloat16, (T, Hq, D), dev)
+    dtype = _check_pool(k_cache, "k_cache", (nb, bs, H, D), dev)
+    if _check_pool(v_cache, "v_cache", (nb, bs, H, D), dev) != dtype:
+        raise ValueError("the pools must have the same dtype")
+    _check(block_table, "block_table", torch.int32, (B, mb), dev)
+    _check(cached_lens, "cached_lens", torch.int32, (B,), dev)
+    _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _check(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    _check_scales(k_scale, v_scale, H, dev)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (T, Hq), dev)
+    workspace = _scratch(workspace, _chunk_bytes(T, B, Hq, H, D, mb, bs),
+                         "mova_attention_chunk_paged", dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", torch.bfloat16, (T, Hq, D), dev)
+    _launch(lib.mova_attention_chunk_paged, "mova_attention_chunk_paged", dev, _ptr(q),
+            _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale), nb, bs,
+            _ptr(block_table), mb, _ptr(cached_lens), _ptr(seq_lens), _ptr(cu_new), T, B, Hq, H, D,
+            float(scale), max(-1, min(int(window), _INT_MAX)), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel())
+    return out
+
+
+class PagedFork(NamedTuple):
+    """Outputs of ``paged_fork``."""
+    seq_lens: torch.Tensor    # int32 [B]
+    copy_src: torch.Tensor    # int32 [n]
+    copy_dst: torch.Tensor    # int32 [n]
+    free_count: torch.Tensor  # int32 [1]
+
+
+class PagedFree(NamedTuple):
+    """Outputs of ``paged_free``."""
+    seq_lens: torch.Tensor    # int32 [B]
+    free_count: torch.Tensor  # int32 [1]
+
+
+class PagedCompact(NamedTuple):
+    """Outputs of ``paged_compact``."""
+    block_table: torch.Tensor  # int32 [B, max_blocks]
+    free_blocks: torch.Tensor  # int32 [capacity]
+    free_count: torch.Tensor   # int32 [1]
+    shares: torch.Tensor       # int32 [num_blocks]
+    remap: torch.Tensor        # int32 [num_blocks]
+    move_src: torch.Tensor     # int32 [num_blocks // 2]
+    move_dst: torch.Tensor     # int32 [num_blocks // 2]
+    move_count: torch.Tensor   # int32 [1]
+
+
+def _given(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """An int32 output: the caller's, or a new one."""
+    if t is None:
+        return like.new_empty(shape)
+    _check(t, name, torch.int32, shape, like.device)
+    return t
+
+
+def _upkeep(block_table, free_blocks, free_count, shares, cached_lens, block_size):
+    """The checks that the upkeep of the blocks shares."""
+    B, mb = _dims(block_table, "block_table", 2, "[B, max_blocks]")
+    (cap,) = _dims(free_blocks, "free_blocks", 1, "[capacity]")
+    (nb,) = _dims(shares, "shares", 1, "[num_blocks]")
+    dev, i32 = block_table.device, torch.int32
+    _check(block_table, "block_table", i32, (B, mb), dev)
+    _check(free_blocks, "free_blocks", i32, (cap,), dev)
+    _check(free_count, "free_count", i32, (1,), dev)
+    _check(shares, "shares", i32, (nb,), dev)
+    _check(cached_lens, "cached_lens", i32, (B,), dev)
+    _fits(block_size)
+    return B, mb, cap, nb, dev
+
+
+def paged_fork(parents: torch.Tensor, children: torch.Tensor, block_size: int,
+               block_table: torch.Tensor, cached_lens: torch.Tensor, free_blocks: torch.Tensor,
+               free_count: torch.Tensor, shares: torch.Tensor,
+               fork_lens: Optional[torch.Tensor] = None, seq_lens: Optional[torch.Tensor] = None,
+               copy_src: Optional[torch.Tensor] = None, copy_dst: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None) -> PagedFork:
+    """mova_paged_fork: rows ``children`` of the block table begin with the
+    first ``fork_lens`` tokens (None: all) of rows ``parents`` (int32 [n]).
+
+    Full blocks are shared and counted in ``shares`` (int32 [num_blocks],
+    updated in place like ``block_table``); for a last block filled in part a
+    free one is taken, and ``copy_src`` and ``copy_dst`` name the two for
+    ``paged_copy`` (-1: nothing to copy).  The new lengths and count are new
+    tensors."""
+    lib = load_library()
+    (n,) = _dims(parents, "parents", 1, "[n]")
+    B, mb, cap, nb, dev = _upkeep(block_table, free_blocks, free_count, shares, cached_lens,
+                                  block_size)
+    _check(parents, "parents", torch.int32, (n,), dev)
+    _check(children, "children", torch.int32, (n,), dev)
+    if fork_lens is not None:
+        _check(fork_lens, "fork_lens", torch.int32, (n,), dev)
+    seq_lens = _given(seq_lens, "seq_lens", (B,), cached_lens)
+    copy_src = _given(copy_src, "copy_src", (n,), cached_lens)
+    copy_dst = _given(copy_dst, "copy_dst", (n,), cached_lens)
+    free_count_out = _given(free_count_out, "free_count_out", (1,), free_count)
+    _launch(lib.mova_paged_fork, "mova_paged_fork", dev, _ptr(parents), _ptr(children),
+            _ptr(fork_lens), n, _ptr(cached_lens), B, block_size, mb, _ptr(block_table),
+            _ptr(free_blocks), cap, _ptr(free_count), _ptr(free_count_out), _ptr(shares), nb,
+            _ptr(seq_lens), _ptr(copy_src), _ptr(copy_dst))
+    return PagedFork(seq_lens, copy_src, copy_dst, free_count_out)
+
+
+def paged_free(cached_lens: torch.Tensor, keep_lens: torch.Tensor, block_size: int,
+               block_table: torch.Tensor, free_blocks: torch.Tensor, free_count: torch.Tensor,
+               shares: torch.Tensor, seq_lens: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None) -> PagedFree:
+    """mova_paged_free: each row keeps its first ``keep_lens`` tokens (0 ends
+    the request) and lets go of the blocks behind them; a block's last holder
+    puts it on the free stack.  ``free_blocks`` and ``shares`` are updated in
+    place; the new lengths and count are new tensors.  A row that would be cut
+    inside a block that others hold too keeps its length."""
+    lib = load_library()
+    B, mb, cap, nb, dev = _upkeep(block_table, free_blocks, free_count, shares, cached_lens,
+                                  block_size)
+    _check(keep_lens, "keep_lens", torch.int32, (B,), dev)
+    seq_lens = _given(seq_lens, "seq_lens", (B,), cached_lens)
+    free_count_out = _given(free_count_out, "free_count_out", (1,), free_count)
+    _launch(lib.mova_paged_free, "mova_paged_free", dev, _ptr(cached_lens), _ptr(keep_lens), B,
+            block_size, mb, _ptr(block_table), _ptr(free_blocks), cap, _ptr(free_count),
+            _ptr(free_count_out), _ptr(shares), nb, _ptr(seq_lens))
+    return PagedFree(seq_lens, free_count_out)
+
+
+@functools.lru_cache(maxsize=64)
+def _compact_bytes(num_blocks: int) -> int:
+    return load_library().mova_paged_compact_workspace_bytes(num_blocks)
+
+
+def paged_compact(cached_lens: torch.Tensor, block_size: int, block_table: torch.Tensor,
+                  free_blocks: torch.Tensor, free_count: torch.Tensor, shares: torch.Tensor,
+                  limit: int = 0, block_table_out: Optional[torch.Tensor] = None,
+                  free_blocks_out: Optional[torch.Tensor] = None,
+                  shares_out: Optional[torch.Tensor] = None,
+                  remap: Optional[torch.Tensor] = None, move_src: Optional[torch.Tensor] = None,
+                  move_dst: Optional[torch.Tensor] = None,
+                  move_count: Optional[torch.Tensor] = None,
+                  free_count_out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> PagedCompact:
+    """mova_paged_compact: blocks in use at or above max(``limit``, their
+    number) go to the lowest free ones.  ``block_table``, ``free_blocks`` and
+    ``shares`` are updated in place unless other tensors are given for the new
+    ones; ``move_src``, ``move_dst`` and ``move_count`` are the list for
+    ``paged_copy``, ``remap`` gives every block's new place (-1: free)."""
+    lib = load_library()
+    B, mb, cap, nb, dev = _upkeep(block_table, free_blocks, free_count, shares, cached_lens,
+                                  block_size)
+    _fits(limit)
+    if block_table_out is None:
+        block_table_out = block_table
+    else:
+        _check(block_table_out, "block_table_out", torch.int32, (B, mb), dev)
+    if free_blocks_out is None:
+        free_blocks_out = free_blocks
+    else:
+        _check(free_blocks_out, "free_blocks_out", torch.int32, (cap,), dev)
+    if shares_out is None:
+        shares_out = shares
+    else:
+        _check(shares_out, "shares_out", torch.int32, (nb,), dev)
+    remap = _given(remap, "remap", (nb,), shares)
+    move_src = _given(move_src, "move_src", (nb // 2,), shares)
+    move_dst = _given(move_dst, "move_dst", (nb // 2,), shares)
+    move_count = _given(move_count, "move_count", (1,), free_count)
+    free_count_out = _given(free_count_out, "free_count_out", (1,), free_count)
+    workspace = _scratch(workspace, _compact_bytes(nb), "mova_paged_compact", dev)
+    _launch(lib.mova_paged_compact, "mova_paged_compact", dev, _ptr(cached_lens), B, block_size,
+            mb, _ptr(block_table), _ptr(block_table_out), _ptr(free_blocks), _ptr(free_blocks_out),
+            cap, _ptr(free_count), _ptr(free_count_out), _ptr(shares), _ptr(shares_out), nb, limit,
+            _ptr(remap), _ptr(move_src), _ptr(move_dst), _ptr(move_count), _ptr(workspace),
+            workspace.numel())
+    return PagedCompact(block_table_out, free_blocks_out, free_count_out, shares_out, remap,
+                        move_src, move_dst, move_count)
+
+
+def paged_copy(copy_src: torch.Tensor, copy_dst: torch.Tensor, k_cache: Optional[torch.Tensor],
+               v_cache: Optional[torch.Tensor] = None, k_bounds: Optional[torch.Tensor] = None,
+               count: Optional[torch.Tensor] = None) -> None:
+    """mova_paged_copy: block ``copy_dst[i]`` of each pool given becomes as
+    block ``copy_src[i]`` (int32 [n], as from ``paged_fork`` or
+    ``paged_compact``); pairs outside the pool, and those behind ``count``
+    (int32 [1], None: n), are passed over."""
+    lib = load_library()
+    (n,) = _dims(copy_src, "copy_src", 1, "[n]")
+    pool = k_cache if k_cache is not None else v_cache
+    if pool is None:
+        raise ValueError("neither keys nor values are given")
+    nb, bs, H, D = _dims(pool, "the pools", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")
+    dev = copy_src.device
+    dtype = CACHE_DTYPES.get(pool.dtype)
+    for p, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if p is not None and _check_pool(p, name, (nb, bs, H, D), dev) != dtype:
+            raise ValueError("the pools must have the same dtype")
+    _check(copy_src, "copy_src", torch.int32, (n,), dev)
+    _check(copy_dst, "copy_dst", torch.int32, (n,), dev)
+    if k_bounds is not None:
+        _check(k_bounds, "k_bounds", torch.bfloat16, (nb, H, 2, D), dev)
+    if count is not None:
+        _check(count, "count", torch.int32, (1,), dev)
+    _launch(lib.mova_paged_copy, "mova_paged_copy", dev, _ptr(copy_src), _ptr(copy_dst), n,
+            _ptr(count), _ptr(k_cache), _ptr(v_cache), _ptr(k_bounds), dtype, nb, bs, H, D)
 
 
 # Kernel-choice overrides (mova_debug_override): name -> (key, {value name: value}).

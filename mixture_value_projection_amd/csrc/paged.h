@@ -100,7 +100,122 @@ struct AttentionArgs {
 size_t attention_scratch_floats(int B, int Hq, int H, int D);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t stream);
 
+struct ChunkArgs {
+  const __bf16* q;  // [T, Hq, D]
+  const void* k_cache;
+  const void* v_cache;
+  int dtype;
+  const float* k_scale;  // [H] or null
+  const float* v_scale;
+  int num_blocks, block_size;
+  const int32_t* table;  // [B, max_blocks]
+  int max_blocks;
+  const int32_t* cached;    // [B]
+  const int32_t* seq_lens;  // [B]
+  const int32_t* cu_new;    // [B + 1]
+  int T, B, Hq, H, D;
+  float scale;
+  int window;  // 0: none
+  __bf16* out;  // [T, Hq, D]
+  float* lse;   // [T, Hq] or null
+  float* part;  // scratch of chunk_scratch_floats
+};
+// Floats of scratch; depends on the sizes alone.
+size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D);
+hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream);
+
+// Blocks of a pool whose upkeep is done here (a bit of each in LDS).
+constexpr int kMaxUpkeepBlocks = 1 << 20;
+
+struct CopyArgs {
+  const int32_t* src;    // [n]
+  const int32_t* dst;    // [n]
+  const int32_t* count;  // [1] or null (n)
+  int n;
+  u32x4* pool[3];  // keys, values, bounds; null: none
+  int pieces[3];   // 16-byte pieces of a block of each, 0: none
+  int num_blocks;
+};
+hipError_t launch_paged_copy(const CopyArgs& a, hipStream_t stream);
+
+struct ForkArgs {
+  const int32_t* parents;   // [n]
+  const int32_t* children;  // [n]
+  const int32_t* take;      // [n] or null: all of the parent's tokens
+  int n;
+  const int32_t* cached;  // [B]
+  int B, block_size, max_blocks;
+  int32_t* table;              // [B, max_blocks]
+  const int32_t* free_blocks;  // [free_capacity], a stack
+  int free_capacity;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* shares;  // [num_blocks]
+  int num_blocks;
+  int32_t* seq_lens;  // [B]
+  int32_t* copy_src;  // [n]
+  int32_t* copy_dst;  // [n]
+};
+hipError_t launch_paged_fork(const ForkArgs& a, hipStream_t stream);
+
+struct FreeArgs {
+  const int32_t* cached;  // [B]
+  const int32_t* keep;    // [B]
+  int B, block_size, max_blocks;
+  const int32_t* table;  // [B, max_blocks]
+  int32_t* free_blocks;  // [free_capacity], a stack
+  int free_capacity;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* shares;  // [num_blocks]
+  int num_blocks;
+  int32_t* seq_lens;  // [B]
+};
+hipError_t launch_paged_free(const FreeArgs& a, hipStream_t stream);
+
+struct CompactArgs {
+  const int32_t* lens;  // [B]
+  int B, block_size, max_blocks;
+  const int32_t* table;  // [B, max_blocks]
+  int32_t* table_out;
+  const int32_t* free_blocks;  // [free_capacity], a stack
+  int32_t* free_out;
+  int free_capacity;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  const int32_t* shares;  // [num_blocks]
+  int32_t* shares_out;
+  int num_blocks, limit;
+  int32_t* remap;     // [num_blocks]
+  int32_t* move_src;  // [num_blocks / 2]
+  int32_t* move_dst;  // [num_blocks / 2]
+  int32_t* move_count;
+  uint32_t* scratch;  // compact_scratch_words
+};
+// Scratch, in 4-byte words: free blocks before each run of kRankBlocks, their
+// number in all, then a bit a block.
+constexpr int kRankBlocks = 256;
+__host__ __device__ constexpr int compact_groups(int num_blocks) {
+  return (num_blocks + kRankBlocks - 1) / kRankBlocks;
+}
+inline size_t compact_scratch_words(int num_blocks) {
+  return (size_t)compact_groups(num_blocks) * (1 + kRankBlocks / 32) + 1;
+}
+hipError_t launch_paged_compact(const CompactArgs& a, hipStream_t stream);
+
 // ---- device helpers ---------------------------------------------------------
+
+// The last i in [0, n) with a[i] <= x (a[0] <= x, a not decreasing).
+template <class X>
+__device__ __forceinline__ int last_at_most(const X* a, int n, X x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 
 // n / d for 0 <= n < 2^31 as a product and a shift (d > 0).  With
 // s = ceil(log2 d), mul = floor(2^(31 + s) / d) + 1 exceeds 2^(31 + s) / d by at

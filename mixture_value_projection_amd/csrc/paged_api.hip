@@ -67,6 +67,26 @@ int check_attention(int B, int n_heads, int n_kv_heads, int head_dim, int max_bl
   return (long long)keep * block_size > kMaxLen ? MOVA_ERR_UNSUPPORTED : MOVA_OK;
 }
 
+int check_chunk(int T, int B, int n_heads, int n_kv_heads, int head_dim, int max_blocks,
+                int block_size) {
+  if (T < 0) return MOVA_ERR_INVALID_ARG;
+  int rc = check_table(B, max_blocks, block_size);
+  if (rc != MOVA_OK) return rc;
+  rc = check_read_heads(n_heads, n_kv_heads, head_dim);
+  if (rc != MOVA_OK) return rc;
+  return T > kMaxT ? MOVA_ERR_UNSUPPORTED : MOVA_OK;
+}
+
+// Pools whose blocks the upkeep counts.
+int check_upkeep(int B, int max_blocks, int block_size, int num_blocks, int free_capacity) {
+  const int rc = check_table(B, max_blocks, block_size);
+  if (rc != MOVA_OK) return rc;
+  if (num_blocks < 0 || free_capacity < 0) return MOVA_ERR_INVALID_ARG;
+  return num_blocks > kMaxUpkeepBlocks ? MOVA_ERR_UNSUPPORTED : MOVA_OK;
+}
+
+size_t compact_bytes(int num_blocks) { return align256(4 * compact_scratch_words(num_blocks)); }
+
 size_t select_bytes(int B, int n_kv_heads, int max_blocks) {
   return align256(8 * select_scratch_words(B, n_kv_heads, max_blocks));
 }
@@ -207,6 +227,167 @@ int mova_attention_paged(const void* q, const void* k_cache, const void* v_cache
                         keep, B, n_heads, n_kv_heads, head_dim, scale, window, (__bf16*)out, lse,
                         (float*)workspace};
   return launch_attention(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
+}
+
+size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_heads,
+                                            int head_dim, int max_blocks, int block_size) {
+  if (check_chunk(T, B, n_heads, n_kv_heads, head_dim, max_blocks, block_size) != MOVA_OK)
+    return (size_t)-1;
+  return align256(4 * chunk_scratch_floats(T, B, n_heads, n_kv_heads, head_dim));
+}
+
+int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v_cache,
+                               int cache_dtype, const float* k_scale, const float* v_scale,
+                               int num_blocks, int block_size, const int32_t* block_table,
+                               int max_blocks, const int32_t* cached_lens, const int32_t* seq_lens,
+                               const int32_t* cu_new, int T, int B, int n_heads, int n_kv_heads,
+                               int head_dim, float scale, int window, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_chunk(T, B, n_heads, n_kv_heads, head_dim, max_blocks, block_size);
+  if (rc != MOVA_OK) return rc;
+  rc = check_pool(num_blocks, block_size);
+  if (rc != MOVA_OK) return rc;
+  rc = check_dtype(cache_dtype, k_scale, v_scale);
+  if (rc != MOVA_OK) return rc;
+  if (window < 0) return MOVA_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return MOVA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return MOVA_OK;
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_table == nullptr ||
+      cached_lens == nullptr || seq_lens == nullptr || cu_new == nullptr || out == nullptr)
+    return MOVA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_table, 4) || !aligned(cached_lens, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_new, 4) || !aligned(out, 16) || !aligned(lse, 4))
+    return MOVA_ERR_INVALID_ARG;
+  const size_t need = mova_attention_chunk_workspace_bytes(T, B, n_heads, n_kv_heads, head_dim,
+                                                           max_blocks, block_size);
+  rc = check_workspace(workspace, workspace_bytes, need);
+  if (rc != MOVA_OK) return rc;
+  const ChunkArgs a{(const __bf16*)q, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_blocks,
+                    block_size, block_table, max_blocks, cached_lens, seq_lens, cu_new, T, B,
+                    n_heads, n_kv_heads, head_dim, scale, window, (__bf16*)out, lse,
+                    (float*)workspace};
+  return launch_chunk_attention(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
+}
+
+int mova_paged_copy(const int32_t* copy_src, const int32_t* copy_dst, int n,
+                    const int32_t* copy_count, void* k_cache, void* v_cache, void* k_bounds,
+                    int cache_dtype, int num_blocks, int block_size, int n_kv_heads, int head_dim,
+                    hipStream_t stream) {
+  if (n < 0 || num_blocks < 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+    return MOVA_ERR_INVALID_ARG;
+  // A block's bytes in 16-byte pieces stay within 32 bits.
+  if (head_dim % 16 != 0 || (long long)n_kv_heads * head_dim > (1 << 14) ||
+      block_size > (1 << 18) || (long long)num_blocks * block_size > kMaxSlots)
+    return MOVA_ERR_UNSUPPORTED;
+  const int rc = check_dtype(cache_dtype, nullptr, nullptr);
+  if (rc != MOVA_OK) return rc;
+  if (n == 0) return MOVA_OK;
+  if (copy_src == nullptr || copy_dst == nullptr ||
+      (k_cache == nullptr && v_cache == nullptr && k_bounds == nullptr))
+    return MOVA_ERR_INVALID_ARG;
+  if (!aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(copy_count, 4) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_bounds, 16))
+    return MOVA_ERR_INVALID_ARG;
+  const int width = n_kv_heads * head_dim;
+  const int rows = block_size * (width / (cache_dtype == MOVA_CACHE_FP8 ? 16 : 8));
+  const CopyArgs a{copy_src, copy_dst, copy_count, n,
+                   {(u32x4*)k_cache, (u32x4*)v_cache, (u32x4*)k_bounds},
+                   {k_cache == nullptr ? 0 : rows, v_cache == nullptr ? 0 : rows,
+                    k_bounds == nullptr ? 0 : width / 4},
+                   num_blocks};
+  return launch_paged_copy(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
+}
+
+int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32_t* fork_lens,
+                    int n, const int32_t* cached_lens, int B, int block_size, int max_blocks,
+                    int32_t* block_table, const int32_t* free_blocks, int free_capacity,
+                    const int32_t* free_count, int32_t* free_count_out, int32_t* shares,
+                    int num_blocks, int32_t* seq_lens, int32_t* copy_src, int32_t* copy_dst,
+                    hipStream_t stream) {
+  const int rc = check_upkeep(B, max_blocks, block_size, num_blocks, free_capacity);
+  if (rc != MOVA_OK) return rc;
+  if (n < 0) return MOVA_ERR_INVALID_ARG;
+  if (n > kMaxRequests) return MOVA_ERR_UNSUPPORTED;
+  if ((B > 0 && (cached_lens == nullptr || block_table == nullptr || seq_lens == nullptr)) ||
+      (n > 0 && (parents == nullptr || children == nullptr || copy_src == nullptr ||
+                 copy_dst == nullptr)) ||
+      free_count == nullptr || free_count_out == nullptr ||
+      (free_capacity > 0 && free_blocks == nullptr) || (num_blocks > 0 && shares == nullptr))
+    return MOVA_ERR_INVALID_ARG;
+  if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(fork_lens, 4) ||
+      !aligned(cached_lens, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) ||
+      !aligned(free_count, 4) || !aligned(free_count_out, 4) || !aligned(shares, 4) ||
+      !aligned(seq_lens, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4))
+    return MOVA_ERR_INVALID_ARG;
+  // Every workgroup reads these while one of them writes the others.
+  if (free_count == free_count_out || (B > 0 && cached_lens == seq_lens))
+    return MOVA_ERR_INVALID_ARG;
+  const ForkArgs a{parents, children, fork_lens, n, cached_lens, B, block_size, max_blocks,
+                   block_table, free_blocks, free_capacity, free_count, free_count_out, shares,
+                   num_blocks, seq_lens, copy_src, copy_dst};
+  return launch_paged_fork(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
+}
+
+int mova_paged_free(const int32_t* cached_lens, const int32_t* keep_lens, int B, int block_size,
+                    int max_blocks, const int32_t* block_table, int32_t* free_blocks,
+                    int free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                    int32_t* shares, int num_blocks, int32_t* seq_lens, hipStream_t stream) {
+  const int rc = check_upkeep(B, max_blocks, block_size, num_blocks, free_capacity);
+  if (rc != MOVA_OK) return rc;
+  if ((B > 0 && (cached_lens == nullptr || keep_lens == nullptr || block_table == nullptr ||
+                 seq_lens == nullptr)) ||
+      free_count == nullptr || free_count_out == nullptr ||
+      (free_capacity > 0 && free_blocks == nullptr) || (num_blocks > 0 && shares == nullptr))
+    return MOVA_ERR_INVALID_ARG;
+  if (!aligned(cached_lens, 4) || !aligned(keep_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(free_blocks, 4) || !aligned(free_count, 4) || !aligned(free_count_out, 4) ||
+      !aligned(shares, 4) || !aligned(seq_lens, 4))
+    return MOVA_ERR_INVALID_ARG;
+  if (free_count == free_count_out ||
+      (B > 0 && (cached_lens == seq_lens || keep_lens == seq_lens)))
+    return MOVA_ERR_INVALID_ARG;
+  const FreeArgs a{cached_lens, keep_lens, B, block_size, max_blocks, block_table, free_blocks,
+                   free_capacity, free_count, free_count_out, shares, num_blocks, seq_lens};
+  return launch_paged_free(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
+}
+
+size_t mova_paged_compact_workspace_bytes(int num_blocks) {
+  if (num_blocks < 0 || num_blocks > kMaxUpkeepBlocks) return (size_t)-1;
+  return compact_bytes(num_blocks);
+}
+
+int mova_paged_compact(const int32_t* cached_lens, int B, int block_size, int max_blocks,
+                       const int32_t* block_table, int32_t* block_table_out,
+                       const int32_t* free_blocks, int32_t* free_blocks_out, int free_capacity,
+                       const int32_t* free_count, int32_t* free_count_out, const int32_t* shares,
+                       int32_t* shares_out, int num_blocks, int limit, int32_t* remap,
+                       int32_t* move_src, int32_t* move_dst, int32_t* move_count, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_upkeep(B, max_blocks, block_size, num_blocks, free_capacity);
+  if (rc != MOVA_OK) return rc;
+  if (limit < 0) return MOVA_ERR_INVALID_ARG;
+  if ((B > 0 &&
+       (cached_lens == nullptr || block_table == nullptr || block_table_out == nullptr)) ||
+      free_count == nullptr || free_count_out == nullptr || move_count == nullptr ||
+      (free_capacity > 0 && (free_blocks == nullptr || free_blocks_out == nullptr)) ||
+      (num_blocks > 0 && (shares == nullptr || shares_out == nullptr || remap == nullptr)) ||
+      (num_blocks > 1 && (move_src == nullptr || move_dst == nullptr)))
+    return MOVA_ERR_INVALID_ARG;
+  if (!aligned(cached_lens, 4) || !aligned(block_table, 4) || !aligned(block_table_out, 4) ||
+      !aligned(free_blocks, 4) || !aligned(free_blocks_out, 4) || !aligned(free_count, 4) ||
+      !aligned(free_count_out, 4) || !aligned(shares, 4) || !aligned(shares_out, 4) ||
+      !aligned(remap, 4) || !aligned(move_src, 4) || !aligned(move_dst, 4) ||
+      !aligned(move_count, 4))
+    return MOVA_ERR_INVALID_ARG;
+  if (free_count == free_count_out) return MOVA_ERR_INVALID_ARG;
+  rc = check_workspace(workspace, workspace_bytes, compact_bytes(num_blocks));
+  if (rc != MOVA_OK) return rc;
+  const CompactArgs a{cached_lens, B, block_size, max_blocks, block_table, block_table_out,
+                      free_blocks, free_blocks_out, free_capacity, free_count, free_count_out,
+                      shares, shares_out, num_blocks, limit, remap, move_src, move_dst, move_count,
+                      (uint32_t*)workspace};
+  return launch_paged_compact(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
 }
 
 }  // extern "C"

@@ -31,17 +31,6 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 
-// The last i in [0, n) with a[i] <= x (a[0] <= x, a not decreasing).
-__device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ int clamp_int(long long v) {
   return (int)min(v, (long long)0x7fffffff);
 }
