@@ -583,8 +583,8 @@ size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_
  * key's weight is below 2^-126 of the row's largest.  Products accumulate in
  * fp32 and the softmax's maximum and sum are fp32.  Results are bitwise
  * reproducible for identical inputs; how a row's keys are split, and so its
- * last bits, depends on the lengths of the whole batch.  T <= 2^24, scale
- * finite.  out and lse overlap no input.
+ * last bits, depends on the lengths of the whole batch.  T <= 2^24, T * n_heads *
+ * max_blocks * block_size <= 2^52, scale finite.  out and lse overlap no input.
  */
 int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v_cache,
                                int cache_dtype, const float* k_scale, const float* v_scale,

@@ -3,15 +3,19 @@
 //
 //   out_ti = sum_p exp(s_tip - m_ti) v_p / sum_p exp(s_tip - m_ti),  s_tip = scale q_ti . k_p
 //
-// over the positions p up to the token's own.
+// over the positions p up to the token's own, in one pass over the keys with the
+// running maximum m and sum of a softmax.
 #include <algorithm>
+#include <atomic>
 
+#include "kernels.h"
 #include "paged.h"
 
 namespace mova {
 
 namespace {
 
+constexpr int kCus = 256;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // Request b's rows of the packed tokens and positions in the cache.
@@ -54,13 +58,240 @@ __device__ __forceinline__ float load1(const void* pool, size_t at) {
   else return (float)((const bf16_t*)pool)[at];
 }
 
-// One row by one wave, a lane a key for the logits and D / 64 channels a lane for
-// the values: the maximum first, then weights and sums.  Only keys that take part
-// are touched, whatever lies in the others.
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+
+template <int D, bool kFp8>
+struct Tile {
+  static constexpr int kWaves = D == 256 ? 4 : 8;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kRows = 32 * kWaves;            // rows (token and query head) of a workgroup
+  static constexpr int kKeys = D == 256 ? 32 : 64;     // of a tile
+  static constexpr int kParts = kKeys / 32;
+  static constexpr int kRow = 2 * D;                   // bytes of a key in LDS
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kSide = kKeys * kRow;           // bytes of a side (K or V)
+  static constexpr int kStage = 2 * kSide + 64;        // with a byte a key: whether it is there
+  static constexpr bool kQueriesInLds = D == 256;
+  static constexpr int kQueries = kQueriesInLds ? kRows * kRow : 0;
+  static constexpr int kLds = kQueries + 2 * kStage;
+  // Staging: a thread moves kLoads 16-byte pieces of the pool a side.
+  static constexpr int kPieces = D * (kFp8 ? 1 : 2) / 16;  // of a key
+  static constexpr int kTotal = kKeys * kPieces;
+  static constexpr int kLoads = (kTotal + kThreads - 1) / kThreads;
+  static constexpr int kStep = kThreads / kPieces;         // keys between a thread's pieces
+  // 8-bit values are multiplied as fp16, with weights up to 2^kLift rather than 1
+  // so that the small ones keep their bits.
+  static constexpr float kLift = kFp8 ? 14.f : 0.f;
+  // Sums are brought to a new maximum once it is this much higher (in powers of two).
+  static constexpr float kSlack = kFp8 ? 1.f : 8.f;
+  // Piece c of key r lies at piece c ^ swizzle(r).
+  static __device__ __forceinline__ int swizzle_k(int r) { return r & (kChunks - 1) & 15; }
+  static __device__ __forceinline__ int swizzle_v(int r) {
+    constexpr int kShare = kChunks >= 16 ? 1 : 16 / kChunks;
+    return (2 * (r / kShare)) & (kChunks - 1) & 15;
+  }
+};
+
+// How the rows of a request and key head are cut: blocks of `tokens` tokens with
+// `heads` of the query heads.
+struct Cut {
+  int tokens, heads, head_blocks;
+};
+Cut cut_of(int G, int rows) {
+  Cut c;
+  c.head_blocks = ceil_div(G, rows);
+  c.heads = ceil_div(G, c.head_blocks);
+  c.tokens = std::max(1, rows / c.heads);
+  return c;
+}
+
+// What a request brings to the line of work, in keys: each of its row tiles reads
+// keys [lo, hi), and kFixed more for what a tile costs beside them.
+constexpr int kFixed = 128;
+// A stretch of the line is at least this long.
+constexpr int kLeastStretch = 512;
+struct Load {
+  int at, live, tokens, window;
+  __device__ __forceinline__ int tiles() const { return ceil_div(live, tokens); }
+  __device__ __forceinline__ int hi(int k) const {
+    return at + min(live, (int)min((long long)(k + 1) * tokens, (long long)live));
+  }
+  __device__ __forceinline__ int lo(int k) const {
+    return window > 0 ? max(0, at + k * tokens + 1 - window) : 0;
+  }
+  __device__ __forceinline__ long long units(int k) const { return hi(k) - lo(k) + kFixed; }
+  // Units of tiles 0 .. n - 1.
+  __device__ __forceinline__ long long before(int n) const {
+    const long long N = n, s = tokens;
+    long long sum = N * ((long long)at + kFixed) + s * (N * (N + 1) / 2);
+    if (n > 0 && n == tiles()) sum -= N * s - live;
+    if (window > 0) {
+      const int first = window - 1 - at < 0 ? 0 : (window - 1 - at) / tokens + 1;
+      if (first < n) {
+        const long long m = n - first;
+        sum -= m * ((long long)at + 1 - window) + s * ((long long)(n - 1 + first) * m / 2);
+      }
+    }
+    return sum;
+  }
+  // The tile that unit x (< before(tiles())) lies in.
+  __device__ __forceinline__ int tile_at(long long x) const {
+    int lo_ = 0, hi_ = tiles();
+    while (hi_ - lo_ > 1) {
+      const int mid = (lo_ + hi_) >> 1;
+      if (before(mid) <= x) lo_ = mid;
+      else hi_ = mid;
+    }
+    return lo_;
+  }
+};
+__device__ __forceinline__ Load load_of(const ChunkArgs& a, int tokens, int b) {
+  const Chunk c = chunk_of(a, b);
+  return Load{c.at, c.live, tokens, a.window};
+}
+
+// Key tiles [begin, end) of a row tile that units [x0, x1) of it stand for; all
+// of them together are [first, last).
+struct Segment {
+  int begin, end, first, last;
+};
+template <int kKeys>
+__device__ __forceinline__ Segment segment_of(const Load& w, int k, long long x0, long long x1) {
+  const int lo = w.lo(k), hi = w.hi(k);
+  const long long units = hi - lo + kFixed;
+  Segment s;
+  s.first = lo / kKeys;
+  s.last = ceil_div(hi, kKeys);
+  auto at = [&](long long x) {
+    if (x <= 0) return s.first;
+    if (x >= units) return s.last;
+    return (lo + (int)max(x - kFixed, 0ll)) / kKeys;
+  };
+  s.begin = at(x0);
+  s.end = at(x1);
+  return s;
+}
+
+// Parts of rows that were split over stretches: two for each workgroup, of the
+// tile that its stretch begins in and of the one that it ends in.
+struct Parts {
+  long long* prefix;  // [B] first unit of each request, then the stretch
+  float* ml;          // [two a workgroup][rows][2] maximum (in powers of two) and sum
+  float* o;           // [two a workgroup][rows][D] out
+};
+size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
+
+struct Shared {
+  long long tmp[8];
+  long long first;
+  int b;
+};
+// As line_begin, for workgroups of kWaves waves.  `slot`: which stretch.
+template <int kWaves, class Cost>
+__device__ __forceinline__ bool chunk_line(int B, int slot, int slots, Cost cost, Shared& sh,
+                                           long long* prefix, Line* line) {
+  constexpr int kThreads = 64 * kWaves;
+  const int per = ceil_div(B, kThreads);
+  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += cost(b);
+  long long before = block_exclusive_scan<kWaves>(mine, sh.tmp, &total);
+  line->stretch = max(floor_div(total + slots - 1, slots), (long long)kLeastStretch);
+  line->start = line->stretch * slot;
+  line->end = min(line->start + line->stretch, total);
+  if (before <= line->start && line->start < before + mine) {
+    long long at = before;
+    int b = b0;
+    for (long long c; line->start >= at + (c = cost(b)); ++b) at += c;
+    sh.b = b;
+    sh.first = at;
+  }
+  if (prefix != nullptr && slot == 0) {
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = before;
+      before += cost(b);
+    }
+    if (threadIdx.x == 0) prefix[B] = line->stretch;
+  }
+  __syncthreads();
+  if (line->start >= total) return false;
+  line->b = __builtin_amdgcn_readfirstlane(sh.b);
+  line->first = (long long)read_lane((double)sh.first, 0);
+  return true;
+}
+
+// Maximum of lanes i and i + 32, in both.
+__device__ __forceinline__ float max_of_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
+// 16 e4m3 elements as bf16 or fp16 (both exact).
+template <bool kHalf>
+__device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
+  auto two = [](uint32_t x, auto upper) {
+    if constexpr (kHalf)
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(
+                                              (int)x, 1.f, decltype(upper)::value));
+    else
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                              (int)x, 1.f, decltype(upper)::value));
+  };
+  using std::false_type;
+  using std::true_type;
+  *a = u32x4{two(w[0], false_type{}), two(w[0], true_type{}), two(w[1], false_type{}),
+             two(w[1], true_type{})};
+  *b = u32x4{two(w[2], false_type{}), two(w[2], true_type{}), two(w[3], false_type{}),
+             two(w[3], true_type{})};
+}
+
+// Where a row's result goes: its place in the output, or in the parts.
+template <int D>
+struct Sink {
+  bf16_t* out;  // null: the parts
+  float* lse;   // null: none
+  float* o;
+  float* ml;
+  // 4 channels from c on, of values already divided by the sum.
+  __device__ __forceinline__ void put4(int c, f32x4 y) const {
+    if (out != nullptr) {
+      uint2 w;
+      w.x = (uint32_t)f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16);
+      w.y = (uint32_t)f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16);
+      *reinterpret_cast<uint2*>(out + c) = w;
+    } else {
+      *reinterpret_cast<f32x4*>(o + c) = y;
+    }
+  }
+  __device__ __forceinline__ void put1(int c, float y) const {
+    if (out != nullptr) out[c] = (bf16_t)y;
+    else o[c] = y;
+  }
+  // m: the maximum in powers of two, l: the sum of exp2(. - m).
+  __device__ __forceinline__ void put_sum(float m, float l) const {
+    if (out == nullptr) {
+      ml[0] = m;
+      ml[1] = l;
+    } else if (lse != nullptr) {
+      *lse = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+  }
+};
+
+// One row by one wave with everything in fp32, a lane a key for the logits and
+// D / 64 channels a lane for the values: the maximum first, then weights and
+// sums.  Only keys that take part are touched, so infinite and NaN values of
+// others do not show, and sums that pass the largest number are formed with
+// weights 2^-32 as large (a row has at most 2^30 keys).  For the rows whose sums
+// the matrix products left infinite or NaN.
 template <int D, bool kFp8>
 __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block, int b, int h,
-                                           size_t qrow, int lo, int hi) {
+                                           size_t qrow, int lo, int hi, const Sink<D>& sink) {
   constexpr int kPer = D / 64;
+  constexpr float kDown = 0x1p-32f;
   const int lane = threadIdx.x & 63;
   const bf16_t* q = a.q + qrow * D;
   const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
@@ -75,7 +306,7 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
   };
   auto logit = [&](long long at) {
     float s = 0.f;
-#pragma unroll 4
+#pragma unroll 1
     for (int d = 0; d < D; d += 8) {
       float k[8], x[8];
       load8<kFp8>(a.k_cache, (size_t)at + d, k);
@@ -93,15 +324,13 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
   }
   m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
   const float safe = m == -__builtin_huge_valf() ? 0.f : m;
-  // Sums that pass the largest number are taken from those of weights 2^-32 as
-  // large, which cannot (a row has at most 2^30 keys).
-  constexpr float kDown = 0x1p-32f;
   float l = 0.f, o[kPer] = {}, less[kPer] = {};
 #pragma unroll 1
   for (int p = lo; p < hi; p += 64) {
     const long long at = place(p + lane);
     const float w = at >= 0 ? __builtin_amdgcn_exp2f(logit(at) - safe) : 0.f;
     l += w;
+#pragma unroll 1
     for (uint64_t there = __ballot(at >= 0); there != 0; there &= there - 1) {
       const int i = __ffsll((unsigned long long)there) - 1;
       const float wi = __shfl(w, i);
@@ -119,53 +348,458 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const float y = fabsf(o[j]) < __builtin_huge_valf() ? o[j] * f : less[j] * (f / kDown);
-    a.out[qrow * D + lane * kPer + j] = (bf16_t)(l == 0.f ? 0.f : y);
+    sink.put1(lane * kPer + j, l == 0.f ? 0.f : y);
   }
-  if (a.lse != nullptr && lane == 0)
-    a.lse[qrow] = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  if (lane == 0) sink.put_sum(m, l);
 }
 
 }  // namespace
 
-// A wave a row and query head.
 template <int D, bool kFp8>
-__global__ __launch_bounds__(256) void chunk_row_kernel(ChunkArgs a, FastDiv by_block) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long long items = (long long)a.T * a.Hq;
-  for (long long item = (long long)blockIdx.x * 4 + wave; item < items;
-       item += (long long)gridDim.x * 4) {
-    const int t = (int)floor_div(item, a.Hq), hq = (int)(item - (long long)t * a.Hq);
-    if (t >= min(a.cu_new[a.B], a.T) || t < a.cu_new[0]) continue;
-    const int b = __builtin_amdgcn_readfirstlane(last_at_most(a.cu_new, a.B, t));
-    const Chunk c = chunk_of(a, b);
-    const int i = t - c.row0;
-    const int end = i < c.live ? c.at + i + 1 : 0;
-    const int lo = a.window > 0 ? max(0, end - a.window) : 0;
-    attend_row<D, kFp8>(a, by_block, b, hq / (a.Hq / a.H), (size_t)item, lo, end);
+__global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_kernel(
+    ChunkArgs a, Parts parts, FastDiv by_block, Cut cut, FastDiv by_heads) {
+  using T = Tile<D, kFp8>;
+  constexpr int kSteps = D / 16;    // products along the channels
+  constexpr int kBlocks = D / 32;   // 32-channel blocks of the output
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  __shared__ Shared s_line;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, half = lane >> 5;
+  const int G = a.Hq / a.H;
+  const int jobs = a.H * cut.head_blocks;  // of a row tile
+  // Neighbouring stretches on one XCD, whose workgroups then read the same keys.
+  const int slots = gridDim.x;
+  const int slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
+  char* stages = lds + T::kQueries;
+
+  auto cost = [&](int b) {
+    const Load w = load_of(a, cut.tokens, b);
+    return w.live == 0 ? 0ll : jobs * w.before(w.tiles());
+  };
+  Line line;
+  const bool work = chunk_line<T::kWaves>(a.B, slot, slots, cost, s_line, parts.prefix, &line);
+
+  // This thread's pieces of a tile.
+  const int my_key = tid / T::kPieces, my_piece = tid % T::kPieces;
+  const bool my_load = T::kTotal >= T::kThreads || tid < T::kTotal;
+
+  int b = line.b;
+  long long first = line.first;  // first unit of request b
+  if (work) {
+    Chunk ch = chunk_of(a, b);
+    Load w{ch.at, ch.live, cut.tokens, a.window};
+    long long units = w.live == 0 ? 0 : w.before(w.tiles());
+    for (long long pos = line.start; pos < line.end;) {
+      while (pos >= first + jobs * units) {
+        first += jobs * units;
+        if (++b >= a.B) break;
+        ch = chunk_of(a, b);
+        w = Load{ch.at, ch.live, cut.tokens, a.window};
+        units = w.live == 0 ? 0 : w.before(w.tiles());
+      }
+      if (b >= a.B) break;
+      const int job = (int)floor_div(pos - first, units);
+      const long long in_job = pos - first - job * units;
+      const int k = w.tile_at(in_job);
+      const long long x0 = in_job - w.before(k), size = w.units(k);
+      const long long x1 = min(size, x0 + (line.end - pos));
+      pos += x1 - x0;
+      const Segment seg = segment_of<T::kKeys>(w, k, x0, x1);
+      if (seg.begin >= seg.end) continue;
+      const bool all = seg.begin == seg.first && seg.end == seg.last;
+      const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
+      const int len = w.at + w.live;  // keys in all
+      const int32_t* table = a.table + (size_t)b * a.max_blocks;
+
+      // The lane's row: its token and query head.
+      const int r = wave * 32 + r32;
+      const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
+      const int token = k * cut.tokens + ti;
+      const bool live = ti < cut.tokens && token < w.live && xb * cut.heads + hi < G;
+      const size_t qrow =
+          (size_t)(ch.row0 + token) * a.Hq + (size_t)h * G + xb * cut.heads + hi;
+      // Rows without a token see what is there, with queries of 0.
+      const int limit = live ? w.at + token : 0x3fffffff;
+      const int lower = live && a.window > 0 ? max(0, limit + 1 - a.window) : 0;
+      auto imax = [](int x, int y) { return max(x, y); };
+      auto imin = [](int x, int y) { return min(x, y); };
+      const int most_limit = wave_reduce(live ? limit : -1, imax);
+      const int least_limit = wave_reduce(limit, imin);
+      const int least_lower = wave_reduce(live ? lower : 0x3fffffff, imin);
+      const int most_lower = wave_reduce(lower, imax);
+
+      // Queries; a negative scale goes into their signs.
+      const float ks = a.k_scale != nullptr ? a.k_scale[h] : 1.f;
+      const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
+      const float signed_qs = a.scale * ks * kLog2e;
+      const float qs = fmaxf(fabsf(signed_qs), 0x1p-126f);  // logits in powers of two
+      const uint32_t flip = signed_qs < 0.f ? 0x80008000u : 0u;
+      Frag16 qf[T::kQueriesInLds ? 1 : kSteps];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        Frag16 x;
+        x.u = u32x4{0u, 0u, 0u, 0u};
+        if (live) x.u = load16(a.q + qrow * D + 16 * u + 8 * half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.u[i] ^= flip;
+        if constexpr (T::kQueriesInLds)
+          store16(lds + (size_t)r * T::kRow + (((2 * u + half) ^ T::swizzle_k(r)) * 16), x.u);
+        else
+          qf[u] = x;
+      }
+
+      // Staging: block numbers a tile ahead of the keys and values, those a tile
+      // ahead of the products.
+      int page[T::kLoads];
+      u32x4 kreg[T::kLoads], vreg[T::kLoads];
+      bool there[T::kLoads];
+      auto fetch_pages = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+          const int p = j * T::kKeys + my_key + i * T::kStep;
+          page[i] = my_load && p < len ? table[fast_div(p, by_block)] : -1;
+        }
+      };
+      auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+          const int p = j * T::kKeys + my_key + i * T::kStep;
+          there[i] = page[i] >= 0 && page[i] < a.num_blocks;
+          const int row = p - fast_div(p, by_block) * a.block_size;
+          const size_t s = there[i] ? (size_t)page[i] * a.block_size + row : 0;
+          const size_t off = (s * a.H + h) * (T::kPieces * 16) + my_piece * 16;
+          kreg[i] = load16((const char*)a.k_cache + off);
+          vreg[i] = load16((const char*)a.v_cache + off);
+        }
+      };
+      auto stage = [&](int j) {
+        char* to = stages + (j & 1) * T::kStage;
+        if (!my_load) return;
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+          const int key = my_key + i * T::kStep;
+          char* krow = to + key * T::kRow;
+          char* vrow = krow + T::kSide;
+          const u32x4 none = {0u, 0u, 0u, 0u};
+          if constexpr (kFp8) {
+            u32x4 lo16, hi16;
+            widen16<false>(there[i] ? kreg[i] : none, &lo16, &hi16);
+            store16(krow + (((2 * my_piece) ^ T::swizzle_k(key)) * 16), lo16);
+            store16(krow + (((2 * my_piece + 1) ^ T::swizzle_k(key)) * 16), hi16);
+            widen16<true>(there[i] ? vreg[i] : none, &lo16, &hi16);
+            store16(vrow + (((2 * my_piece) ^ T::swizzle_v(key)) * 16), lo16);
+            store16(vrow + (((2 * my_piece + 1) ^ T::swizzle_v(key)) * 16), hi16);
+          } else {
+            store16(krow + ((my_piece ^ T::swizzle_k(key)) * 16), there[i] ? kreg[i] : none);
+            store16(vrow + ((my_piece ^ T::swizzle_v(key)) * 16), there[i] ? vreg[i] : none);
+          }
+          if (my_piece == 0) to[2 * T::kSide + key] = there[i];
+        }
+      };
+
+      f32x16 o[kBlocks];
+#pragma unroll
+      for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c][i] = 0.f;
+      float m = -__builtin_huge_valf(), l = 0.f;  // m: of the products, not scaled
+
+      fetch_pages(seg.begin);
+      fetch(seg.begin);
+      fetch_pages(min(seg.begin + 1, seg.end - 1));
+      // The last segment's reads of the stages are done.
+      __syncthreads();
+      stage(seg.begin);
+      __syncthreads();
+#pragma unroll 1
+      for (int j = seg.begin; j < seg.end; ++j) {
+        const bool more = j + 1 < seg.end;
+        if (more) {
+          fetch(j + 1);
+          fetch_pages(min(j + 2, seg.end - 1));
+        }
+        const int base = j * T::kKeys;
+        const char* st = stages + (j & 1) * T::kStage;
+        if (base <= most_limit && base + T::kKeys > least_lower) {
+          f32x16 s[T::kParts];
+#pragma unroll
+          for (int t = 0; t < T::kParts; ++t) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
+            const int key = 32 * t + r32;
+            const char* krow = st + key * T::kRow;
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+              Frag16 kf, x;
+              kf.u = *reinterpret_cast<const u32x4*>(
+                  krow + (((2 * u + half) ^ T::swizzle_k(key)) * 16));
+              if constexpr (T::kQueriesInLds)
+                x.u = *reinterpret_cast<const u32x4*>(
+                    lds + (size_t)r * T::kRow + (((2 * u + half) ^ T::swizzle_k(r)) * 16));
+              else
+                x = qf[u];
+              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf.h, x.h, s[t], 0, 0, 0);
+            }
+          }
+          const uint64_t present =
+              __ballot(lane < T::kKeys ? st[2 * T::kSide + (lane & (T::kKeys - 1))] : 0);
+          constexpr uint64_t kAll = T::kKeys == 64 ? ~0ull : (1ull << T::kKeys) - 1;
+          if (present != kAll || base + T::kKeys - 1 > least_limit || base < most_lower) {
+            // Bits of the keys that the row sees; the lane's begin at 4 half.
+            uint64_t seen = present;
+            const int above = limit - base, below = lower - base;
+            seen &= above >= 63 ? ~0ull : above < 0 ? 0ull : (2ull << above) - 1;
+            seen &= below <= 0 ? ~0ull : below > 63 ? 0ull : ~0ull << below;
+            seen >>= 4 * half;
+#pragma unroll
+            for (int t = 0; t < T::kParts; ++t) {
+              const uint32_t word = (uint32_t)(seen >> (32 * t));
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!((word >> (8 * (i / 4) + i % 4)) & 1)) s[t][i] = -__builtin_huge_valf();
+            }
+          }
+          float top = s[0][0];
+#pragma unroll
+          for (int t = 0; t < T::kParts; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+          top = max_of_halves(top);
+          if (__any((top - m) * qs > T::kSlack || (m == -__builtin_huge_valf() && top > m))) {
+            const float mn = fmaxf(m, top);
+            const float keep =
+                m == -__builtin_huge_valf() ? 0.f : __builtin_amdgcn_exp2f((m - mn) * qs);
+            l *= keep;
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[c][i] *= keep;
+            m = mn;
+          }
+          const float shift = m == -__builtin_huge_valf() ? 0.f : m * qs - T::kLift;
+          union Weights {
+            bf16_t e[8];
+            f16_t f[8];
+            bf16x8 w;
+            f16x8 v;
+          } pw[T::kParts][2];
+#pragma unroll
+          for (int t = 0; t < T::kParts; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e = __builtin_amdgcn_exp2f(fmaf(s[t][i], qs, -shift));
+              l += e;
+              if constexpr (kFp8) pw[t][i / 8].f[i % 8] = (f16_t)e;
+              else pw[t][i / 8].e[i % 8] = (bf16_t)e;
+            }
+          const int r16 = lane & 15, g = (lane >> 4) & 1;
+#pragma unroll
+          for (int t = 0; t < T::kParts; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int c = 0; c < kBlocks; ++c) {
+                union {
+                  s16x4 q[2];
+                  bf16x8 w;
+                  f16x8 v;
+                } vf;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int key = 32 * t + 16 * y + 8 * z + 4 * half + r16 / 4;
+                  const int piece = 4 * c + 2 * g + (r16 & 3) / 2;
+                  const char* from = st + T::kSide + key * T::kRow +
+                                     ((piece ^ T::swizzle_v(key)) * 16) + 8 * (r16 & 1);
+                  vf.q[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                      (__attribute__((address_space(3))) s16x4*)(uintptr_t)(lds_void*)from);
+                }
+                if constexpr (kFp8)
+                  o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf.v, pw[t][y].v, o[c], 0, 0, 0);
+                else
+                  o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.w, pw[t][y].w, o[c], 0, 0, 0);
+              }
+        }
+        if (more) stage(j + 1);
+        __syncthreads();
+      }
+
+      // The halves of a row hold its sum in parts.
+      l += __shfl_xor(l, 32);
+      float largest = 0.f;  // NaN counts as the largest
+#pragma unroll
+      for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          largest = __builtin_elementwise_maximum(largest, fabsf(o[c][i]));
+      const bool odd = live && l > 0.f && l < __builtin_huge_valf() &&
+                       !(largest < __builtin_huge_valf());
+      const uint64_t odd_lanes = __ballot(odd);
+      const uint32_t again = (uint32_t)odd_lanes | (uint32_t)(odd_lanes >> 32);
+      auto sink_of = [&](size_t row, int place) {
+        Sink<D> to;
+        to.out = all ? a.out + row * D : nullptr;
+        to.lse = a.lse != nullptr ? a.lse + row : nullptr;
+        const size_t part = ((size_t)slot * 2 + (seg.begin == seg.first ? 1 : 0)) * T::kRows + place;
+        to.o = parts.o + part * D;
+        to.ml = parts.ml + part * 2;
+        return to;
+      };
+      if (live && !((again >> r32) & 1)) {
+        const Sink<D> to = sink_of(qrow, r);
+        const float f = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            f32x4 y;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] = l == 0.f ? 0.f : o[c][i + x] * f;
+            to.put4(32 * c + 2 * i + 4 * half, y);
+          }
+        if (half == 0)
+          to.put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
+      }
+#pragma unroll 1
+      for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
+        const int x = __ffs((int)rest) - 1;
+        const int place = wave * 32 + x;
+        const int t2 = fast_div(place, by_heads);
+        const int token2 = k * cut.tokens + t2;
+        const size_t row = (size_t)(ch.row0 + token2) * a.Hq + (size_t)h * G + xb * cut.heads +
+                           (place - t2 * cut.heads);
+        const int end = w.at + token2 + 1;
+        const int from = a.window > 0 ? max(0, end - a.window) : 0;
+        attend_row<D, kFp8>(a, by_block, b, h, row, max(from, seg.begin * T::kKeys),
+                            min(end, seg.end * T::kKeys), sink_of(row, place));
+      }
+    }
+  }
+
+  // Rows that have no token in the cache.
+  for (int x = blockIdx.x; x < a.B; x += gridDim.x) {
+    const Chunk c = chunk_of(a, x);
+    const size_t from = (size_t)(c.row0 + c.live) * a.Hq, to = (size_t)(c.row0 + c.rows) * a.Hq;
+    for (size_t i = from * D + tid * 8; i < to * D; i += T::kThreads * 8)
+      store16(a.out + i, u32x4{0u, 0u, 0u, 0u});
+    if (a.lse != nullptr)
+      for (size_t i = from + tid; i < to; i += T::kThreads) a.lse[i] = -__builtin_huge_valf();
   }
 }
 
-size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D) { return 64; }
+// Adds the parts of rows that were split over stretches: workgroup (x, y) takes
+// the tile that stretch x ends in, if it began there too and goes on, and of its
+// rows every gridDim.y-th group of four, a wave a row.
+template <int D, bool kFp8>
+__global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, Parts parts, Cut cut,
+                                                         FastDiv by_heads, int slots) {
+  using T = Tile<D, kFp8>;
+  constexpr int kPer = D / 64;
+  typedef __attribute__((__vector_size__(kPer * sizeof(float)))) float vec;
+  typedef __attribute__((__vector_size__(kPer * sizeof(__bf16)))) __bf16 half_vec;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.H, jobs = a.H * cut.head_blocks;
+  const int slot = blockIdx.x;
+  const long long stretch = parts.prefix[a.B];
+  const long long start = stretch * slot, end = start + stretch;
+  // The request that unit end - 1 lies in.
+  const int b = __builtin_amdgcn_readfirstlane(last_at_most(parts.prefix, a.B, end - 1));
+  const Chunk ch = chunk_of(a, b);
+  const Load w{ch.at, ch.live, cut.tokens, a.window};
+  if (w.live == 0) return;
+  const long long first = parts.prefix[b], units = w.before(w.tiles());
+  if (end >= first + jobs * units) return;  // the line's end, or the request's
+  const int job = (int)floor_div(end - 1 - first, units);
+  const long long job0 = first + job * units;
+  const int k = w.tile_at(end - 1 - job0);
+  const long long tile0 = job0 + w.before(k), size = w.units(k);
+  if (tile0 < start || tile0 + size <= end) return;
+  const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
+  const int last = min((int)floor_div(tile0 + size - 1, stretch), slots - 1);
+  auto part_of = [&](int x, bool* some, bool* whole) {
+    const Segment s =
+        segment_of<T::kKeys>(w, k, max(stretch * x - tile0, 0ll), min(stretch * (x + 1) - tile0, size));
+    *some = s.begin < s.end;
+    *whole = s.begin == s.first && s.end == s.last;
+    return (size_t)x * 2 + (s.begin == s.first ? 1 : 0);
+  };
+  for (int r = blockIdx.y * 4 + wave; r < T::kRows; r += gridDim.y * 4) {
+    const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
+    const int token = k * cut.tokens + ti;
+    if (ti >= cut.tokens || token >= w.live || xb * cut.heads + hi >= G) continue;
+    const size_t row = (size_t)(ch.row0 + token) * a.Hq + (size_t)h * G + xb * cut.heads + hi;
+    float m = -__builtin_huge_valf(), l = 0.f;
+    vec o = {};
+    bool some, whole = false;
+    for (int x = slot; x <= last; ++x) {
+      const size_t part = part_of(x, &some, &whole) * T::kRows + r;
+      if (whole) break;
+      if (!some) continue;
+      const float m2 = parts.ml[part * 2], l2 = parts.ml[part * 2 + 1];
+      const vec o2 = *reinterpret_cast<const vec*>(parts.o + part * D + kPer * lane);
+      if (l2 == 0.f) continue;
+      const float mn = fmaxf(m, m2);
+      const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
+      const float w1 = l * __builtin_amdgcn_exp2f(m - safe), w2 = l2 * __builtin_amdgcn_exp2f(m2 - safe);
+      l = w1 + w2;
+      m = mn;
+      const float f1 = w1 / l, f2 = w2 / l;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = (w1 == 0.f ? 0.f : o[i] * f1) + o2[i] * f2;
+    }
+    if (whole) continue;
+    half_vec y;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) y[i] = (__bf16)o[i];
+    *reinterpret_cast<half_vec*>(a.out + row * D + kPer * lane) = y;
+    if (a.lse != nullptr && lane == 0)
+      a.lse[row] = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
 
 namespace {
 
-template <int D>
-hipError_t launch_chunk(const ChunkArgs& a, hipStream_t stream) {
-  const int grid = (int)std::min<long long>(((long long)a.T * a.Hq + 3) / 4, 1 << 16);
-  if (a.dtype == kCacheFp8)
-    chunk_row_kernel<D, true><<<grid, 256, 0, stream>>>(a, make_fast_div(a.block_size));
-  else
-    chunk_row_kernel<D, false><<<grid, 256, 0, stream>>>(a, make_fast_div(a.block_size));
+size_t part_rows(int D) { return (size_t)kCus * 2 * 32 * (D == 256 ? 4 : 8); }
+
+template <int D, bool kFp8>
+hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
+  using T = Tile<D, kFp8>;
+  static std::atomic<unsigned long long> done{0};
+  hipError_t e = once_per_device(done, [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(chunk_attention_kernel<D, kFp8>),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+  });
+  if (e != hipSuccess) return e;
+  Parts parts;
+  parts.prefix = (long long*)a.part;
+  parts.ml = a.part + prefix_floats(a.B);
+  parts.o = parts.ml + part_rows(D) * 2;
+  const Cut cut = cut_of(a.Hq / a.H, T::kRows);
+  const FastDiv by_heads = make_fast_div(cut.heads);
+  chunk_attention_kernel<D, kFp8><<<kCus, T::kThreads, T::kLds, stream>>>(
+      a, parts, make_fast_div(a.block_size), cut, by_heads);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  chunk_join_kernel<D, kFp8><<<dim3(kCus, 8), 256, 0, stream>>>(a, parts, cut, by_heads, kCus);
   return hipGetLastError();
 }
 
 }  // namespace
 
+size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D) {
+  if (T == 0 || B == 0) return 0;
+  return prefix_floats(B) + part_rows(D) * (2 + D);
+}
+
 hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream) {
+  const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
-    case 64: return launch_chunk<64>(a, stream);
-    case 128: return launch_chunk<128>(a, stream);
-    case 256: return launch_chunk<256>(a, stream);
+    case 64: return fp8 ? launch_cfg<64, true>(a, stream) : launch_cfg<64, false>(a, stream);
+    case 128: return fp8 ? launch_cfg<128, true>(a, stream) : launch_cfg<128, false>(a, stream);
+    case 256: return fp8 ? launch_cfg<256, true>(a, stream) : launch_cfg<256, false>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -74,7 +74,10 @@ int check_chunk(int T, int B, int n_heads, int n_kv_heads, int head_dim, int max
   if (rc != MOVA_OK) return rc;
   rc = check_read_heads(n_heads, n_kv_heads, head_dim);
   if (rc != MOVA_OK) return rc;
-  return T > kMaxT ? MOVA_ERR_UNSUPPORTED : MOVA_OK;
+  if (T > kMaxT) return MOVA_ERR_UNSUPPORTED;
+  // The line of work counts keys of row tiles in 53 bits.
+  return (double)T * n_heads * ((double)max_blocks * block_size) > 0x1p52 ? MOVA_ERR_UNSUPPORTED
+                                                                          : MOVA_OK;
 }
 
 // Pools whose blocks the upkeep counts.

@@ -42,6 +42,7 @@ CHUNK = dict(q=FAKE, k=FAKE, v=FAKE, dtype=1, ks=FAKE, vs=FAKE, nb=40, bs=16, ta
     (dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(B=2049), UNSUPPORTED), (dict(D=96), UNSUPPORTED),
     (dict(Hq=33), UNSUPPORTED), (dict(H=256, Hq=256), UNSUPPORTED), (dict(Hq=2048), UNSUPPORTED),
     (dict(mb=1 << 27), UNSUPPORTED), (dict(nb=1 << 28), UNSUPPORTED),
+    (dict(T=1 << 20, mb=1 << 24, bs=16), UNSUPPORTED),  # 2^20 rows of 32 heads over 2^28 keys
     (dict(scale=float("nan")), UNSUPPORTED), (dict(scale=float("inf")), UNSUPPORTED),
     *[({n: None}, INVALID) for n in ("q", "k", "v", "table", "cached", "lens", "cu", "out")],
     *[({n: FAKE + 8}, INVALID) for n in ("q", "k", "v", "out")],
