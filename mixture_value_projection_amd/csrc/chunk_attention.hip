@@ -69,13 +69,17 @@ struct Tile {
   static constexpr int kRows = 32 * kWaves;            // rows (token and query head) of a workgroup
   static constexpr int kKeys = D == 256 ? 32 : 64;     // of a tile
   static constexpr int kParts = kKeys / 32;
-  static constexpr int kRow = 2 * D;                   // bytes of a key in LDS
-  static constexpr int kChunks = kRow / 16;
-  static constexpr int kSide = kKeys * kRow;           // bytes of a side (K or V)
-  static constexpr int kStage = 2 * kSide + 64;        // with a byte a key: whether it is there
   static constexpr bool kQueriesInLds = D == 256;
-  static constexpr int kQueries = kQueriesInLds ? kRows * kRow : 0;
-  static constexpr int kLds = kQueries + 2 * kStage;
+  // Bytes between rows in LDS: padded so that the 8 rows of a phase of the keys'
+  // reads, and the 4 that 16 lanes of a transposing read take, lie in different
+  // banks, with all of a tile's places at constant offsets from one address.
+  static constexpr int kKeyRow = 2 * D + 16;
+  static constexpr int kValueRow = 2 * D + 32;
+  static constexpr int kValuesAt = kKeys * kKeyRow;    // in a stage, behind the keys
+  static constexpr int kStage = kValuesAt + kKeys * kValueRow;
+  static constexpr int kQueries = kQueriesInLds ? kRows * kKeyRow : 0;
+  static constexpr int kSlots = 8;                     // tiles whose keys' slots are at hand
+  static constexpr int kLds = kQueries + 2 * kStage + kSlots * kKeys * 4;
   // Staging: a thread moves kLoads 16-byte pieces of the pool a side.
   static constexpr int kPieces = D * (kFp8 ? 1 : 2) / 16;  // of a key
   static constexpr int kTotal = kKeys * kPieces;
@@ -86,12 +90,6 @@ struct Tile {
   static constexpr float kLift = kFp8 ? 14.f : 0.f;
   // Sums are brought to a new maximum once it is this much higher (in powers of two).
   static constexpr float kSlack = kFp8 ? 1.f : 8.f;
-  // Piece c of key r lies at piece c ^ swizzle(r).
-  static __device__ __forceinline__ int swizzle_k(int r) { return r & (kChunks - 1) & 15; }
-  static __device__ __forceinline__ int swizzle_v(int r) {
-    constexpr int kShare = kChunks >= 16 ? 1 : 16 / kChunks;
-    return (2 * (r / kShare)) & (kChunks - 1) & 15;
-  }
 };
 
 // How the rows of a request and key head are cut: blocks of `tokens` tokens with
@@ -374,6 +372,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
   const int slots = gridDim.x;
   const int slot = (int)(blockIdx.x & 7) * (slots >> 3) + (int)(blockIdx.x >> 3);
   char* stages = lds + T::kQueries;
+  int* slots_of_keys = (int*)(stages + 2 * T::kStage);
 
   auto cost = [&](int b) {
     const Load w = load_of(a, cut.tokens, b);
@@ -446,58 +445,79 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
 #pragma unroll
         for (int i = 0; i < 4; ++i) x.u[i] ^= flip;
         if constexpr (T::kQueriesInLds)
-          store16(lds + (size_t)r * T::kRow + (((2 * u + half) ^ T::swizzle_k(r)) * 16), x.u);
+          store16(lds + r * T::kKeyRow + (2 * u + half) * 16, x.u);
         else
           qf[u] = x;
       }
 
-      // Staging: block numbers a tile ahead of the keys and values, those a tile
-      // ahead of the products.
-      int page[T::kLoads];
+      // Staging, through registers: in tile j's turn the keys of tile j + 2 and the
+      // values of tile j + 1 go into LDS and those of the tiles behind them are asked
+      // for.  One wave looks up the slots of a tile's keys, a lane a key, some tiles
+      // ahead (-1: not there, or behind the segment).
+      constexpr int kLookup = 3;  // the wave
+      const uint32_t row_bytes = (uint32_t)a.H * (T::kPieces * 16);
+      const size_t mine = (size_t)h * (T::kPieces * 16) + my_piece * 16;
+      const char* my_k = (const char*)a.k_cache + mine;
+      const char* my_v = (const char*)a.v_cache + mine;
+      const int key_end = min(len, seg.end * T::kKeys);
+      auto page_of = [&](int j) {
+        return table[fast_div(min(j * T::kKeys + lane, key_end - 1), by_block)];
+      };
+      auto ring = [&](int j) {
+        return slots_of_keys + ((j - seg.begin) & (T::kSlots - 1)) * T::kKeys;
+      };
+      auto put_slots = [&](int j, int page) {
+        const int p = j * T::kKeys + lane;
+        const bool ok = p < key_end && page >= 0 && page < a.num_blocks;
+        const int row = p - fast_div(p, by_block) * a.block_size;
+        if (lane < T::kKeys) ring(j)[lane] = ok ? page * a.block_size + row : -1;
+      };
+      auto get_slots = [&](int j, int (&slot_of)[T::kLoads]) {
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i)
+          slot_of[i] = ring(j)[(my_key + i * T::kStep) & (T::kKeys - 1)];
+      };
       u32x4 kreg[T::kLoads], vreg[T::kLoads];
-      bool there[T::kLoads];
-      auto fetch_pages = [&](int j) {
+      bool k_there[T::kLoads], v_there[T::kLoads];
+      int v_slot[T::kLoads], k_slot[T::kLoads];
+      auto fetch_key = [&](int i, int slot_of) {
+        k_there[i] = slot_of >= 0;
+        kreg[i] = load16(my_k + (size_t)(uint32_t)max(slot_of, 0) * row_bytes);
+      };
+      auto fetch_value = [&](int i, int slot_of) {
+        v_there[i] = slot_of >= 0;
+        vreg[i] = load16(my_v + (size_t)(uint32_t)max(slot_of, 0) * row_bytes);
+      };
+      // Zeros for keys that are not there: infinities and NaN would show through
+      // weights of 0.
+      auto clear = [&] {
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) all = all && k_there[i] && v_there[i];
+        if (__all(all)) return;
+        asm volatile("");  // a branch, and no selects, which would wait for the loads
 #pragma unroll
         for (int i = 0; i < T::kLoads; ++i) {
-          const int p = j * T::kKeys + my_key + i * T::kStep;
-          page[i] = my_load && p < len ? table[fast_div(p, by_block)] : -1;
+          kreg[i] = k_there[i] ? kreg[i] : u32x4{0u, 0u, 0u, 0u};
+          vreg[i] = v_there[i] ? vreg[i] : u32x4{0u, 0u, 0u, 0u};
         }
       };
-      auto fetch = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-          const int p = j * T::kKeys + my_key + i * T::kStep;
-          there[i] = page[i] >= 0 && page[i] < a.num_blocks;
-          const int row = p - fast_div(p, by_block) * a.block_size;
-          const size_t s = there[i] ? (size_t)page[i] * a.block_size + row : 0;
-          const size_t off = (s * a.H + h) * (T::kPieces * 16) + my_piece * 16;
-          kreg[i] = load16((const char*)a.k_cache + off);
-          vreg[i] = load16((const char*)a.v_cache + off);
-        }
-      };
-      auto stage = [&](int j) {
-        char* to = stages + (j & 1) * T::kStage;
+      auto put = [&](char* row, const u32x4& x, auto half_precision) {
         if (!my_load) return;
-#pragma unroll
-        for (int i = 0; i < T::kLoads; ++i) {
-          const int key = my_key + i * T::kStep;
-          char* krow = to + key * T::kRow;
-          char* vrow = krow + T::kSide;
-          const u32x4 none = {0u, 0u, 0u, 0u};
-          if constexpr (kFp8) {
-            u32x4 lo16, hi16;
-            widen16<false>(there[i] ? kreg[i] : none, &lo16, &hi16);
-            store16(krow + (((2 * my_piece) ^ T::swizzle_k(key)) * 16), lo16);
-            store16(krow + (((2 * my_piece + 1) ^ T::swizzle_k(key)) * 16), hi16);
-            widen16<true>(there[i] ? vreg[i] : none, &lo16, &hi16);
-            store16(vrow + (((2 * my_piece) ^ T::swizzle_v(key)) * 16), lo16);
-            store16(vrow + (((2 * my_piece + 1) ^ T::swizzle_v(key)) * 16), hi16);
-          } else {
-            store16(krow + ((my_piece ^ T::swizzle_k(key)) * 16), there[i] ? kreg[i] : none);
-            store16(vrow + ((my_piece ^ T::swizzle_v(key)) * 16), there[i] ? vreg[i] : none);
-          }
-          if (my_piece == 0) to[2 * T::kSide + key] = there[i];
+        if constexpr (kFp8) {
+          u32x4 first8, last8;
+          widen16<decltype(half_precision)::value>(x, &first8, &last8);
+          store16(row + 2 * my_piece * 16, first8);
+          store16(row + (2 * my_piece + 1) * 16, last8);
+        } else {
+          store16(row + my_piece * 16, x);
         }
+      };
+      auto put_key = [&](char* st, int i) {
+        put(st + (my_key + i * T::kStep) * T::kKeyRow, kreg[i], std::false_type{});
+      };
+      auto put_value = [&](char* st, int i) {
+        put(st + T::kValuesAt + (my_key + i * T::kStep) * T::kValueRow, vreg[i], std::true_type{});
       };
 
       f32x16 o[kBlocks];
@@ -507,123 +527,240 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         for (int i = 0; i < 16; ++i) o[c][i] = 0.f;
       float m = -__builtin_huge_valf(), l = 0.f;  // m: of the products, not scaled
 
-      fetch_pages(seg.begin);
-      fetch(seg.begin);
-      fetch_pages(min(seg.begin + 1, seg.end - 1));
-      // The last segment's reads of the stages are done.
-      __syncthreads();
-      stage(seg.begin);
-      __syncthreads();
-#pragma unroll 1
-      for (int j = seg.begin; j < seg.end; ++j) {
-        const bool more = j + 1 < seg.end;
-        if (more) {
-          fetch(j + 1);
-          fetch_pages(min(j + 2, seg.end - 1));
+      // Products with a tile's keys.  Their LDS reads run kAhead products ahead: left
+      // to itself, the compiler waits for each read right before its product.
+      constexpr int kAhead = 4, kProducts = kSteps * T::kParts;
+      f32x16 s[2][T::kParts];  // of even and odd tiles of the segment
+      Frag16 kf[kProducts], xf[kProducts];
+      auto read_keys = [&](const char* st, int n) {
+        const int t = n % T::kParts, u = n / T::kParts;
+        kf[n].u = *reinterpret_cast<const u32x4*>(st + (32 * t + r32) * T::kKeyRow +
+                                                  (2 * u + half) * 16);
+        if constexpr (T::kQueriesInLds)
+          xf[n].u = *reinterpret_cast<const u32x4*>(lds + r * T::kKeyRow + (2 * u + half) * 16);
+        else
+          xf[n] = qf[u];
+      };
+      auto product = [&](f32x16 (&to)[T::kParts], int n) {
+        const int t = n % T::kParts;  // neighbours do not wait for each other
+        if (n < T::kParts) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) to[t][i] = 0.f;
         }
+        to[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n].h, xf[n].h, to[t], 0, 0, 0);
+      };
+      auto all_products = [&](const char* st, f32x16 (&to)[T::kParts]) {
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) read_keys(st, n);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kProducts; ++n) {
+          if (n + kAhead < kProducts) read_keys(st, n + kAhead);
+          product(to, n);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      const bool any_row = most_limit >= 0;
+      auto read_by_wave = [&](int j) {
         const int base = j * T::kKeys;
-        const char* st = stages + (j & 1) * T::kStage;
-        if (base <= most_limit && base + T::kKeys > least_lower) {
-          f32x16 s[T::kParts];
+        return any_row && base <= most_limit && base + T::kKeys > least_lower;
+      };
+
+      // (The reads of the last segment's slots and stages are behind a barrier.)
+      for (int x = wave; x < 5; x += T::kWaves) put_slots(seg.begin + x, page_of(seg.begin + x));
+      int page = -1;
+      if (wave == kLookup) page = page_of(seg.begin + 5);
+      __syncthreads();
+      int slot_here = ring(seg.begin)[lane & (T::kKeys - 1)];
+      get_slots(seg.begin, v_slot);
+      get_slots(seg.begin + 1, k_slot);
 #pragma unroll
-          for (int t = 0; t < T::kParts; ++t) {
+      for (int i = 0; i < T::kLoads; ++i) {
+        fetch_key(i, v_slot[i]);
+        fetch_value(i, v_slot[i]);
+      }
+      clear();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
-            const int key = 32 * t + r32;
-            const char* krow = st + key * T::kRow;
+      for (int i = 0; i < T::kLoads; ++i) {
+        put_key(stages, i);
+        put_value(stages, i);
+        fetch_key(i, k_slot[i]);
+        fetch_value(i, k_slot[i]);
+      }
+      get_slots(seg.begin + 2, v_slot);
+      clear();
 #pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-              Frag16 kf, x;
-              kf.u = *reinterpret_cast<const u32x4*>(
-                  krow + (((2 * u + half) ^ T::swizzle_k(key)) * 16));
-              if constexpr (T::kQueriesInLds)
-                x.u = *reinterpret_cast<const u32x4*>(
-                    lds + (size_t)r * T::kRow + (((2 * u + half) ^ T::swizzle_k(r)) * 16));
-              else
-                x = qf[u];
-              s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf.h, x.h, s[t], 0, 0, 0);
+      for (int i = 0; i < T::kLoads; ++i) {
+        put_key(stages + T::kStage, i);
+        fetch_key(i, v_slot[i]);
+      }
+      get_slots(seg.begin + 3, k_slot);
+      __syncthreads();
+      if (read_by_wave(seg.begin)) all_products(stages, s[0]);
+      __syncthreads();  // the first turn puts other keys there
+
+      // Whether a row's products of a tile reach so far above m that its sums have to be
+      // brought to them.
+      constexpr int kValues = 16 * T::kParts;  // products of a lane
+      auto above_slack = [&](float top) -> bool {
+        return __any((top - m) * qs > T::kSlack || (m == -__builtin_huge_valf() && top > m));
+      };
+      bool check = true;  // the tile's maximum is not known, or above
+
+      // Tile j, in stage kAt, along with the products of the next one's keys (of what
+      // lies there, behind the last tile; they are not used).
+      auto turn = [&](int j, auto at) {
+        constexpr int kAt = decltype(at)::value;
+        const int base = j * T::kKeys;
+        char* st = stages + kAt * T::kStage;
+        char* st_next = stages + (1 - kAt) * T::kStage;
+        const uint64_t present = __ballot(lane < T::kKeys && slot_here >= 0);
+        slot_here = ring(j + 1)[lane & (T::kKeys - 1)];
+        if (wave == kLookup) {
+          put_slots(j + 5, page);
+          page = page_of(j + 6);
+        }
+        clear();
+        auto next_slots = [&] {
+#pragma unroll
+          for (int i = 0; i < T::kLoads; ++i) v_slot[i] = k_slot[i];
+          get_slots(j + 4, k_slot);
+        };
+        if (read_by_wave(j)) {
+          f32x16 (&sj)[T::kParts] = s[kAt];
+          f32x16 (&sn)[T::kParts] = s[1 - kAt];
+          constexpr uint64_t kAll = ~0ull >> (64 - T::kKeys);
+          const bool some_hidden =
+              present != kAll || base + T::kKeys - 1 > least_limit || base < most_lower;
+          if (check || some_hidden) {
+            if (some_hidden) {
+              // Bits of the keys that the row sees; the lane's begin at 4 half.
+              uint64_t seen = present;
+              const int above = limit - base, below = lower - base;
+              seen &= above >= 63 ? ~0ull : above < 0 ? 0ull : (2ull << above) - 1;
+              seen &= below <= 0 ? ~0ull : below > 63 ? 0ull : ~0ull << below;
+              seen >>= 4 * half;
+#pragma unroll
+              for (int t = 0; t < T::kParts; ++t) {
+                const uint32_t word = (uint32_t)(seen >> (32 * t));
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (!((word >> (8 * (i / 4) + i % 4)) & 1)) sj[t][i] = -__builtin_huge_valf();
+              }
             }
-          }
-          const uint64_t present =
-              __ballot(lane < T::kKeys ? st[2 * T::kSide + (lane & (T::kKeys - 1))] : 0);
-          constexpr uint64_t kAll = T::kKeys == 64 ? ~0ull : (1ull << T::kKeys) - 1;
-          if (present != kAll || base + T::kKeys - 1 > least_limit || base < most_lower) {
-            // Bits of the keys that the row sees; the lane's begin at 4 half.
-            uint64_t seen = present;
-            const int above = limit - base, below = lower - base;
-            seen &= above >= 63 ? ~0ull : above < 0 ? 0ull : (2ull << above) - 1;
-            seen &= below <= 0 ? ~0ull : below > 63 ? 0ull : ~0ull << below;
-            seen >>= 4 * half;
+            float top = sj[0][0];
 #pragma unroll
-            for (int t = 0; t < T::kParts; ++t) {
-              const uint32_t word = (uint32_t)(seen >> (32 * t));
+            for (int i = 1; i < kValues; ++i) top = fmaxf(top, sj[i / 16][i % 16]);
+            top = max_of_halves(top);
+            if (above_slack(top)) {
+              const float mn = fmaxf(m, top);
+              const float keep =
+                  m == -__builtin_huge_valf() ? 0.f : __builtin_amdgcn_exp2f((m - mn) * qs);
+              l *= keep;
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (!((word >> (8 * (i / 4) + i % 4)) & 1)) s[t][i] = -__builtin_huge_valf();
+              for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[c][i] *= keep;
+              m = mn;
             }
-          }
-          float top = s[0][0];
-#pragma unroll
-          for (int t = 0; t < T::kParts; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-          top = max_of_halves(top);
-          if (__any((top - m) * qs > T::kSlack || (m == -__builtin_huge_valf() && top > m))) {
-            const float mn = fmaxf(m, top);
-            const float keep =
-                m == -__builtin_huge_valf() ? 0.f : __builtin_amdgcn_exp2f((m - mn) * qs);
-            l *= keep;
-#pragma unroll
-            for (int c = 0; c < kBlocks; ++c)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[c][i] *= keep;
-            m = mn;
           }
           const float shift = m == -__builtin_huge_valf() ? 0.f : m * qs - T::kLift;
+
+          // The weights go between the products with the next tile's keys and the
+          // first half of those with the values; the next tile's maximum goes between
+          // the second half, so that only the tiles that raise it, or hide keys from
+          // some row, need more.
+          constexpr int kGroups = 2 * T::kParts, kSums = kGroups * kBlocks;  // of 16 keys
+          constexpr int kFirst = kValues * 5 / 8;  // weights among the products with keys
+          static_assert(2 * T::kLoads <= kProducts / 2 && kFirst >= 8 * (kGroups / 2), "order");
           union Weights {
             bf16_t e[8];
             f16_t f[8];
             bf16x8 w;
             f16x8 v;
-          } pw[T::kParts][2];
-#pragma unroll
-          for (int t = 0; t < T::kParts; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e = __builtin_amdgcn_exp2f(fmaf(s[t][i], qs, -shift));
-              l += e;
-              if constexpr (kFp8) pw[t][i / 8].f[i % 8] = (f16_t)e;
-              else pw[t][i / 8].e[i % 8] = (bf16_t)e;
-            }
+          } pw[kGroups];
+          union Values {
+            s16x4 q[2];
+            bf16x8 w;
+            f16x8 v;
+          } vf[kSums];
           const int r16 = lane & 15, g = (lane >> 4) & 1;
+          auto weigh = [&](int i) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(sj[i / 16][i % 16], qs, -shift));
+            l += e;
+            if constexpr (kFp8) pw[i / 8].f[i % 8] = (f16_t)e;
+            else pw[i / 8].e[i % 8] = (bf16_t)e;
+          };
+          auto weights = [&](int from, int to) {
 #pragma unroll
-          for (int t = 0; t < T::kParts; ++t)
+            for (int i = from; i < to; ++i) weigh(i);
+          };
+          auto read_values = [&](int n) {
+            const int y = n / kBlocks, c = n % kBlocks;
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+            for (int z = 0; z < 2; ++z) {
+              const int key = 16 * y + 8 * z + 4 * half + r16 / 4;
+              char* from = st + T::kValuesAt + key * T::kValueRow + 64 * c + 32 * g + 8 * (r16 & 3);
+              vf[n].q[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                  (__attribute__((address_space(3))) s16x4*)(uintptr_t)(lds_void*)from);
+            }
+          };
 #pragma unroll
-              for (int c = 0; c < kBlocks; ++c) {
-                union {
-                  s16x4 q[2];
-                  bf16x8 w;
-                  f16x8 v;
-                } vf;
+          for (int n = 0; n < kAhead; ++n) read_keys(st_next, n);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int key = 32 * t + 16 * y + 8 * z + 4 * half + r16 / 4;
-                  const int piece = 4 * c + 2 * g + (r16 & 3) / 2;
-                  const char* from = st + T::kSide + key * T::kRow +
-                                     ((piece ^ T::swizzle_v(key)) * 16) + 8 * (r16 & 1);
-                  vf.q[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                      (__attribute__((address_space(3))) s16x4*)(uintptr_t)(lds_void*)from);
-                }
-                if constexpr (kFp8)
-                  o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf.v, pw[t][y].v, o[c], 0, 0, 0);
-                else
-                  o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf.w, pw[t][y].w, o[c], 0, 0, 0);
-              }
+          for (int n = 0; n < kProducts; ++n) {
+            if (n + kAhead < kProducts) read_keys(st_next, n + kAhead);
+            else read_values(n + kAhead - kProducts);
+            product(sn, n);
+            constexpr int kFetch = kProducts / 2;
+            if (n < T::kLoads) put_key(st, n);
+            else if (n < 2 * T::kLoads) put_value(st_next, n - T::kLoads);
+            if (n >= kFetch && n < kFetch + T::kLoads) fetch_key(n - kFetch, k_slot[n - kFetch]);
+            else if (n >= kFetch + T::kLoads && n < kFetch + 2 * T::kLoads)
+              fetch_value(n - kFetch - T::kLoads, v_slot[n - kFetch - T::kLoads]);
+            weights(n * kFirst / kProducts, (n + 1) * kFirst / kProducts);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          next_slots();
+          float top = -__builtin_huge_valf();
+#pragma unroll
+          for (int n = 0; n < kSums; ++n) {
+            const int y = n / kBlocks, c = n % kBlocks;
+            constexpr int kHalf = kSums / 2, kRest = kValues - kFirst;
+            if (n + kAhead < kSums) read_values(n + kAhead);
+            if constexpr (kFp8)
+              o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n].v, pw[y].v, o[c], 0, 0, 0);
+            else
+              o[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n].w, pw[y].w, o[c], 0, 0, 0);
+            if (n < kHalf) {
+              weights(kFirst + n * kRest / kHalf, kFirst + (n + 1) * kRest / kHalf);
+            } else {
+#pragma unroll
+              for (int i = (n - kHalf) * kValues / kHalf; i < (n - kHalf + 1) * kValues / kHalf; ++i)
+                top = fmaxf(top, sn[i / 16][i % 16]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          check = above_slack(max_of_halves(top));
+        } else {
+          if (read_by_wave(j + 1)) all_products(st_next, s[1 - kAt]);
+          check = true;
+#pragma unroll
+          for (int i = 0; i < T::kLoads; ++i) {
+            put_key(st, i);
+            put_value(st_next, i);
+            fetch_key(i, k_slot[i]);
+            fetch_value(i, v_slot[i]);
+          }
+          next_slots();
         }
-        if (more) stage(j + 1);
         __syncthreads();
+      };
+#pragma unroll 1
+      for (int j = seg.begin; j < seg.end; j += 2) {
+        turn(j, std::integral_constant<int, 0>{});
+        if (j + 1 < seg.end) turn(j + 1, std::integral_constant<int, 1>{});
       }
 
       // The halves of a row hold its sum in parts.
@@ -783,7 +920,8 @@ hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
       a, parts, make_fast_div(a.block_size), cut, by_heads);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  chunk_join_kernel<D, kFp8><<<dim3(kCus, 8), 256, 0, stream>>>(a, parts, cut, by_heads, kCus);
+  chunk_join_kernel<D, kFp8><<<dim3(kCus, 8), 256, 0, stream>>>(
+      a, parts, cut, by_heads, kCus);
   return hipGetLastError();
 }
 
