@@ -107,7 +107,7 @@ Cut cut_of(int G, int rows) {
 
 // What a request brings to the line of work, in keys: each of its row tiles reads
 // keys [lo, hi), and kFixed more for what a tile costs beside them.
-constexpr int kFixed = 128;
+constexpr int kFixed = 192;
 // A stretch of the line is at least this long.
 constexpr int kLeastStretch = 512;
 struct Load {
@@ -193,8 +193,11 @@ __device__ __forceinline__ bool chunk_line(int B, int slot, int slots, Cost cost
   constexpr int kThreads = 64 * kWaves;
   const int per = ceil_div(B, kThreads);
   const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
+  // The thread's first request (up to 256 the only one) is looked at once.
+  const long long cost0 = b0 < b1 ? cost(b0) : 0;
+  auto cost_of = [&](int b) { return b == b0 ? cost0 : cost(b); };
   long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += cost(b);
+  for (int b = b0; b < b1; ++b) mine += cost_of(b);
   long long before = block_exclusive_scan<kWaves>(mine, sh.tmp, &total);
   line->stretch = max(floor_div(total + slots - 1, slots), (long long)kLeastStretch);
   line->start = line->stretch * slot;
@@ -202,14 +205,14 @@ __device__ __forceinline__ bool chunk_line(int B, int slot, int slots, Cost cost
   if (before <= line->start && line->start < before + mine) {
     long long at = before;
     int b = b0;
-    for (long long c; line->start >= at + (c = cost(b)); ++b) at += c;
+    for (long long c; line->start >= at + (c = cost_of(b)); ++b) at += c;
     sh.b = b;
     sh.first = at;
   }
   if (prefix != nullptr && slot == 0) {
     for (int b = b0; b < b1; ++b) {
       prefix[b] = before;
-      before += cost(b);
+      before += cost_of(b);
     }
     if (threadIdx.x == 0) prefix[B] = line->stretch;
   }
@@ -253,17 +256,6 @@ struct Sink {
   float* lse;   // null: none
   float* o;
   float* ml;
-  // 4 channels from c on, of values already divided by the sum.
-  __device__ __forceinline__ void put4(int c, f32x4 y) const {
-    if (out != nullptr) {
-      uint2 w;
-      w.x = (uint32_t)f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16);
-      w.y = (uint32_t)f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16);
-      *reinterpret_cast<uint2*>(out + c) = w;
-    } else {
-      *reinterpret_cast<f32x4*>(o + c) = y;
-    }
-  }
   __device__ __forceinline__ void put1(int c, float y) const {
     if (out != nullptr) out[c] = (bf16_t)y;
     else o[c] = y;
@@ -385,27 +377,33 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
   const int my_key = tid / T::kPieces, my_piece = tid % T::kPieces;
   const bool my_load = T::kTotal >= T::kThreads || tid < T::kTotal;
 
-  int b = line.b;
-  long long first = line.first;  // first unit of request b
   if (work) {
+    int b = line.b;
     Chunk ch = chunk_of(a, b);
     Load w{ch.at, ch.live, cut.tokens, a.window};
-    long long units = w.live == 0 ? 0 : w.before(w.tiles());
-    for (long long pos = line.start; pos < line.end;) {
-      while (pos >= first + jobs * units) {
-        first += jobs * units;
-        if (++b >= a.B) break;
+    int tiles = w.tiles();
+    const long long units = w.before(tiles);
+    int job = (int)floor_div(line.start - line.first, units);
+    long long x0 = line.start - line.first - job * units;  // first unit in tile k
+    int k = w.tile_at(x0);
+    x0 -= w.before(k);
+    // The next tile, of the next job, of the next request with tokens.
+    auto advance = [&] {
+      x0 = 0;
+      if (++k < tiles) return;
+      k = 0;
+      if (++job < jobs) return;
+      job = 0;
+      do {
+        if (++b >= a.B) return;
         ch = chunk_of(a, b);
-        w = Load{ch.at, ch.live, cut.tokens, a.window};
-        units = w.live == 0 ? 0 : w.before(w.tiles());
-      }
-      if (b >= a.B) break;
-      const int job = (int)floor_div(pos - first, units);
-      const long long in_job = pos - first - job * units;
-      const int k = w.tile_at(in_job);
-      const long long x0 = in_job - w.before(k), size = w.units(k);
-      const long long x1 = min(size, x0 + (line.end - pos));
-      pos += x1 - x0;
+      } while (ch.live == 0);
+      w = Load{ch.at, ch.live, cut.tokens, a.window};
+      tiles = w.tiles();
+    };
+    for (long long left = line.end - line.start; left > 0 && b < a.B; advance()) {
+      const long long x1 = min(w.units(k), x0 + left);
+      left -= x1 - x0;
       const Segment seg = segment_of<T::kKeys>(w, k, x0, x1);
       if (seg.begin >= seg.end) continue;
       const bool all = seg.begin == seg.first && seg.end == seg.last;
@@ -430,6 +428,23 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const int least_lower = wave_reduce(live ? lower : 0x3fffffff, imin);
       const int most_lower = wave_reduce(lower, imax);
 
+      // Staging, through registers: in tile j's turn the keys of tile j + 2 and the
+      // values of tile j + 1 go into LDS and those of the tiles behind them are asked
+      // for.  One wave looks up the slots of a tile's keys, a lane a key, some tiles
+      // ahead (-1: not there, or behind the segment).
+      constexpr int kLookup = 3;  // the wave
+      const uint32_t row_bytes = (uint32_t)a.H * (T::kPieces * 16);
+      const size_t mine = (size_t)h * (T::kPieces * 16) + my_piece * 16;
+      const char* my_k = (const char*)a.k_cache + mine;
+      const char* my_v = (const char*)a.v_cache + mine;
+      const int key_end = min(len, seg.end * T::kKeys);
+      auto page_of = [&](int j) {
+        return table[fast_div(min(j * T::kKeys + lane, key_end - 1), by_block)];
+      };
+      // (Ahead of the queries' loads, as they are waited for first.)
+      const int page0 = page_of(seg.begin + min(wave, 4));
+      int page = page_of(seg.begin + 5);
+
       // Queries; a negative scale goes into their signs.
       const float ks = a.k_scale != nullptr ? a.k_scale[h] : 1.f;
       const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
@@ -450,19 +465,6 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
           qf[u] = x;
       }
 
-      // Staging, through registers: in tile j's turn the keys of tile j + 2 and the
-      // values of tile j + 1 go into LDS and those of the tiles behind them are asked
-      // for.  One wave looks up the slots of a tile's keys, a lane a key, some tiles
-      // ahead (-1: not there, or behind the segment).
-      constexpr int kLookup = 3;  // the wave
-      const uint32_t row_bytes = (uint32_t)a.H * (T::kPieces * 16);
-      const size_t mine = (size_t)h * (T::kPieces * 16) + my_piece * 16;
-      const char* my_k = (const char*)a.k_cache + mine;
-      const char* my_v = (const char*)a.v_cache + mine;
-      const int key_end = min(len, seg.end * T::kKeys);
-      auto page_of = [&](int j) {
-        return table[fast_div(min(j * T::kKeys + lane, key_end - 1), by_block)];
-      };
       auto ring = [&](int j) {
         return slots_of_keys + ((j - seg.begin) & (T::kSlots - 1)) * T::kKeys;
       };
@@ -513,11 +515,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
           store16(row + my_piece * 16, x);
         }
       };
-      auto put_key = [&](char* st, int i) {
-        put(st + (my_key + i * T::kStep) * T::kKeyRow, kreg[i], std::false_type{});
+      auto put_key = [&](char* st, int i, const u32x4& x) {
+        put(st + (my_key + i * T::kStep) * T::kKeyRow, x, std::false_type{});
       };
-      auto put_value = [&](char* st, int i) {
-        put(st + T::kValuesAt + (my_key + i * T::kStep) * T::kValueRow, vreg[i], std::true_type{});
+      auto put_value = [&](char* st, int i, const u32x4& x) {
+        put(st + T::kValuesAt + (my_key + i * T::kStep) * T::kValueRow, x, std::true_type{});
       };
 
       f32x16 o[kBlocks];
@@ -567,33 +569,32 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       };
 
       // (The reads of the last segment's slots and stages are behind a barrier.)
-      for (int x = wave; x < 5; x += T::kWaves) put_slots(seg.begin + x, page_of(seg.begin + x));
-      int page = -1;
-      if (wave == kLookup) page = page_of(seg.begin + 5);
+      if (wave < 5) put_slots(seg.begin + wave, page0);
+      if (T::kWaves == 4 && wave == 0) put_slots(seg.begin + 4, page_of(seg.begin + 4));
       __syncthreads();
       int slot_here = ring(seg.begin)[lane & (T::kKeys - 1)];
-      get_slots(seg.begin, v_slot);
-      get_slots(seg.begin + 1, k_slot);
+      {
+        int at[3][T::kLoads];  // slots of the first three tiles' keys
+        u32x4 first[3][T::kLoads];
 #pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) {
-        fetch_key(i, v_slot[i]);
-        fetch_value(i, v_slot[i]);
-      }
-      clear();
+        for (int x = 0; x < 3; ++x) get_slots(seg.begin + x, at[x]);
 #pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) {
-        put_key(stages, i);
-        put_value(stages, i);
-        fetch_key(i, k_slot[i]);
-        fetch_value(i, k_slot[i]);
+        for (int i = 0; i < T::kLoads; ++i) {
+          first[0][i] = load16(my_k + (size_t)(uint32_t)max(at[0][i], 0) * row_bytes);
+          first[1][i] = load16(my_v + (size_t)(uint32_t)max(at[0][i], 0) * row_bytes);
+          first[2][i] = load16(my_k + (size_t)(uint32_t)max(at[1][i], 0) * row_bytes);
+          fetch_key(i, at[2][i]);
+          fetch_value(i, at[1][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) {
+          const u32x4 none = {0u, 0u, 0u, 0u};
+          put_key(stages, i, at[0][i] >= 0 ? first[0][i] : none);
+          put_value(stages, i, at[0][i] >= 0 ? first[1][i] : none);
+          put_key(stages + T::kStage, i, at[1][i] >= 0 ? first[2][i] : none);
+        }
       }
       get_slots(seg.begin + 2, v_slot);
-      clear();
-#pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) {
-        put_key(stages + T::kStage, i);
-        fetch_key(i, v_slot[i]);
-      }
       get_slots(seg.begin + 3, k_slot);
       __syncthreads();
       if (read_by_wave(seg.begin)) all_products(stages, s[0]);
@@ -714,8 +715,8 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
             else read_values(n + kAhead - kProducts);
             product(sn, n);
             constexpr int kFetch = kProducts / 2;
-            if (n < T::kLoads) put_key(st, n);
-            else if (n < 2 * T::kLoads) put_value(st_next, n - T::kLoads);
+            if (n < T::kLoads) put_key(st, n, kreg[n]);
+            else if (n < 2 * T::kLoads) put_value(st_next, n - T::kLoads, vreg[n - T::kLoads]);
             if (n >= kFetch && n < kFetch + T::kLoads) fetch_key(n - kFetch, k_slot[n - kFetch]);
             else if (n >= kFetch + T::kLoads && n < kFetch + 2 * T::kLoads)
               fetch_value(n - kFetch - T::kLoads, v_slot[n - kFetch - T::kLoads]);
@@ -748,8 +749,8 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
           check = true;
 #pragma unroll
           for (int i = 0; i < T::kLoads; ++i) {
-            put_key(st, i);
-            put_value(st_next, i);
+            put_key(st, i, kreg[i]);
+            put_value(st_next, i, vreg[i]);
             fetch_key(i, k_slot[i]);
             fetch_value(i, v_slot[i]);
           }
@@ -775,6 +776,14 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
                        !(largest < __builtin_huge_valf());
       const uint64_t odd_lanes = __ballot(odd);
       const uint32_t again = (uint32_t)odd_lanes | (uint32_t)(odd_lanes >> 32);
+      if (__any(l == 0.f)) {
+        // No weight: nothing, also where a value is infinite or NaN.
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[c][i] = l == 0.f ? 0.f : o[c][i];
+      }
+      const float f = l == 0.f ? 0.f : vs / l;
       auto sink_of = [&](size_t row, int place) {
         Sink<D> to;
         to.out = all ? a.out + row * D : nullptr;
@@ -784,20 +793,43 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         to.ml = parts.ml + part * 2;
         return to;
       };
-      if (live && !((again >> r32) & 1)) {
-        const Sink<D> to = sink_of(qrow, r);
-        const float f = l == 0.f ? 0.f : vs / l;
+      const bool plain = live && !((again >> r32) & 1);
+      if (plain && half == 0)
+        sink_of(qrow, r).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
+      if (all) {
+        // Rows lie across the lanes: through LDS (all waves are done with the stages),
+        // so that a store has whole rows.
+        constexpr int kOutRow = 2 * D + 16, kPieces = D / 8;
+        static_assert(32 * T::kWaves * kOutRow <= 2 * T::kStage, "rows fit the stages");
+        char* box = stages + wave * 32 * kOutRow;
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            f32x4 y;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = l == 0.f ? 0.f : o[c][i + x] * f;
-            to.put4(32 * c + 2 * i + 4 * half, y);
+            uint2 x;
+            x.x = (uint32_t)f32_to_bf16_bits(o[c][i] * f) |
+                  ((uint32_t)f32_to_bf16_bits(o[c][i + 1] * f) << 16);
+            x.y = (uint32_t)f32_to_bf16_bits(o[c][i + 2] * f) |
+                  ((uint32_t)f32_to_bf16_bits(o[c][i + 3] * f) << 16);
+            *reinterpret_cast<uint2*>(box + r32 * kOutRow + (32 * c + 2 * i + 4 * half) * 2) = x;
           }
-        if (half == 0)
-          to.put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
+        const uint32_t rows = (uint32_t)__ballot(plain);
+#pragma unroll
+        for (int i = 0; i < 32 * kPieces / 64; ++i) {
+          const int x = i * 64 + lane, row = x / kPieces, piece = x % kPieces;
+          const size_t to = (size_t)(uint32_t)__shfl((int)qrow, row) |
+                            (size_t)(uint32_t)__shfl((int)(qrow >> 32), row) << 32;
+          const u32x4 y = *reinterpret_cast<const u32x4*>(box + row * kOutRow + piece * 16);
+          if ((rows >> row) & 1) store16(a.out + to * D + piece * 8, y);
+        }
+      } else if (plain) {
+        const Sink<D> to = sink_of(qrow, r);
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4*>(to.o + 32 * c + 2 * i + 4 * half) =
+                f32x4{o[c][i] * f, o[c][i + 1] * f, o[c][i + 2] * f, o[c][i + 3] * f};
       }
 #pragma unroll 1
       for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
