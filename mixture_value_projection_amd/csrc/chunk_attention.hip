@@ -107,7 +107,7 @@ Cut cut_of(int G, int rows) {
 
 // What a request brings to the line of work, in keys: each of its row tiles reads
 // keys [lo, hi), and kFixed more for what a tile costs beside them.
-constexpr int kFixed = 192;
+constexpr int kFixed = 320;
 // A stretch of the line is at least this long.
 constexpr int kLeastStretch = 512;
 struct Load {
@@ -279,11 +279,10 @@ struct Sink {
 // the matrix products left infinite or NaN.
 template <int D, bool kFp8>
 __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block, int b, int h,
-                                           size_t qrow, int lo, int hi, const Sink<D>& sink) {
+                                           const bf16_t* q, int lo, int hi, const Sink<D>& sink) {
   constexpr int kPer = D / 64;
   constexpr float kDown = 0x1p-32f;
   const int lane = threadIdx.x & 63;
-  const bf16_t* q = a.q + qrow * D;
   const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
   const int32_t* table = a.table + (size_t)b * a.max_blocks;
   // Element of the pools where the head's row of position p begins, or -1.
@@ -412,12 +411,19 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const int32_t* table = a.table + (size_t)b * a.max_blocks;
 
       // The lane's row: its token and query head.
-      const int r = wave * 32 + r32;
+      int r = wave * 32 + r32;
+      loaded(r);  // no registers between tiles for what follows from it
       const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
       const int token = k * cut.tokens + ti;
       const bool live = ti < cut.tokens && token < w.live && xb * cut.heads + hi < G;
-      const size_t qrow =
-          (size_t)(ch.row0 + token) * a.Hq + (size_t)h * G + xb * cut.heads + hi;
+      // Rows of q and out: from the tile's first one on.
+      const size_t row0 = (size_t)(ch.row0 + k * cut.tokens) * a.Hq + (size_t)h * G + xb * cut.heads;
+      auto row_of = [&](int place) {
+        const int x = fast_div(place, by_heads);
+        return x * a.Hq + (place - x * cut.heads);
+      };
+      const bf16_t* q_rows = a.q + row0 * D;
+      bf16_t* out_rows = a.out + row0 * D;
       // Rows without a token see what is there, with queries of 0.
       const int limit = live ? w.at + token : 0x3fffffff;
       const int lower = live && a.window > 0 ? max(0, limit + 1 - a.window) : 0;
@@ -456,7 +462,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       for (int u = 0; u < kSteps; ++u) {
         Frag16 x;
         x.u = u32x4{0u, 0u, 0u, 0u};
-        if (live) x.u = load16(a.q + qrow * D + 16 * u + 8 * half);
+        if (live) x.u = load16(q_rows + (uint32_t)(row_of(r) * D + 16 * u + 8 * half));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x.u[i] ^= flip;
         if constexpr (T::kQueriesInLds)
@@ -784,10 +790,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
           for (int i = 0; i < 16; ++i) o[c][i] = l == 0.f ? 0.f : o[c][i];
       }
       const float f = l == 0.f ? 0.f : vs / l;
-      auto sink_of = [&](size_t row, int place) {
+      auto sink_of = [&](int place) {
+        const size_t row = (size_t)row_of(place);
         Sink<D> to;
-        to.out = all ? a.out + row * D : nullptr;
-        to.lse = a.lse != nullptr ? a.lse + row : nullptr;
+        to.out = all ? out_rows + row * D : nullptr;
+        to.lse = a.lse != nullptr ? a.lse + row0 + row : nullptr;
         const size_t part = ((size_t)slot * 2 + (seg.begin == seg.first ? 1 : 0)) * T::kRows + place;
         to.o = parts.o + part * D;
         to.ml = parts.ml + part * 2;
@@ -795,7 +802,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       };
       const bool plain = live && !((again >> r32) & 1);
       if (plain && half == 0)
-        sink_of(qrow, r).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
+        sink_of(r).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
       if (all) {
         // Rows lie across the lanes: through LDS (all waves are done with the stages),
         // so that a store has whole rows.
@@ -816,14 +823,15 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         const uint32_t rows = (uint32_t)__ballot(plain);
 #pragma unroll
         for (int i = 0; i < 32 * kPieces / 64; ++i) {
-          const int x = i * 64 + lane, row = x / kPieces, piece = x % kPieces;
-          const size_t to = (size_t)(uint32_t)__shfl((int)qrow, row) |
-                            (size_t)(uint32_t)__shfl((int)(qrow >> 32), row) << 32;
+          int x = i * 64 + lane;
+          loaded(x);  // (as r)
+          const int row = x / kPieces, piece = x % kPieces;
           const u32x4 y = *reinterpret_cast<const u32x4*>(box + row * kOutRow + piece * 16);
-          if ((rows >> row) & 1) store16(a.out + to * D + piece * 8, y);
+          if ((rows >> row) & 1)
+            store16(out_rows + (uint32_t)(row_of(wave * 32 + row) * D + piece * 8), y);
         }
       } else if (plain) {
-        const Sink<D> to = sink_of(qrow, r);
+        const Sink<D> to = sink_of(r);
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
@@ -835,14 +843,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
         const int x = __ffs((int)rest) - 1;
         const int place = wave * 32 + x;
-        const int t2 = fast_div(place, by_heads);
-        const int token2 = k * cut.tokens + t2;
-        const size_t row = (size_t)(ch.row0 + token2) * a.Hq + (size_t)h * G + xb * cut.heads +
-                           (place - t2 * cut.heads);
+        const int token2 = k * cut.tokens + fast_div(place, by_heads);
         const int end = w.at + token2 + 1;
         const int from = a.window > 0 ? max(0, end - a.window) : 0;
-        attend_row<D, kFp8>(a, by_block, b, h, row, max(from, seg.begin * T::kKeys),
-                            min(end, seg.end * T::kKeys), sink_of(row, place));
+        attend_row<D, kFp8>(a, by_block, b, h, q_rows + (size_t)row_of(place) * D, max(from, seg.begin * T::kKeys),
+                            min(end, seg.end * T::kKeys), sink_of(place));
       }
     }
   }
