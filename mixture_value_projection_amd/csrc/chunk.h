@@ -1,0 +1,277 @@
+// What the two kernels of the chunk attention share: the rows of a request, the
+// line of work over the batch, where results go and how parts of them are joined.
+#pragma once
+
+#include "paged.h"
+
+namespace mova {
+
+// Requests of so few rows (tokens times query heads of a key head) are the few-rows
+// kernel's, where it is launched.
+constexpr int kFewRows = 64;
+
+// Floats of scratch of the few-rows kernel, and its launch (with the joining of its
+// parts).
+size_t chunk_few_scratch_floats(int B, int D);
+hipError_t launch_chunk_few(const ChunkArgs& a, float* scratch, hipStream_t stream);
+
+namespace {
+
+constexpr int kCus = 256;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// Request b's rows of the packed tokens and positions in the cache.
+struct Chunk {
+  int row0, rows;  // packed rows [row0, row0 + rows)
+  int at;          // position of the first
+  int live;        // of the rows, how many have a token in the cache
+};
+__device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, int b) {
+  const int most = a.max_blocks * a.block_size;
+  Chunk c;
+  c.row0 = min(max(a.cu_new[b], 0), a.T);
+  c.rows = min(max(a.cu_new[b + 1], c.row0), a.T) - c.row0;
+  c.at = min(max(a.cached[b], 0), most);
+  const int len = a.num_blocks > 0 ? request_len(a.seq_lens, b, a.max_blocks, a.block_size) : 0;
+  c.live = min(max(len - c.at, 0), c.rows);
+  return c;
+}
+
+// 8 elements of the pool.
+template <bool kFp8>
+__device__ __forceinline__ void load8(const void* pool, size_t at, float (&x)[8]) {
+  if constexpr (kFp8) {
+    const uint2 w = *reinterpret_cast<const uint2*>((const uint8_t*)pool + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.x >> (8 * i)), 0);
+      x[4 + i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.y >> (8 * i)), 0);
+    }
+  } else {
+    Frag16 f;
+    f.u = load16((const bf16_t*)pool + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)f.h[i];
+  }
+}
+template <bool kFp8>
+__device__ __forceinline__ float load1(const void* pool, size_t at) {
+  if constexpr (kFp8) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)pool)[at], 0);
+  else return (float)((const bf16_t*)pool)[at];
+}
+
+// Parts of rows that were split over stretches: two for each workgroup, of the
+// tile that its stretch begins in and of the one that it ends in.
+struct Parts {
+  long long* prefix;  // [B] first unit of each request, then the stretch
+  float* ml;          // [two a workgroup][rows][2] maximum (in powers of two) and sum
+  float* o;           // [two a workgroup][rows][D] out, divided by the sum
+};
+size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
+
+struct Shared {
+  long long tmp[8];
+  long long first;
+  int b;
+};
+// As line_begin, for workgroups of kWaves waves.  `slot`: which stretch; `least`: units of
+// one at least.
+template <int kWaves, class Cost>
+__device__ __forceinline__ bool chunk_line(int B, int slot, int slots, int least, Cost cost,
+                                           Shared& sh, long long* prefix, Line* line) {
+  constexpr int kThreads = 64 * kWaves;
+  const int per = ceil_div(B, kThreads);
+  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
+  // The thread's first request (up to 256 the only one) is looked at once.
+  const long long cost0 = b0 < b1 ? cost(b0) : 0;
+  auto cost_of = [&](int b) { return b == b0 ? cost0 : cost(b); };
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += cost_of(b);
+  long long before = block_exclusive_scan<kWaves>(mine, sh.tmp, &total);
+  line->stretch = max(floor_div(total + slots - 1, slots), (long long)least);
+  line->start = line->stretch * slot;
+  line->end = min(line->start + line->stretch, total);
+  if (before <= line->start && line->start < before + mine) {
+    long long at = before;
+    int b = b0;
+    for (long long c; line->start >= at + (c = cost_of(b)); ++b) at += c;
+    sh.b = b;
+    sh.first = at;
+  }
+  if (prefix != nullptr && slot == 0) {
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = before;
+      before += cost_of(b);
+    }
+    if (threadIdx.x == 0) prefix[B] = line->stretch;
+  }
+  __syncthreads();
+  if (line->start >= total) return false;
+  line->b = __builtin_amdgcn_readfirstlane(sh.b);
+  line->first = (long long)read_lane((double)sh.first, 0);
+  return true;
+}
+
+// Where a row's result goes: its place in the output, or in the parts.
+template <int D>
+struct Sink {
+  bf16_t* out;  // null: the parts
+  float* lse;   // null: none
+  float* o;
+  float* ml;
+  __device__ __forceinline__ void put1(int c, float y) const {
+    if (out != nullptr) out[c] = (bf16_t)y;
+    else o[c] = y;
+  }
+  // m: the maximum in powers of two, l: the sum of exp2(. - m).
+  __device__ __forceinline__ void put_sum(float m, float l) const {
+    if (out == nullptr) {
+      ml[0] = m;
+      ml[1] = l;
+    } else if (lse != nullptr) {
+      *lse = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+  }
+};
+
+// One row by one wave with everything in fp32, a lane a key for the logits and
+// D / 64 channels a lane for the values: the maximum first, then weights and
+// sums.  Only keys that take part are touched, so infinite and NaN values of
+// others do not show, and sums that pass the largest number are formed with
+// weights 2^-32 as large (a row has at most 2^30 keys).  For the rows whose sums
+// the matrix products left infinite or NaN.
+template <int D, bool kFp8>
+__device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block, int b, int h,
+                                           const bf16_t* q, int lo, int hi, const Sink<D>& sink) {
+  constexpr int kPer = D / 64;
+  constexpr float kDown = 0x1p-32f;
+  const int lane = threadIdx.x & 63;
+  const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
+  const int32_t* table = a.table + (size_t)b * a.max_blocks;
+  // Element of the pools where the head's row of position p begins, or -1.
+  auto place = [&](int p) -> long long {
+    if (p >= hi) return -1;
+    const int j = fast_div(p, by_block);
+    const int page = table[j];
+    if (page < 0 || page >= a.num_blocks) return -1;
+    return (((long long)page * a.block_size + (p - j * a.block_size)) * a.H + h) * D;
+  };
+  auto logit = [&](long long at) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+      float k[8], x[8];
+      load8<kFp8>(a.k_cache, (size_t)at + d, k);
+      load8<false>(q, d, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(k[i], x[i], s);
+    }
+    return s * qs;
+  };
+  float m = -__builtin_huge_valf();
+#pragma unroll 1
+  for (int p = lo; p < hi; p += 64) {
+    const long long at = place(p + lane);
+    if (at >= 0) m = fmaxf(m, logit(at));
+  }
+  m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
+  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
+  float l = 0.f, o[kPer] = {}, less[kPer] = {};
+#pragma unroll 1
+  for (int p = lo; p < hi; p += 64) {
+    const long long at = place(p + lane);
+    const float w = at >= 0 ? __builtin_amdgcn_exp2f(logit(at) - safe) : 0.f;
+    l += w;
+#pragma unroll 1
+    for (uint64_t there = __ballot(at >= 0); there != 0; there &= there - 1) {
+      const int i = __ffsll((unsigned long long)there) - 1;
+      const float wi = __shfl(w, i);
+      const size_t from = (size_t)__shfl(at, i) + lane * kPer;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float v = load1<kFp8>(a.v_cache, from + j);
+        o[j] = fmaf(wi, v, o[j]);
+        less[j] = fmaf(wi * kDown, v, less[j]);
+      }
+    }
+  }
+  l = wave_sum(l);
+  const float f = l == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[h] : 1.f) / l;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const float y = fabsf(o[j]) < __builtin_huge_valf() ? o[j] * f : less[j] * (f / kDown);
+    sink.put1(lane * kPer + j, l == 0.f ? 0.f : y);
+  }
+  if (lane == 0) sink.put_sum(m, l);
+}
+
+// Zeros for the rows that have no token in the cache; the whole grid takes part.
+__device__ __forceinline__ void clear_rows(const ChunkArgs& a) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Chunk c = chunk_of(a, b);
+    const size_t from = (size_t)(c.row0 + c.live) * a.Hq, to = (size_t)(c.row0 + c.rows) * a.Hq;
+    for (size_t i = from * a.D + threadIdx.x * 8; i < to * a.D; i += blockDim.x * 8)
+      store16(a.out + i, u32x4{0u, 0u, 0u, 0u});
+    if (a.lse != nullptr)
+      for (size_t i = from + threadIdx.x; i < to; i += blockDim.x) a.lse[i] = -__builtin_huge_valf();
+  }
+}
+
+// A row's parts joined by one wave: part_of(x) for x in [0, n) is a part's row in
+// `parts`, or -1.  The sums are looked at first, a lane a part; then 64 / (D / 4)
+// parts are added at a time, eight of them asked for ahead, four channels a lane.
+template <int D, class PartOf>
+__device__ __forceinline__ void join_row(const Parts& parts, int n, PartOf part_of, bf16_t* out,
+                                         float* lse) {
+  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kBatch = 8;
+  const int lane = threadIdx.x & 63;
+  const int mine = lane / kLanes, channel = lane % kLanes * 4;
+  float m = -__builtin_huge_valf();
+  for (int x = lane; x < n; x += 64) {
+    const long long p = part_of(x);
+    if (p >= 0 && parts.ml[2 * p + 1] != 0.f) m = fmaxf(m, parts.ml[2 * p]);
+  }
+  m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
+  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
+  auto weight = [&](long long p) {
+    return p < 0 ? 0.f : parts.ml[2 * p + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
+  };
+  float sum = 0.f;
+  for (int x = lane; x < n; x += 64) sum += weight(part_of(x));
+  sum = wave_sum(sum);
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+  for (int x = 0; x < n; x += kAtOnce * kBatch) {
+    float w[kBatch];
+    f32x4 y[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = x + i * kAtOnce + mine;
+      const long long p = at < n ? part_of(at) : -1;
+      w[i] = weight(p) * f;
+      y[i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)max(p, 0ll) * D + channel);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)  // (what a part without weight holds may be anything)
+        o[c] = w[i] == 0.f ? o[c] : fmaf(w[i], y[i][c], o[c]);
+  }
+#pragma unroll
+  for (int step = kLanes; step < 64; step *= 2)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], step);
+  if (mine == 0) {
+    uint2 y;
+    y.x = (uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16);
+    y.y = (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16);
+    *reinterpret_cast<uint2*>(out + channel) = y;
+  }
+  if (lse != nullptr && lane == 0)
+    *lse = sum == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+}  // namespace
+
+}  // namespace mova

@@ -8,55 +8,12 @@
 #include <algorithm>
 #include <atomic>
 
+#include "chunk.h"
 #include "kernels.h"
-#include "paged.h"
 
 namespace mova {
 
 namespace {
-
-constexpr int kCus = 256;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
-// Request b's rows of the packed tokens and positions in the cache.
-struct Chunk {
-  int row0, rows;  // packed rows [row0, row0 + rows)
-  int at;          // position of the first
-  int live;        // of the rows, how many have a token in the cache
-};
-__device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, int b) {
-  const int most = a.max_blocks * a.block_size;
-  Chunk c;
-  c.row0 = min(max(a.cu_new[b], 0), a.T);
-  c.rows = min(max(a.cu_new[b + 1], c.row0), a.T) - c.row0;
-  c.at = min(max(a.cached[b], 0), most);
-  const int len = a.num_blocks > 0 ? request_len(a.seq_lens, b, a.max_blocks, a.block_size) : 0;
-  c.live = min(max(len - c.at, 0), c.rows);
-  return c;
-}
-
-// 8 elements of the pool.
-template <bool kFp8>
-__device__ __forceinline__ void load8(const void* pool, size_t at, float (&x)[8]) {
-  if constexpr (kFp8) {
-    const uint2 w = *reinterpret_cast<const uint2*>((const uint8_t*)pool + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.x >> (8 * i)), 0);
-      x[4 + i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.y >> (8 * i)), 0);
-    }
-  } else {
-    Frag16 f;
-    f.u = load16((const bf16_t*)pool + at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)f.h[i];
-  }
-}
-template <bool kFp8>
-__device__ __forceinline__ float load1(const void* pool, size_t at) {
-  if constexpr (kFp8) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)pool)[at], 0);
-  else return (float)((const bf16_t*)pool)[at];
-}
 
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
@@ -145,9 +102,9 @@ struct Load {
     return lo_;
   }
 };
-__device__ __forceinline__ Load load_of(const ChunkArgs& a, int tokens, int b) {
-  const Chunk c = chunk_of(a, b);
-  return Load{c.at, c.live, tokens, a.window};
+// Whether the request is this kernel's.
+__device__ __forceinline__ bool many_rows(const ChunkArgs& a, const Chunk& c) {
+  return c.live * (a.Hq / a.H) > a.few;
 }
 
 // Key tiles [begin, end) of a row tile that units [x0, x1) of it stand for; all
@@ -170,57 +127,6 @@ __device__ __forceinline__ Segment segment_of(const Load& w, int k, long long x0
   s.begin = at(x0);
   s.end = at(x1);
   return s;
-}
-
-// Parts of rows that were split over stretches: two for each workgroup, of the
-// tile that its stretch begins in and of the one that it ends in.
-struct Parts {
-  long long* prefix;  // [B] first unit of each request, then the stretch
-  float* ml;          // [two a workgroup][rows][2] maximum (in powers of two) and sum
-  float* o;           // [two a workgroup][rows][D] out
-};
-size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
-
-struct Shared {
-  long long tmp[8];
-  long long first;
-  int b;
-};
-// As line_begin, for workgroups of kWaves waves.  `slot`: which stretch.
-template <int kWaves, class Cost>
-__device__ __forceinline__ bool chunk_line(int B, int slot, int slots, Cost cost, Shared& sh,
-                                           long long* prefix, Line* line) {
-  constexpr int kThreads = 64 * kWaves;
-  const int per = ceil_div(B, kThreads);
-  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
-  // The thread's first request (up to 256 the only one) is looked at once.
-  const long long cost0 = b0 < b1 ? cost(b0) : 0;
-  auto cost_of = [&](int b) { return b == b0 ? cost0 : cost(b); };
-  long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += cost_of(b);
-  long long before = block_exclusive_scan<kWaves>(mine, sh.tmp, &total);
-  line->stretch = max(floor_div(total + slots - 1, slots), (long long)kLeastStretch);
-  line->start = line->stretch * slot;
-  line->end = min(line->start + line->stretch, total);
-  if (before <= line->start && line->start < before + mine) {
-    long long at = before;
-    int b = b0;
-    for (long long c; line->start >= at + (c = cost_of(b)); ++b) at += c;
-    sh.b = b;
-    sh.first = at;
-  }
-  if (prefix != nullptr && slot == 0) {
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = before;
-      before += cost_of(b);
-    }
-    if (threadIdx.x == 0) prefix[B] = line->stretch;
-  }
-  __syncthreads();
-  if (line->start >= total) return false;
-  line->b = __builtin_amdgcn_readfirstlane(sh.b);
-  line->first = (long long)read_lane((double)sh.first, 0);
-  return true;
 }
 
 // Maximum of lanes i and i + 32, in both.
@@ -249,99 +155,6 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
              two(w[3], true_type{})};
 }
 
-// Where a row's result goes: its place in the output, or in the parts.
-template <int D>
-struct Sink {
-  bf16_t* out;  // null: the parts
-  float* lse;   // null: none
-  float* o;
-  float* ml;
-  __device__ __forceinline__ void put1(int c, float y) const {
-    if (out != nullptr) out[c] = (bf16_t)y;
-    else o[c] = y;
-  }
-  // m: the maximum in powers of two, l: the sum of exp2(. - m).
-  __device__ __forceinline__ void put_sum(float m, float l) const {
-    if (out == nullptr) {
-      ml[0] = m;
-      ml[1] = l;
-    } else if (lse != nullptr) {
-      *lse = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
-    }
-  }
-};
-
-// One row by one wave with everything in fp32, a lane a key for the logits and
-// D / 64 channels a lane for the values: the maximum first, then weights and
-// sums.  Only keys that take part are touched, so infinite and NaN values of
-// others do not show, and sums that pass the largest number are formed with
-// weights 2^-32 as large (a row has at most 2^30 keys).  For the rows whose sums
-// the matrix products left infinite or NaN.
-template <int D, bool kFp8>
-__device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block, int b, int h,
-                                           const bf16_t* q, int lo, int hi, const Sink<D>& sink) {
-  constexpr int kPer = D / 64;
-  constexpr float kDown = 0x1p-32f;
-  const int lane = threadIdx.x & 63;
-  const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
-  const int32_t* table = a.table + (size_t)b * a.max_blocks;
-  // Element of the pools where the head's row of position p begins, or -1.
-  auto place = [&](int p) -> long long {
-    if (p >= hi) return -1;
-    const int j = fast_div(p, by_block);
-    const int page = table[j];
-    if (page < 0 || page >= a.num_blocks) return -1;
-    return (((long long)page * a.block_size + (p - j * a.block_size)) * a.H + h) * D;
-  };
-  auto logit = [&](long long at) {
-    float s = 0.f;
-#pragma unroll 1
-    for (int d = 0; d < D; d += 8) {
-      float k[8], x[8];
-      load8<kFp8>(a.k_cache, (size_t)at + d, k);
-      load8<false>(q, d, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(k[i], x[i], s);
-    }
-    return s * qs;
-  };
-  float m = -__builtin_huge_valf();
-#pragma unroll 1
-  for (int p = lo; p < hi; p += 64) {
-    const long long at = place(p + lane);
-    if (at >= 0) m = fmaxf(m, logit(at));
-  }
-  m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
-  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
-  float l = 0.f, o[kPer] = {}, less[kPer] = {};
-#pragma unroll 1
-  for (int p = lo; p < hi; p += 64) {
-    const long long at = place(p + lane);
-    const float w = at >= 0 ? __builtin_amdgcn_exp2f(logit(at) - safe) : 0.f;
-    l += w;
-#pragma unroll 1
-    for (uint64_t there = __ballot(at >= 0); there != 0; there &= there - 1) {
-      const int i = __ffsll((unsigned long long)there) - 1;
-      const float wi = __shfl(w, i);
-      const size_t from = (size_t)__shfl(at, i) + lane * kPer;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float v = load1<kFp8>(a.v_cache, from + j);
-        o[j] = fmaf(wi, v, o[j]);
-        less[j] = fmaf(wi * kDown, v, less[j]);
-      }
-    }
-  }
-  l = wave_sum(l);
-  const float f = l == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[h] : 1.f) / l;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const float y = fabsf(o[j]) < __builtin_huge_valf() ? o[j] * f : less[j] * (f / kDown);
-    sink.put1(lane * kPer + j, l == 0.f ? 0.f : y);
-  }
-  if (lane == 0) sink.put_sum(m, l);
-}
-
 }  // namespace
 
 template <int D, bool kFp8>
@@ -366,11 +179,12 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
   int* slots_of_keys = (int*)(stages + 2 * T::kStage);
 
   auto cost = [&](int b) {
-    const Load w = load_of(a, cut.tokens, b);
-    return w.live == 0 ? 0ll : jobs * w.before(w.tiles());
+    const Chunk c = chunk_of(a, b);
+    const Load w{c.at, c.live, cut.tokens, a.window};
+    return many_rows(a, c) ? jobs * w.before(w.tiles()) : 0ll;
   };
   Line line;
-  const bool work = chunk_line<T::kWaves>(a.B, slot, slots, cost, s_line, parts.prefix, &line);
+  const bool work = chunk_line<T::kWaves>(a.B, slot, slots, kLeastStretch, cost, s_line, parts.prefix, &line);
 
   // This thread's pieces of a tile.
   const int my_key = tid / T::kPieces, my_piece = tid % T::kPieces;
@@ -396,7 +210,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       do {
         if (++b >= a.B) return;
         ch = chunk_of(a, b);
-      } while (ch.live == 0);
+      } while (!many_rows(a, ch));
       w = Load{ch.at, ch.live, cut.tokens, a.window};
       tiles = w.tiles();
     };
@@ -852,15 +666,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
     }
   }
 
-  // Rows that have no token in the cache.
-  for (int x = blockIdx.x; x < a.B; x += gridDim.x) {
-    const Chunk c = chunk_of(a, x);
-    const size_t from = (size_t)(c.row0 + c.live) * a.Hq, to = (size_t)(c.row0 + c.rows) * a.Hq;
-    for (size_t i = from * D + tid * 8; i < to * D; i += T::kThreads * 8)
-      store16(a.out + i, u32x4{0u, 0u, 0u, 0u});
-    if (a.lse != nullptr)
-      for (size_t i = from + tid; i < to; i += T::kThreads) a.lse[i] = -__builtin_huge_valf();
-  }
+  if (a.few == 0) clear_rows(a);
 }
 
 // Adds the parts of rows that were split over stretches: workgroup (x, y) takes
@@ -870,10 +676,6 @@ template <int D, bool kFp8>
 __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, Parts parts, Cut cut,
                                                          FastDiv by_heads, int slots) {
   using T = Tile<D, kFp8>;
-  constexpr int kPer = D / 64;
-  typedef __attribute__((__vector_size__(kPer * sizeof(float)))) float vec;
-  typedef __attribute__((__vector_size__(kPer * sizeof(__bf16)))) __bf16 half_vec;
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.Hq / a.H, jobs = a.H * cut.head_blocks;
   const int slot = blockIdx.x;
@@ -883,7 +685,7 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, Parts part
   const int b = __builtin_amdgcn_readfirstlane(last_at_most(parts.prefix, a.B, end - 1));
   const Chunk ch = chunk_of(a, b);
   const Load w{ch.at, ch.live, cut.tokens, a.window};
-  if (w.live == 0) return;
+  if (!many_rows(a, ch)) return;
   const long long first = parts.prefix[b], units = w.before(w.tiles());
   if (end >= first + jobs * units) return;  // the line's end, or the request's
   const int job = (int)floor_div(end - 1 - first, units);
@@ -893,44 +695,27 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, Parts part
   if (tile0 < start || tile0 + size <= end) return;
   const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
   const int last = min((int)floor_div(tile0 + size - 1, stretch), slots - 1);
-  auto part_of = [&](int x, bool* some, bool* whole) {
+  // (One stretch may hold all of the tile's keys: it wrote the rows itself.)
+  bool whole = false;
+  for (int x = slot; x <= last; ++x) {
     const Segment s =
         segment_of<T::kKeys>(w, k, max(stretch * x - tile0, 0ll), min(stretch * (x + 1) - tile0, size));
-    *some = s.begin < s.end;
-    *whole = s.begin == s.first && s.end == s.last;
-    return (size_t)x * 2 + (s.begin == s.first ? 1 : 0);
-  };
+    whole = whole || (s.begin == s.first && s.end == s.last);
+  }
+  if (whole) return;
   for (int r = blockIdx.y * 4 + wave; r < T::kRows; r += gridDim.y * 4) {
     const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
     const int token = k * cut.tokens + ti;
     if (ti >= cut.tokens || token >= w.live || xb * cut.heads + hi >= G) continue;
     const size_t row = (size_t)(ch.row0 + token) * a.Hq + (size_t)h * G + xb * cut.heads + hi;
-    float m = -__builtin_huge_valf(), l = 0.f;
-    vec o = {};
-    bool some, whole = false;
-    for (int x = slot; x <= last; ++x) {
-      const size_t part = part_of(x, &some, &whole) * T::kRows + r;
-      if (whole) break;
-      if (!some) continue;
-      const float m2 = parts.ml[part * 2], l2 = parts.ml[part * 2 + 1];
-      const vec o2 = *reinterpret_cast<const vec*>(parts.o + part * D + kPer * lane);
-      if (l2 == 0.f) continue;
-      const float mn = fmaxf(m, m2);
-      const float safe = mn == -__builtin_huge_valf() ? 0.f : mn;
-      const float w1 = l * __builtin_amdgcn_exp2f(m - safe), w2 = l2 * __builtin_amdgcn_exp2f(m2 - safe);
-      l = w1 + w2;
-      m = mn;
-      const float f1 = w1 / l, f2 = w2 / l;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] = (w1 == 0.f ? 0.f : o[i] * f1) + o2[i] * f2;
-    }
-    if (whole) continue;
-    half_vec y;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] = (__bf16)o[i];
-    *reinterpret_cast<half_vec*>(a.out + row * D + kPer * lane) = y;
-    if (a.lse != nullptr && lane == 0)
-      a.lse[row] = l == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    auto part_of = [&](int i) -> long long {
+      const long long x = slot + i;
+      const Segment s = segment_of<T::kKeys>(w, k, max(stretch * x - tile0, 0ll),
+                                             min(stretch * (x + 1) - tile0, size));
+      return s.begin < s.end ? (x * 2 + (s.begin == s.first ? 1 : 0)) * T::kRows + r : -1;
+    };
+    join_row<D>(parts, last - slot + 1, part_of, a.out + row * D,
+                a.lse != nullptr ? a.lse + row : nullptr);
   }
 }
 
@@ -957,7 +742,7 @@ hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
       a, parts, make_fast_div(a.block_size), cut, by_heads);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  chunk_join_kernel<D, kFp8><<<dim3(kCus, 8), 256, 0, stream>>>(
+  chunk_join_kernel<D, kFp8><<<dim3(kCus, 32), 256, 0, stream>>>(
       a, parts, cut, by_heads, kCus);
   return hipGetLastError();
 }
@@ -966,10 +751,21 @@ hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
 
 size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D) {
   if (T == 0 || B == 0) return 0;
-  return prefix_floats(B) + part_rows(D) * (2 + D);
+  return prefix_floats(B) + part_rows(D) * (2 + D) + chunk_few_scratch_floats(B, D);
 }
 
-hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream) {
+// Requests of few rows (single tokens, drafts) are read by the few-rows kernel, whose
+// waves go through keys of their own, where such requests are most: where the rows of
+// the batch, whose lengths the host does not know, are on average as few.
+hipError_t launch_chunk_attention(const ChunkArgs& all, hipStream_t stream) {
+  ChunkArgs a = all;
+  const long long rows = (long long)a.T * (a.Hq / a.H);
+  a.few = rows <= (long long)kFewRows * a.B ? kFewRows : 0;
+  if (a.few > 0) {
+    float* scratch = a.part + prefix_floats(a.B) + part_rows(a.D) * (2 + a.D);
+    const hipError_t e = launch_chunk_few(a, scratch, stream);
+    if (e != hipSuccess || rows <= kFewRows) return e;
+  }
   const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
     case 64: return fp8 ? launch_cfg<64, true>(a, stream) : launch_cfg<64, false>(a, stream);

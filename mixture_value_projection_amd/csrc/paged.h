@@ -119,6 +119,7 @@ struct ChunkArgs {
   __bf16* out;  // [T, Hq, D]
   float* lse;   // [T, Hq] or null
   float* part;  // scratch of chunk_scratch_floats
+  int few = 0;  // requests of at most so many rows are the few-rows kernel's
 };
 // Floats of scratch; depends on the sizes alone.
 size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D);
