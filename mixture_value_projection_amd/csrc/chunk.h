@@ -10,10 +10,34 @@ namespace mova {
 // kernel's, where it is launched.
 constexpr int kFewRows = 64;
 
-// Floats of scratch of the few-rows kernel, and its launch (with the joining of its
-// parts).
-size_t chunk_few_scratch_floats(int B, int D);
-hipError_t launch_chunk_few(const ChunkArgs& a, float* scratch, hipStream_t stream);
+// What a stretch leaves to be joined.
+struct Split {
+  long long row0;    // the rows' place in the output
+  long long before;  // units of the stretch ahead of them
+  int n;             // stretches; 0: nothing was split
+  int lo, hi;        // keys
+  int rows, heads;   // tokens and query heads
+  int pad;
+};
+// Rows whose keys were split over stretches: each stretch leaves its part, at place
+// 2 slot + 1 where it holds the beginning and 2 slot where it goes on, and the one that
+// they begin in says what there is to join.
+struct Parts {
+  Split* split;  // [a workgroup]
+  float* ml;     // [two a workgroup][rows][2] maximum (in powers of two) and sum
+  float* o;      // [two a workgroup][rows][D] out, divided by the sum
+};
+
+constexpr size_t split_floats(int groups) { return (size_t)groups * sizeof(Split) / 4; }
+static_assert(sizeof(Split) % 8 == 0, "whole words");
+
+// Of the few-rows kernel: floats of scratch, workgroups, key heads (tracks) of one, the
+// parts in the scratch, and the launch, without the joining of its parts.
+size_t chunk_few_scratch_floats(int D);
+int chunk_few_groups(const ChunkArgs& a);
+int chunk_few_tracks(int H);
+Parts chunk_few_parts(float* scratch);
+hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, hipStream_t stream);
 
 namespace {
 
@@ -60,15 +84,6 @@ __device__ __forceinline__ float load1(const void* pool, size_t at) {
   else return (float)((const bf16_t*)pool)[at];
 }
 
-// Parts of rows that were split over stretches: two for each workgroup, of the
-// tile that its stretch begins in and of the one that it ends in.
-struct Parts {
-  long long* prefix;  // [B] first unit of each request, then the stretch
-  float* ml;          // [two a workgroup][rows][2] maximum (in powers of two) and sum
-  float* o;           // [two a workgroup][rows][D] out, divided by the sum
-};
-size_t prefix_floats(int B) { return ((size_t)(B + 1) * 2 + 63) / 64 * 64; }
-
 struct Shared {
   long long tmp[8];
   long long first;
@@ -78,7 +93,7 @@ struct Shared {
 // one at least.
 template <int kWaves, class Cost>
 __device__ __forceinline__ bool chunk_line(int B, int slot, int slots, int least, Cost cost,
-                                           Shared& sh, long long* prefix, Line* line) {
+                                           Shared& sh, Line* line) {
   constexpr int kThreads = 64 * kWaves;
   const int per = ceil_div(B, kThreads);
   const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
@@ -97,13 +112,6 @@ __device__ __forceinline__ bool chunk_line(int B, int slot, int slots, int least
     for (long long c; line->start >= at + (c = cost_of(b)); ++b) at += c;
     sh.b = b;
     sh.first = at;
-  }
-  if (prefix != nullptr && slot == 0) {
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = before;
-      before += cost_of(b);
-    }
-    if (threadIdx.x == 0) prefix[B] = line->stretch;
   }
   __syncthreads();
   if (line->start >= total) return false;
@@ -217,59 +225,126 @@ __device__ __forceinline__ void clear_rows(const ChunkArgs& a) {
   }
 }
 
-// A row's parts joined by one wave: part_of(x) for x in [0, n) is a part's row in
-// `parts`, or -1.  The sums are looked at first, a lane a part; then 64 / (D / 4)
-// parts are added at a time, eight of them asked for ahead, four channels a lane.
-template <int D, class PartOf>
-__device__ __forceinline__ void join_row(const Parts& parts, int n, PartOf part_of, bf16_t* out,
-                                         float* lse) {
+// Four channels of a joined row, and its lse once a row.
+template <int D>
+__device__ __forceinline__ void put_joined(const ChunkArgs& a, size_t row, int channel, f32x4 o,
+                                           float m, float sum) {
+  uint2 y;
+  y.x = (uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16);
+  y.y = (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16);
+  *reinterpret_cast<uint2*>(a.out + row * D + channel) = y;
+  if (a.lse != nullptr && channel == 0)
+    a.lse[row] = sum == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+__device__ __forceinline__ float finite_or_0(float m) {
+  return m == -__builtin_huge_valf() ? 0.f : m;
+}
+// o += w y; what a part without weight holds may be anything.
+__device__ __forceinline__ void add_part(f32x4& o, float w, const f32x4& y) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) o[c] = w == 0.f ? o[c] : fmaf(w, y[c], o[c]);
+}
+
+// Joins the parts of `rows` rows, n of each, with the kWaves waves of the gridDim.y
+// workgroups of a stretch.  part_of(r, i) is a part's place, or -1; row_of(r) the row's
+// in the output, or -1.
+//
+// Of up to kFew parts a row has D / 4 lanes, and a wave asks for all parts of kSets such
+// sets of rows at once: there are many rows, and what they cost is the round trips.  (The
+// parts of 255 tiles of 256 rows, 128 wide, two of each: a wave a row 44 us, so 26.)  Of
+// more parts a row has a wave: the maxima and sums come first, a lane a part, and then
+// the parts, 64 / (D / 4) times eight of them at once.
+template <int D, int kWaves, int kFew, int kSets, class PartOf, class RowOf>
+__device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts, int rows, int n,
+                                          PartOf part_of, RowOf row_of) {
   constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kBatch = 8;
   const int lane = threadIdx.x & 63;
+  const int wave = blockIdx.y * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = gridDim.y * kWaves;
   const int mine = lane / kLanes, channel = lane % kLanes * 4;
-  float m = -__builtin_huge_valf();
-  for (int x = lane; x < n; x += 64) {
-    const long long p = part_of(x);
-    if (p >= 0 && parts.ml[2 * p + 1] != 0.f) m = fmaxf(m, parts.ml[2 * p]);
-  }
-  m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
-  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
-  auto weight = [&](long long p) {
-    return p < 0 ? 0.f : parts.ml[2 * p + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * p] - safe);
-  };
-  float sum = 0.f;
-  for (int x = lane; x < n; x += 64) sum += weight(part_of(x));
-  sum = wave_sum(sum);
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll 1
-  for (int x = 0; x < n; x += kAtOnce * kBatch) {
-    float w[kBatch];
-    f32x4 y[kBatch];
+  if (n <= kFew) {
+    for (int r0 = wave * kAtOnce + mine; r0 < rows; r0 += waves * kAtOnce * kSets) {
+      float pm[kSets][kFew], pl[kSets][kFew];
+      f32x4 y[kSets][kFew];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int at = x + i * kAtOnce + mine;
-      const long long p = at < n ? part_of(at) : -1;
-      w[i] = weight(p) * f;
-      y[i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)max(p, 0ll) * D + channel);
+      for (int s = 0; s < kSets; ++s) {
+        const int r = r0 + s * waves * kAtOnce;
+        const bool live = r < rows && row_of(r) >= 0;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          const long long p = live && i < n ? part_of(r, i) : -1;
+          pm[s][i] = -__builtin_huge_valf();
+          pl[s][i] = 0.f;
+          y[s][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (p >= 0) {
+            pm[s][i] = parts.ml[2 * p];
+            pl[s][i] = parts.ml[2 * p + 1];
+            y[s][i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)p * D + channel);
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kSets; ++s) {
+        const int r = r0 + s * waves * kAtOnce;
+        const long long row = r < rows ? row_of(r) : -1;
+        if (row < 0) continue;
+        float m = -__builtin_huge_valf(), sum = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+          if (pl[s][i] != 0.f) m = fmaxf(m, pm[s][i]);
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+          pl[s][i] = pl[s][i] == 0.f
+                         ? 0.f
+                         : pl[s][i] * __builtin_amdgcn_exp2f(pm[s][i] - finite_or_0(m));
+          sum += pl[s][i];
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) add_part(o, pl[s][i] * f, y[s][i]);
+        put_joined<D>(a, (size_t)row, channel, o, m, sum);
+      }
+    }
+    return;
+  }
+  for (int r = wave; r < rows; r += waves) {
+    const long long row = row_of(r);
+    if (row < 0) continue;
+    float m = -__builtin_huge_valf(), sum = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int x = lane; x < n; x += 64) {
+      const long long p = part_of(r, x);
+      if (p >= 0 && parts.ml[2 * p + 1] != 0.f) m = fmaxf(m, parts.ml[2 * p]);
+    }
+    m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
+    auto weight = [&](long long p) {
+      const float l = p < 0 ? 0.f : parts.ml[2 * p + 1];
+      return l == 0.f ? 0.f : l * __builtin_amdgcn_exp2f(parts.ml[2 * p] - finite_or_0(m));
+    };
+    for (int x = lane; x < n; x += 64) sum += weight(part_of(r, x));
+    sum = wave_sum(sum);
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+    for (int x = 0; x < n; x += kAtOnce * kBatch) {
+      float w[kBatch];
+      f32x4 y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int at = x + i * kAtOnce + mine;
+        const long long p = at < n ? part_of(r, at) : -1;
+        w[i] = weight(p) * f;
+        y[i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)max(p, 0ll) * D + channel);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add_part(o, w[i], y[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int step = kLanes; step < 64; step *= 2)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)  // (what a part without weight holds may be anything)
-        o[c] = w[i] == 0.f ? o[c] : fmaf(w[i], y[i][c], o[c]);
+      for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], step);
+    if (mine == 0) put_joined<D>(a, (size_t)row, channel, o, m, sum);
   }
-#pragma unroll
-  for (int step = kLanes; step < 64; step *= 2)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], step);
-  if (mine == 0) {
-    uint2 y;
-    y.x = (uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16);
-    y.y = (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16);
-    *reinterpret_cast<uint2*>(out + channel) = y;
-  }
-  if (lse != nullptr && lane == 0)
-    *lse = sum == 0.f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 }  // namespace

@@ -107,14 +107,13 @@ __device__ __forceinline__ bool many_rows(const ChunkArgs& a, const Chunk& c) {
   return c.live * (a.Hq / a.H) > a.few;
 }
 
-// Key tiles [begin, end) of a row tile that units [x0, x1) of it stand for; all
-// of them together are [first, last).
+// Key tiles [begin, end) that units [x0, x1) of a row tile over keys [lo, hi) stand
+// for; all of them together are [first, last).
 struct Segment {
   int begin, end, first, last;
 };
 template <int kKeys>
-__device__ __forceinline__ Segment segment_of(const Load& w, int k, long long x0, long long x1) {
-  const int lo = w.lo(k), hi = w.hi(k);
+__device__ __forceinline__ Segment segment_of(int lo, int hi, long long x0, long long x1) {
   const long long units = hi - lo + kFixed;
   Segment s;
   s.first = lo / kKeys;
@@ -159,7 +158,7 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 
 template <int D, bool kFp8>
 __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_kernel(
-    ChunkArgs a, Parts parts, FastDiv by_block, Cut cut, FastDiv by_heads) {
+    ChunkArgs a, Parts parts, FastDiv by_block, Cut cut, FastDiv by_heads, long long* stretch_of) {
   using T = Tile<D, kFp8>;
   constexpr int kSteps = D / 16;    // products along the channels
   constexpr int kBlocks = D / 32;   // 32-channel blocks of the output
@@ -184,12 +183,14 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
     return many_rows(a, c) ? jobs * w.before(w.tiles()) : 0ll;
   };
   Line line;
-  const bool work = chunk_line<T::kWaves>(a.B, slot, slots, kLeastStretch, cost, s_line, parts.prefix, &line);
+  const bool work = chunk_line<T::kWaves>(a.B, slot, slots, kLeastStretch, cost, s_line, &line);
 
   // This thread's pieces of a tile.
   const int my_key = tid / T::kPieces, my_piece = tid % T::kPieces;
   const bool my_load = T::kTotal >= T::kThreads || tid < T::kTotal;
 
+  if (tid == 0) parts.split[slot].n = 0;
+  if (tid == 0 && slot == 0) *stretch_of = line.stretch;
   if (work) {
     int b = line.b;
     Chunk ch = chunk_of(a, b);
@@ -217,7 +218,20 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
     for (long long left = line.end - line.start; left > 0 && b < a.B; advance()) {
       const long long x1 = min(w.units(k), x0 + left);
       left -= x1 - x0;
-      const Segment seg = segment_of<T::kKeys>(w, k, x0, x1);
+      const Segment seg = segment_of<T::kKeys>(w.lo(k), w.hi(k), x0, x1);
+      if (x0 == 0 && x1 < w.units(k) && tid == 0) {
+        const int xb = job % cut.head_blocks;
+        Split p;
+        p.row0 = (long long)(ch.row0 + k * cut.tokens) * a.Hq +
+                 (long long)(job / cut.head_blocks) * G + xb * cut.heads;
+        p.before = line.stretch - x1;
+        p.n = (int)floor_div(p.before + w.units(k) - 1, line.stretch) + 1;
+        p.lo = w.lo(k);
+        p.hi = w.hi(k);
+        p.rows = min(cut.tokens, w.live - k * cut.tokens);
+        p.heads = min(cut.heads, G - xb * cut.heads);
+        parts.split[slot] = p;
+      }
       if (seg.begin >= seg.end) continue;
       const bool all = seg.begin == seg.first && seg.end == seg.last;
       const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
@@ -669,62 +683,73 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
   if (a.few == 0) clear_rows(a);
 }
 
-// Adds the parts of rows that were split over stretches: workgroup (x, y) takes
-// the tile that stretch x ends in, if it began there too and goes on, and of its
-// rows every gridDim.y-th group of four, a wave a row.
+// Joins what the stretches left to be joined: workgroups (x, y) with x below `many`
+// stretch x of this kernel, the others those of the few-rows kernel.
 template <int D, bool kFp8>
-__global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, Parts parts, Cut cut,
-                                                         FastDiv by_heads, int slots) {
+__global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts parts, int many,
+                                                         int cut_heads, FastDiv by_heads,
+                                                         const long long* stretch_of,
+                                                         Parts few_parts, int few_tracks,
+                                                         FastDiv by_group) {
   using T = Tile<D, kFp8>;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.Hq / a.H, jobs = a.H * cut.head_blocks;
+  if ((int)blockIdx.x >= many) {
+    const int slot = blockIdx.x - many;
+    const Split p = few_parts.split[slot];
+    if (p.n == 0) return;
+    const int G = a.Hq / a.H, all_rows = 16 * few_tracks;
+    join_rows<D, 8, 8, 1>(
+        a, few_parts, all_rows, p.n,
+        [&](int r, int i) -> long long {
+          return (((long long)slot + i) * 2 + (i == 0)) * all_rows + r;
+        },
+        [&](int r) -> long long {
+          const int place = p.lo + r % 16;  // lo: the first of the sixteen rows
+          const int token = fast_div(place, by_group);
+          return place < p.rows
+                     ? p.row0 + (long long)token * a.Hq + (r / 16) * G + (place - token * G)
+                     : -1;
+        });
+    return;
+  }
   const int slot = blockIdx.x;
-  const long long stretch = parts.prefix[a.B];
-  const long long start = stretch * slot, end = start + stretch;
-  // The request that unit end - 1 lies in.
-  const int b = __builtin_amdgcn_readfirstlane(last_at_most(parts.prefix, a.B, end - 1));
-  const Chunk ch = chunk_of(a, b);
-  const Load w{ch.at, ch.live, cut.tokens, a.window};
-  if (!many_rows(a, ch)) return;
-  const long long first = parts.prefix[b], units = w.before(w.tiles());
-  if (end >= first + jobs * units) return;  // the line's end, or the request's
-  const int job = (int)floor_div(end - 1 - first, units);
-  const long long job0 = first + job * units;
-  const int k = w.tile_at(end - 1 - job0);
-  const long long tile0 = job0 + w.before(k), size = w.units(k);
-  if (tile0 < start || tile0 + size <= end) return;
-  const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
-  const int last = min((int)floor_div(tile0 + size - 1, stretch), slots - 1);
-  // (One stretch may hold all of the tile's keys: it wrote the rows itself.)
+  const Split p = parts.split[slot];
+  if (p.n == 0) return;
+  const long long stretch = *stretch_of, size = p.hi - p.lo + kFixed;
+  auto segment = [&](int i) {
+    return segment_of<T::kKeys>(p.lo, p.hi, max(stretch * i - p.before, 0ll),
+                                min(stretch * (i + 1) - p.before, size));
+  };
+  // (One stretch may hold all of the keys: it wrote the rows itself.)
   bool whole = false;
-  for (int x = slot; x <= last; ++x) {
-    const Segment s =
-        segment_of<T::kKeys>(w, k, max(stretch * x - tile0, 0ll), min(stretch * (x + 1) - tile0, size));
+  for (int i = 0; i < p.n; ++i) {
+    const Segment s = segment(i);
     whole = whole || (s.begin == s.first && s.end == s.last);
   }
   if (whole) return;
-  for (int r = blockIdx.y * 4 + wave; r < T::kRows; r += gridDim.y * 4) {
-    const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
-    const int token = k * cut.tokens + ti;
-    if (ti >= cut.tokens || token >= w.live || xb * cut.heads + hi >= G) continue;
-    const size_t row = (size_t)(ch.row0 + token) * a.Hq + (size_t)h * G + xb * cut.heads + hi;
-    auto part_of = [&](int i) -> long long {
-      const long long x = slot + i;
-      const Segment s = segment_of<T::kKeys>(w, k, max(stretch * x - tile0, 0ll),
-                                             min(stretch * (x + 1) - tile0, size));
-      return s.begin < s.end ? (x * 2 + (s.begin == s.first ? 1 : 0)) * T::kRows + r : -1;
-    };
-    join_row<D>(parts, last - slot + 1, part_of, a.out + row * D,
-                a.lse != nullptr ? a.lse + row : nullptr);
-  }
+  join_rows<D, 8, 4, 2>(
+      a, parts, T::kRows, p.n,
+      [&](int r, int i) -> long long {
+        const Segment s = segment(i);
+        return s.begin < s.end ? ((long long)(slot + i) * 2 + (s.begin == s.first)) * T::kRows + r
+                               : -1;
+      },
+      [&](int r) -> long long {
+        const int ti = fast_div(r, by_heads), hi = r - ti * cut_heads;
+        return ti < p.rows && hi < p.heads ? p.row0 + (long long)ti * a.Hq + hi : -1;
+      });
 }
 
 namespace {
 
 size_t part_rows(int D) { return (size_t)kCus * 2 * 32 * (D == 256 ? 4 : 8); }
 
+size_t many_floats(int D) { return 64 + split_floats(kCus) + part_rows(D) * (2 + D); }
+
+// Requests of few rows (single tokens, drafts) are read by the few-rows kernel, whose
+// waves go through keys of their own, where such requests are most: where the rows of
+// the batch, whose lengths the host does not know, are on average as few.
 template <int D, bool kFp8>
-hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
+hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
   using T = Tile<D, kFp8>;
   static std::atomic<unsigned long long> done{0};
   hipError_t e = once_per_device(done, [&] {
@@ -732,18 +757,33 @@ hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
                                hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   });
   if (e != hipSuccess) return e;
+  const long long rows = (long long)a.T * (a.Hq / a.H);
+  a.few = rows <= (long long)kFewRows * a.B ? kFewRows : 0;
+  const Parts few_parts = chunk_few_parts(a.part + many_floats(D));
+  // The stretch, then what was split, then the parts.
+  long long* stretch = (long long*)a.part;
   Parts parts;
-  parts.prefix = (long long*)a.part;
-  parts.ml = a.part + prefix_floats(a.B);
+  parts.split = (Split*)(a.part + 64);
+  parts.ml = a.part + 64 + split_floats(kCus);
   parts.o = parts.ml + part_rows(D) * 2;
   const Cut cut = cut_of(a.Hq / a.H, T::kRows);
   const FastDiv by_heads = make_fast_div(cut.heads);
-  chunk_attention_kernel<D, kFp8><<<kCus, T::kThreads, T::kLds, stream>>>(
-      a, parts, make_fast_div(a.block_size), cut, by_heads);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  chunk_join_kernel<D, kFp8><<<dim3(kCus, 32), 256, 0, stream>>>(
-      a, parts, cut, by_heads, kCus);
+  int many = 0, few = 0;
+  if (a.few > 0) {
+    few = chunk_few_groups(a);
+    e = launch_chunk_few(a, few_parts, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (a.few == 0 || rows > kFewRows) {
+    many = kCus;
+    chunk_attention_kernel<D, kFp8><<<many, T::kThreads, T::kLds, stream>>>(
+        a, parts, make_fast_div(a.block_size), cut, by_heads, stretch);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  chunk_join_kernel<D, kFp8><<<dim3(many + few, few > 0 ? 4 : 8), 512, 0, stream>>>(
+      a, parts, many, cut.heads, by_heads, stretch, few_parts, chunk_few_tracks(a.H),
+      make_fast_div(a.Hq / a.H));
   return hipGetLastError();
 }
 
@@ -751,21 +791,10 @@ hipError_t launch_cfg(const ChunkArgs& a, hipStream_t stream) {
 
 size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D) {
   if (T == 0 || B == 0) return 0;
-  return prefix_floats(B) + part_rows(D) * (2 + D) + chunk_few_scratch_floats(B, D);
+  return many_floats(D) + chunk_few_scratch_floats(D);
 }
 
-// Requests of few rows (single tokens, drafts) are read by the few-rows kernel, whose
-// waves go through keys of their own, where such requests are most: where the rows of
-// the batch, whose lengths the host does not know, are on average as few.
-hipError_t launch_chunk_attention(const ChunkArgs& all, hipStream_t stream) {
-  ChunkArgs a = all;
-  const long long rows = (long long)a.T * (a.Hq / a.H);
-  a.few = rows <= (long long)kFewRows * a.B ? kFewRows : 0;
-  if (a.few > 0) {
-    float* scratch = a.part + prefix_floats(a.B) + part_rows(a.D) * (2 + a.D);
-    const hipError_t e = launch_chunk_few(a, scratch, stream);
-    if (e != hipSuccess || rows <= kFewRows) return e;
-  }
+hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream) {
   const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
     case 64: return fp8 ? launch_cfg<64, true>(a, stream) : launch_cfg<64, false>(a, stream);

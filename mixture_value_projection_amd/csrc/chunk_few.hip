@@ -28,8 +28,6 @@ constexpr int kMaxGrid = 2 * kCus;
 // Tiles of a stretch at least: a row of so few is not cut.
 constexpr int kLeastTiles = 4;
 
-int tracks_per_group(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
-
 // Request b as this kernel sees it.
 template <int kTracks>
 struct Few {
@@ -84,8 +82,8 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
   Line line;
   const bool work = chunk_line<4>(
       a.B, slot, slots, kLeastTiles,
-      [&](int b) { return few_of<kTracks>(a, b, kTileKeys).units(a.H); }, s_line, parts.prefix,
-      &line);
+      [&](int b) { return few_of<kTracks>(a, b, kTileKeys).units(a.H); }, s_line, &line);
+  if (tid == 0) parts.split[slot].n = 0;
   clear_rows(a);
   if (!work) return;
 
@@ -109,6 +107,17 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
     const int h = heads * kTracks + tsub;
     const int len = f.c.at + f.c.live;
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
+    if (t0 == 0 && !all && tid == 0) {
+      Split p;
+      p.row0 = (long long)f.c.row0 * a.Hq + (long long)heads * kTracks * G;
+      p.before = 0;
+      p.n = (int)floor_div(line.stretch - nt + f.n - 1, line.stretch) + 1;
+      p.lo = qt * 16;
+      p.hi = 0;
+      p.rows = f.rows;
+      p.heads = 0;
+      parts.split[slot] = p;
+    }
 
     // The lane's row.
     const int place = qt * 16 + r16;
@@ -408,43 +417,12 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
   }
 }
 
-// Workgroup (x, y) joins the rows of the group that stretch x ends in, if it began
-// there too and goes on, a wave a row.
-template <int D, int kTracks>
-__global__ __launch_bounds__(256) void chunk_few_join_kernel(ChunkArgs a, Parts parts,
-                                                             FastDiv by_group, int slots,
-                                                             int tile_keys) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = blockIdx.x;
-  const long long stretch = parts.prefix[a.B];
-  const long long start = stretch * slot, end = start + stretch;
-  const int b = __builtin_amdgcn_readfirstlane(last_at_most(parts.prefix, a.B, end - 1));
-  const Few<kTracks> f = few_of<kTracks>(a, b, tile_keys);
-  const long long first = parts.prefix[b];
-  if (f.rows == 0 || end >= first + f.units(a.H)) return;  // the line's end, or the request's
-  const int group = (int)floor_div(end - 1 - first, f.n);
-  const long long group0 = first + (long long)group * f.n;
-  if (group0 < start || group0 + f.n <= end) return;
-  const int last = min((int)floor_div(group0 + f.n - 1, stretch), slots - 1);
-  const int heads = group / f.qtiles, qt = group - heads * f.qtiles;
-  const int G = a.Hq / a.H;
-  const int r = blockIdx.y * 4 + wave, tsub = r / 16, place = qt * 16 + r % 16;
-  if (tsub >= kTracks || place >= f.rows) return;
-  const int token = fast_div(place, by_group), h = heads * kTracks + tsub;
-  const size_t row = (size_t)(f.c.row0 + token) * a.Hq + h * G + (place - token * G);
-  auto part_of = [&](int i) -> long long {
-    return ((long long)((slot + i) * 2 + (i == 0 ? 1 : 0)) * kTracks + tsub) * 16 + r % 16;
-  };
-  join_row<D>(parts, last - slot + 1, part_of, a.out + row * D,
-              a.lse != nullptr ? a.lse + row : nullptr);
-}
-
 namespace {
 
 size_t few_part_rows() { return (size_t)kMaxGrid * 2 * 4 * 16; }
 
 template <int D, bool kFp8, int kTracks>
-hipError_t launch_cfg(const ChunkArgs& a, float* scratch, hipStream_t stream) {
+hipError_t launch_cfg(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
   using T = Tile<D, kFp8>;
   static std::atomic<unsigned long long> done{0};
   hipError_t e = once_per_device(done, [&] {
@@ -452,48 +430,58 @@ hipError_t launch_cfg(const ChunkArgs& a, float* scratch, hipStream_t stream) {
                                hipFuncAttributeMaxDynamicSharedMemorySize, 4 * T::kLds);
   });
   if (e != hipSuccess) return e;
-  Parts parts;
-  parts.prefix = (long long*)scratch;
-  parts.ml = scratch + prefix_floats(a.B);
-  parts.o = parts.ml + few_part_rows() * 2;
-  const int slots = T::kPerCu * kCus;
-  const FastDiv by_group = make_fast_div(a.Hq / a.H);
-  chunk_few_kernel<D, kFp8, kTracks><<<slots, 256, 4 * T::kLds, stream>>>(
-      a, parts, make_fast_div(a.block_size), by_group);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  chunk_few_join_kernel<D, kTracks><<<dim3(slots, 4 * kTracks), 256, 0, stream>>>(
-      a, parts, by_group, slots, T::kKeys * (4 / kTracks));
+  chunk_few_kernel<D, kFp8, kTracks><<<chunk_few_groups(a), 256, 4 * T::kLds, stream>>>(
+      a, parts, make_fast_div(a.block_size), make_fast_div(a.Hq / a.H));
   return hipGetLastError();
 }
 
 template <int D, bool kFp8>
-hipError_t launch_tracks(const ChunkArgs& a, float* scratch, hipStream_t stream) {
-  switch (tracks_per_group(a.H)) {
-    case 4: return launch_cfg<D, kFp8, 4>(a, scratch, stream);
-    case 2: return launch_cfg<D, kFp8, 2>(a, scratch, stream);
-    default: return launch_cfg<D, kFp8, 1>(a, scratch, stream);
+hipError_t launch_tracks(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
+  switch (chunk_few_tracks(a.H)) {
+    case 4: return launch_cfg<D, kFp8, 4>(a, parts, stream);
+    case 2: return launch_cfg<D, kFp8, 2>(a, parts, stream);
+    default: return launch_cfg<D, kFp8, 1>(a, parts, stream);
   }
+}
+
+template <int D>
+int groups_of(bool fp8) {
+  return kCus * (fp8 ? Tile<D, true>::kPerCu : Tile<D, false>::kPerCu);
 }
 
 }  // namespace
 
-size_t chunk_few_scratch_floats(int B, int D) {
-  return prefix_floats(B) + few_part_rows() * (2 + D);
+size_t chunk_few_scratch_floats(int D) {
+  return split_floats(kMaxGrid) + few_part_rows() * (2 + D);
 }
 
-hipError_t launch_chunk_few(const ChunkArgs& a, float* scratch, hipStream_t stream) {
+int chunk_few_groups(const ChunkArgs& a) {
+  const bool fp8 = a.dtype == kCacheFp8;
+  return a.D == 64 ? groups_of<64>(fp8) : a.D == 128 ? groups_of<128>(fp8) : groups_of<256>(fp8);
+}
+
+int chunk_few_tracks(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
+
+Parts chunk_few_parts(float* scratch) {
+  Parts parts;
+  parts.split = (Split*)scratch;
+  parts.ml = scratch + split_floats(kMaxGrid);
+  parts.o = parts.ml + few_part_rows() * 2;
+  return parts;
+}
+
+hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
   const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
     case 64:
-      return fp8 ? launch_tracks<64, true>(a, scratch, stream)
-                 : launch_tracks<64, false>(a, scratch, stream);
+      return fp8 ? launch_tracks<64, true>(a, parts, stream)
+                 : launch_tracks<64, false>(a, parts, stream);
     case 128:
-      return fp8 ? launch_tracks<128, true>(a, scratch, stream)
-                 : launch_tracks<128, false>(a, scratch, stream);
+      return fp8 ? launch_tracks<128, true>(a, parts, stream)
+                 : launch_tracks<128, false>(a, parts, stream);
     case 256:
-      return fp8 ? launch_tracks<256, true>(a, scratch, stream)
-                 : launch_tracks<256, false>(a, scratch, stream);
+      return fp8 ? launch_tracks<256, true>(a, parts, stream)
+                 : launch_tracks<256, false>(a, parts, stream);
     default: return hipErrorInvalidValue;
   }
 }
