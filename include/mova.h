@@ -639,6 +639,9 @@ int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32
                     int num_blocks, int32_t* seq_lens, int32_t* copy_src, int32_t* copy_dst,
                     hipStream_t stream);
 
+/* Bytes of workspace of mova_paged_free; (size_t)-1 outside the domain. */
+size_t mova_paged_free_workspace_bytes(int num_blocks);
+
 /*
  * Rows given back in whole or from some token on: row b keeps its first
  * keep_lens[b] tokens (0: the request ends; at or above cached_lens[b]: it stays
@@ -656,13 +659,16 @@ int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32
  *   seq_lens     int32 [B]  out: the tokens kept; not the address of
  *                cached_lens or keep_lens
  *
- * The block table itself stays: what lies behind a row's last block does not
- * matter.
+ *   workspace    mova_paged_free_workspace_bytes bytes, 256-byte aligned
+ *
+ * A row holds a block once.  The block table itself stays: what lies behind a
+ * row's last block does not matter.
  */
 int mova_paged_free(const int32_t* cached_lens, const int32_t* keep_lens, int B, int block_size,
                     int max_blocks, const int32_t* block_table, int32_t* free_blocks,
                     int free_capacity, const int32_t* free_count, int32_t* free_count_out,
-                    int32_t* shares, int num_blocks, int32_t* seq_lens, hipStream_t stream);
+                    int32_t* shares, int num_blocks, int32_t* seq_lens, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace of mova_paged_compact; (size_t)-1 outside the domain. */
 size_t mova_paged_compact_workspace_bytes(int num_blocks);

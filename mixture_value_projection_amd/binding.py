@@ -95,7 +95,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mova_paged_fork.argtypes = [vp, vp, vp, i, vp, i, i, i, vp, vp, i, vp, vp, vp, i, vp, vp,
                                     vp, vp]
     lib.mova_paged_free.restype = i
-    lib.mova_paged_free.argtypes = [vp, vp, i, i, i, vp, vp, i, vp, vp, vp, i, vp, vp]
+    lib.mova_paged_free.argtypes = [vp, vp, i, i, i, vp, vp, i, vp, vp, vp, i, vp, vp, sz, vp]
+    lib.mova_paged_free_workspace_bytes.restype = sz
+    lib.mova_paged_free_workspace_bytes.argtypes = [i]
     lib.mova_paged_compact_workspace_bytes.restype = sz
     lib.mova_paged_compact_workspace_bytes.argtypes = [i]
     lib.mova_paged_compact.restype = i
@@ -946,10 +948,16 @@ def paged_fork(parents: torch.Tensor, children: torch.Tensor, block_size: int,
     return PagedFork(seq_lens, copy_src, copy_dst, free_count_out)
 
 
+@functools.lru_cache(maxsize=64)
+def _free_bytes(num_blocks: int) -> int:
+    return load_library().mova_paged_free_workspace_bytes(num_blocks)
+
+
 def paged_free(cached_lens: torch.Tensor, keep_lens: torch.Tensor, block_size: int,
                block_table: torch.Tensor, free_blocks: torch.Tensor, free_count: torch.Tensor,
                shares: torch.Tensor, seq_lens: Optional[torch.Tensor] = None,
-               free_count_out: Optional[torch.Tensor] = None) -> PagedFree:
+               free_count_out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> PagedFree:
     """mova_paged_free: each row keeps its first ``keep_lens`` tokens (0 ends
     the request) and lets go of the blocks behind them; a block's last holder
     puts it on the free stack.  ``free_blocks`` and ``shares`` are updated in
@@ -961,9 +969,11 @@ def paged_free(cached_lens: torch.Tensor, keep_lens: torch.Tensor, block_size: i
     _check(keep_lens, "keep_lens", torch.int32, (B,), dev)
     seq_lens = _given(seq_lens, "seq_lens", (B,), cached_lens)
     free_count_out = _given(free_count_out, "free_count_out", (1,), free_count)
+    workspace = _scratch(workspace, _free_bytes(nb), "mova_paged_free", dev)
     _launch(lib.mova_paged_free, "mova_paged_free", dev, _ptr(cached_lens), _ptr(keep_lens), B,
             block_size, mb, _ptr(block_table), _ptr(free_blocks), cap, _ptr(free_count),
-            _ptr(free_count_out), _ptr(shares), nb, _ptr(seq_lens))
+            _ptr(free_count_out), _ptr(shares), nb, _ptr(seq_lens), _ptr(workspace),
+            workspace.numel())
     return PagedFree(seq_lens, free_count_out)
 
 

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -171,7 +172,17 @@ struct FreeArgs {
   int32_t* shares;  // [num_blocks]
   int num_blocks;
   int32_t* seq_lens;  // [B]
+  uint32_t* scratch;  // free_scratch_words
 };
+// The pool in at most kFreeRuns runs of whole 512 blocks, each a workgroup's; scratch:
+// what each run gives, then how often each block is let go, 16 bits a block.
+constexpr int kFreeRuns = 256;
+inline int free_run(int num_blocks) {
+  return std::max((num_blocks + kFreeRuns * 512 - 1) / (kFreeRuns * 512), 2) * 512;
+}
+inline size_t free_scratch_words(int num_blocks) {
+  return kFreeRuns + ((size_t)num_blocks + 1) / 2;
+}
 hipError_t launch_paged_free(const FreeArgs& a, hipStream_t stream);
 
 struct CompactArgs {

@@ -88,6 +88,7 @@ int check_upkeep(int B, int max_blocks, int block_size, int num_blocks, int free
   return num_blocks > kMaxUpkeepBlocks ? MOVA_ERR_UNSUPPORTED : MOVA_OK;
 }
 
+size_t free_bytes(int num_blocks) { return align256(4 * free_scratch_words(num_blocks)); }
 size_t compact_bytes(int num_blocks) { return align256(4 * compact_scratch_words(num_blocks)); }
 
 size_t select_bytes(int B, int n_kv_heads, int max_blocks) {
@@ -332,11 +333,17 @@ int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32
   return launch_paged_fork(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
 }
 
+size_t mova_paged_free_workspace_bytes(int num_blocks) {
+  if (num_blocks < 0 || num_blocks > kMaxUpkeepBlocks) return (size_t)-1;
+  return free_bytes(num_blocks);
+}
+
 int mova_paged_free(const int32_t* cached_lens, const int32_t* keep_lens, int B, int block_size,
                     int max_blocks, const int32_t* block_table, int32_t* free_blocks,
                     int free_capacity, const int32_t* free_count, int32_t* free_count_out,
-                    int32_t* shares, int num_blocks, int32_t* seq_lens, hipStream_t stream) {
-  const int rc = check_upkeep(B, max_blocks, block_size, num_blocks, free_capacity);
+                    int32_t* shares, int num_blocks, int32_t* seq_lens, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_upkeep(B, max_blocks, block_size, num_blocks, free_capacity);
   if (rc != MOVA_OK) return rc;
   if ((B > 0 && (cached_lens == nullptr || keep_lens == nullptr || block_table == nullptr ||
                  seq_lens == nullptr)) ||
@@ -350,8 +357,11 @@ int mova_paged_free(const int32_t* cached_lens, const int32_t* keep_lens, int B,
   if (free_count == free_count_out ||
       (B > 0 && (cached_lens == seq_lens || keep_lens == seq_lens)))
     return MOVA_ERR_INVALID_ARG;
+  rc = check_workspace(workspace, workspace_bytes, free_bytes(num_blocks));
+  if (rc != MOVA_OK) return rc;
   const FreeArgs a{cached_lens, keep_lens, B, block_size, max_blocks, block_table, free_blocks,
-                   free_capacity, free_count, free_count_out, shares, num_blocks, seq_lens};
+                   free_capacity, free_count, free_count_out, shares, num_blocks, seq_lens,
+                   (uint32_t*)workspace};
   return launch_paged_free(a, stream) == hipSuccess ? MOVA_OK : MOVA_ERR_HIP;
 }
 

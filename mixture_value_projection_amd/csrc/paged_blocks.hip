@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kForkThreads = 256;
 constexpr int kFreeThreads = 1024;
+constexpr int kFreeAtOnce = 8;
+constexpr int kFreeRows = kMaxRequests / kFreeThreads;  // of a thread
+
 constexpr int kRankWords = kRankBlocks / 32;
 
 __device__ __forceinline__ bool in_pool(int page, int num_blocks) {
@@ -36,9 +39,16 @@ __device__ __forceinline__ int clamp_len(int n, int most) { return min(max(n, 0)
 // ---- copy ---------------------------------------------------------------------
 
 // Workgroup items: 16 KB of a block's keys, values and bounds, seen as one run of
-// pieces; a thread has four pieces in flight.
+// pieces; a thread has four pieces in flight, and every item has a workgroup of its
+// own, as far as a grid goes (770 MB read and written in blocks of 32 KB: 2048
+// workgroups with items in turn 180 us, this 150).  Pools larger than the last cache
+// pass the caches by: that takes 132 us (5.8 TB/s) for those 770 MB, but for 60 MB of
+// a pool of 128 MB 14 us, and 11 through the caches.
+constexpr size_t kLastCache = (size_t)256 << 20;
+constexpr int kCopyGrid = 65536;
 constexpr int kCopyAtOnce = 4, kCopyPieces = 256 * kCopyAtOnce;
 
+template <bool kPast>
 __global__ __launch_bounds__(256) void paged_copy_kernel(CopyArgs a) {
   const int count = a.count == nullptr ? a.n : min(max(*a.count, 0), a.n);
   const int pieces = a.pieces[0] + a.pieces[1] + a.pieces[2];
@@ -68,19 +78,29 @@ __global__ __launch_bounds__(256) void paged_copy_kernel(CopyArgs a) {
           width = a.pieces[2];
         }
       }
-      x[i] = pool[(size_t)src * width + p];
+      const u32x4* from = pool + (size_t)src * width + p;
+      x[i] = kPast ? __builtin_nontemporal_load(from) : *from;
       to[i] = pool + (size_t)dst * width + p;
     }
 #pragma unroll
     for (int i = 0; i < kCopyAtOnce; ++i)
-      if (to[i] != nullptr) *to[i] = x[i];
+      if (to[i] != nullptr) {
+        if constexpr (kPast)
+          __builtin_nontemporal_store(x[i], to[i]);
+        else
+          *to[i] = x[i];
+      }
   }
 }
 
 hipError_t launch_paged_copy(const CopyArgs& a, hipStream_t stream) {
   const long long parts = ceil_div(a.pieces[0] + a.pieces[1] + a.pieces[2], kCopyPieces);
-  const int grid = (int)std::min<long long>(a.n * parts, 2048);
-  paged_copy_kernel<<<grid, 256, 0, stream>>>(a);
+  const int grid = (int)std::min<long long>(a.n * parts, kCopyGrid);
+  const size_t bytes = (size_t)a.num_blocks * (a.pieces[0] + a.pieces[1] + a.pieces[2]) * 16;
+  if (bytes > kLastCache)
+    paged_copy_kernel<true><<<grid, 256, 0, stream>>>(a);
+  else
+    paged_copy_kernel<false><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -189,82 +209,161 @@ hipError_t launch_paged_fork(const ForkArgs& a, hipStream_t stream) {
 
 // ---- free ---------------------------------------------------------------------
 
-// One workgroup: which rows are cut where, from the counts as they came; then
-// the counts go down, and whoever finds 0 sets the block's bit; then the bits go
-// on the stack.
-__global__ __launch_bounds__(kFreeThreads) void paged_free_kernel(FreeArgs a, FastDiv by_block) {
+// The pool lies in runs of free_run() blocks, a workgroup each.  The first kernel
+// finds out which rows are cut where, every workgroup for itself and from the counts
+// as they came; it goes through all entries that are given back and counts, in LDS,
+// those of its blocks.  What it leaves is how often each block is let go, and how many
+// of a run's blocks are let go more often than they have holders beyond the first.
+// With those numbers the second one brings the counts down and puts the blocks on
+// the stack, highest first.
+//
+// A workgroup alone waits for memory at each turn: the 28,689 entries of 150 rows of
+// a pool of 15,000 blocks took one 80 us with atomics on the counts and 32 with counts
+// in LDS; these two take 17 and 4.  The 1051 of a step of 64 rows took it 8; 6 and 4.
+__global__ __launch_bounds__(kFreeThreads) void free_count_kernel(FreeArgs a, FastDiv by_block,
+                                                                  int run) {
   extern __shared__ __attribute__((aligned(16))) char free_lds[];
-  long long* s_first = (long long*)free_lds;    // [B] entries given back before the row
-  int* s_from = (int*)(s_first + a.B);          // [B] first of its entries that goes
-  uint32_t* s_bits = (uint32_t*)(s_from + a.B);  // a bit a block
-  __shared__ long long tmp[2][kFreeThreads / 64];
+  // Rows that give back: entries given back before the row, and its first one's
+  // place in the table less that.
+  long long* s_first = (long long*)free_lds;     // [B]
+  long long* s_base = s_first + a.B;             // [B]
+  uint32_t* s_gone = (uint32_t*)(s_base + a.B);  // [run / 2] two blocks' counts a word
+  __shared__ long long tmp[3][kFreeThreads / 64];
   const int tid = threadIdx.x, bs = a.block_size;
   const int most = a.max_blocks * bs;
-  const int words = ceil_div(a.num_blocks, 32);
-  const int count = min(max(*a.free_count, 0), a.free_capacity);
+  const int lo = blockIdx.x * run, here = min(run, a.num_blocks - lo);
   auto blocks = [&](int n) { return fast_div(n + bs - 1, by_block); };
-  for (int w = tid; w < words; w += kFreeThreads) s_bits[w] = 0;
+  auto kept = [&](int b, int n) {
+    const int m = clamp_len(a.keep[b], n), full = fast_div(m, by_block);
+    if (m == n || m == full * bs) return m;
+    const int page = a.table[(size_t)b * a.max_blocks + full];
+    return in_pool(page, a.num_blocks) && a.shares[page] > 0 ? n : m;
+  };
+  for (int w = tid; w < run / 2; w += kFreeThreads) s_gone[w] = 0;
 
   const int per = ceil_div(a.B, kFreeThreads);
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  long long gone = 0, all_gone;
-  for (int b = b0; b < b1; ++b) {
-    const int n = clamp_len(a.cached[b], most);
-    int m = clamp_len(a.keep[b], n);
-    const int full = fast_div(m, by_block);
-    if (m < n && m != full * bs) {
-      const int page = a.table[(size_t)b * a.max_blocks + full];
-      if (in_pool(page, a.num_blocks) && a.shares[page] > 0) m = n;
-    }
-    a.seq_lens[b] = m;
-    s_from[b] = blocks(m);
-    s_first[b] = blocks(n) - blocks(m);  // for now
-    gone += blocks(n) - blocks(m);
+  long long gone = 0, all_gone, giving = 0, rows;
+  int going[kFreeRows];
+  long long base[kFreeRows];
+#pragma unroll
+  for (int i = 0; i < kFreeRows; ++i) {
+    const int b = tid * per + i;
+    going[i] = 0;
+    if (i >= per || b >= a.B) continue;
+    const int n = clamp_len(a.cached[b], most), m = kept(b, n);
+    if (blockIdx.x == 0) a.seq_lens[b] = m;
+    going[i] = blocks(n) - blocks(m);
+    base[i] = (long long)b * a.max_blocks + blocks(m);
+    gone += going[i];
+    giving += going[i] > 0;
   }
   long long first = block_exclusive_scan<kFreeThreads / 64>(gone, tmp[0], &all_gone);
-  for (int b = b0; b < b1; ++b) {
-    const long long mine = s_first[b];
-    s_first[b] = first;
-    first += mine;
+  long long row = block_exclusive_scan<kFreeThreads / 64>(giving, tmp[1], &rows);
+#pragma unroll
+  for (int i = 0; i < kFreeRows; ++i) {
+    if (going[i] == 0) continue;
+    s_first[row] = first;
+    s_base[row++] = base[i] - first;
+    first += going[i];
   }
   __syncthreads();
-
-  for (long long e = tid; e < all_gone; e += kFreeThreads) {
-    const int b = last_at_most(s_first, a.B, e);
-    const int page = a.table[(size_t)b * a.max_blocks + s_from[b] + (e - s_first[b])];
-    if (!in_pool(page, a.num_blocks)) continue;
-    if (atomicSub(&a.shares[page], 1) <= 0) atomicOr(&s_bits[page >> 5], 1u << (page & 31));
-  }
-  __syncthreads();
-
-  // Descending: thread 0 has the highest words.
-  const int run = ceil_div(words, kFreeThreads);
-  const int w1 = words - min(tid * run, words), w0 = max(w1 - run, 0);
-  long long mine = 0, all;
-  for (int w = w0; w < w1; ++w) mine += __popc(s_bits[w]);
-  long long at = count + block_exclusive_scan<kFreeThreads / 64>(mine, tmp[1], &all);
-  for (int w = w1 - 1; w >= w0; --w) {
-    for (uint32_t bits = s_bits[w]; bits != 0; ++at) {
-      const int bit = 31 - __clz((int)bits);
-      bits &= ~(1u << bit);
-      a.shares[w * 32 + bit] = 0;
-      if (at < a.free_capacity) a.free_blocks[at] = w * 32 + bit;
+  // Eight entries of a thread: their pages are asked for together.
+  for (long long e0 = (long long)tid * kFreeAtOnce; e0 < all_gone;
+       e0 += kFreeThreads * kFreeAtOnce) {
+    int r = last_at_most(s_first, (int)rows, e0);
+    long long from = s_base[r], next = r + 1 < rows ? s_first[r + 1] : all_gone;
+    int page[kFreeAtOnce];
+#pragma unroll
+    for (int i = 0; i < kFreeAtOnce; ++i) {
+      const long long e = min(e0 + i, all_gone - 1);
+      if (e == next) {
+        from = s_base[++r];
+        next = r + 1 < rows ? s_first[r + 1] : all_gone;
+      }
+      page[i] = a.table[from + e];
+    }
+#pragma unroll
+    for (int i = 0; i < kFreeAtOnce; ++i) {
+      const uint32_t p = (uint32_t)(page[i] - lo);
+      if (e0 + i < all_gone && page[i] >= lo && p < (uint32_t)here)
+        atomicAdd(&s_gone[p >> 1], 1u << 16 * (p & 1));
     }
   }
-  if (tid == 0) *a.free_count_out = (int)min(count + all, (long long)a.free_capacity);
+  __syncthreads();
+  int last = 0;
+  for (int w = tid; w < ceil_div(here, 2); w += kFreeThreads) {
+    const uint32_t n = s_gone[w];
+    a.scratch[kFreeRuns + lo / 2 + w] = n;
+    if (n == 0) continue;
+    last += (int)(n & 0xffffu) > max(a.shares[lo + 2 * w], 0);
+    last += (int)(n >> 16) > max(a.shares[lo + min(2 * w + 1, here - 1)], 0);
+  }
+  long long all;
+  block_exclusive_scan<kFreeThreads / 64>(last, tmp[2], &all);
+  if (tid == 0) a.scratch[blockIdx.x] = (uint32_t)all;
+}
+
+__global__ __launch_bounds__(256) void free_apply_kernel(FreeArgs a, int run) {
+  static_assert(kFreeRuns == 256, "a thread a run");
+  __shared__ long long tmp[2][4];
+  __shared__ int s_mine[4];
+  __shared__ uint32_t s_last[kMaxUpkeepBlocks / kFreeRuns / 2];  // a word's blocks that go
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lo = blockIdx.x * run, here = min(run, a.num_blocks - lo);
+  const int count = min(max(*a.free_count, 0), a.free_capacity);
+  const int at = tid < (int)gridDim.x ? (int)a.scratch[tid] : 0;
+  long long above, all;
+  block_exclusive_scan<4>(tid > (int)blockIdx.x ? at : 0, tmp[0], &above);
+  block_exclusive_scan<4>(at, tmp[1], &all);
+  if (blockIdx.x == 0 && tid == 0)
+    *a.free_count_out = (int)min(count + all, (long long)a.free_capacity);
+
+  // A wave's words, highest first, a lane a word.
+  const int words = ceil_div(here, 2), mine = run / 8;
+  const int top = words - wave * mine, bottom = max(top - mine, 0);
+  int pushed = 0;
+  for (int w0 = top; w0 > bottom; w0 -= 64) {
+    const int w = w0 - 1 - lane;
+    uint32_t last = 0;
+    if (w >= bottom) {
+      const uint32_t n = a.scratch[kFreeRuns + lo / 2 + w];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int times = (int)(n >> 16 * i & 0xffffu);
+        if (times == 0) continue;
+        const int held = max(a.shares[lo + 2 * w + i], 0);
+        a.shares[lo + 2 * w + i] = max(held - times, 0);
+        last |= (uint32_t)(times > held) << i;
+      }
+      s_last[w] = last;
+    }
+    pushed += __popcll(__ballot(last & 1)) + __popcll(__ballot(last & 2));
+  }
+  if (lane == 0) s_mine[wave] = pushed;
+  __syncthreads();
+  long long to = count + above;
+  for (int w = 0; w < wave; ++w) to += s_mine[w];
+  for (int w0 = top; w0 > bottom && pushed > 0; w0 -= 64) {
+    const int w = w0 - 1 - lane;
+    const uint32_t last = w >= bottom ? s_last[w] : 0;
+    const uint64_t odd = __ballot(last & 2), even = __ballot(last & 1);
+    const uint64_t before = (1ull << lane) - 1;
+    const long long mark = to + __popcll(odd & before) + __popcll(even & before);
+    const long long after = mark + (last >> 1);
+    if ((last & 2) && mark < a.free_capacity) a.free_blocks[mark] = lo + 2 * w + 1;
+    if ((last & 1) && after < a.free_capacity) a.free_blocks[after] = lo + 2 * w;
+    to += __popcll(odd) + __popcll(even);
+  }
 }
 
 hipError_t launch_paged_free(const FreeArgs& a, hipStream_t stream) {
   if (a.B > kMaxRequests || a.num_blocks > kMaxUpkeepBlocks) return hipErrorInvalidValue;
-  static std::atomic<unsigned long long> done{0};
-  const size_t lds = (size_t)a.B * 12 + (size_t)ceil_div(a.num_blocks, 32) * 4;
-  hipError_t e = once_per_device(done, [&] {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(paged_free_kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize,
-                               kMaxRequests * 12 + kMaxUpkeepBlocks / 8);
-  });
+  const int run = free_run(a.num_blocks), runs = std::max(ceil_div(a.num_blocks, run), 1);
+  free_count_kernel<<<runs, kFreeThreads, (size_t)a.B * 16 + run * 2, stream>>>(
+      a, make_fast_div(a.block_size), run);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  paged_free_kernel<<<1, kFreeThreads, lds, stream>>>(a, make_fast_div(a.block_size));
+  free_apply_kernel<<<runs, 256, 0, stream>>>(a, run);
   return hipGetLastError();
 }
 

@@ -83,7 +83,8 @@ def test_fork_rejects(lib, kw, rc):
 
 
 FREE = dict(cached=FAKE, keep=FAKE, B=4, bs=16, mb=10, table=FAKE, free=FAKE, cap=40, count=FAKE,
-            count_out=FAKE + 4, shares=FAKE, nb=40, seq=FAKE + 64, stream=None)
+            count_out=FAKE + 4, shares=FAKE, nb=40, seq=FAKE + 64, ws=FAKE, wsb=1 << 20,
+            stream=None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -96,6 +97,7 @@ FREE = dict(cached=FAKE, keep=FAKE, B=4, bs=16, mb=10, table=FAKE, free=FAKE, ca
                                          "shares", "seq")],
     (dict(count_out=FAKE), INVALID), (dict(seq=FAKE), INVALID),
     (dict(keep=FAKE + 64), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(wsb=8), WORKSPACE), (dict(ws=FAKE + 16), INVALID),
 ])
 def test_free_rejects(lib, kw, rc):
     assert call(lib.mova_paged_free, FREE, kw) == rc
@@ -121,6 +123,14 @@ COMPACT = dict(cached=FAKE, B=4, bs=16, mb=10, table=FAKE, table_out=FAKE, free=
 ])
 def test_compact_rejects(lib, kw, rc):
     assert call(lib.mova_paged_compact, COMPACT, kw) == rc
+
+
+def test_free_workspace(lib):
+    size = lib.mova_paged_free_workspace_bytes
+    assert size(-1) == BAD and size((1 << 20) + 1) == BAD
+    for nb in (0, 1, 1024, 1025, 262144, 262145, 1 << 20):
+        # A count of each of 256 runs, and 16 bits a block in whole words.
+        assert size(nb) >= 4 * 256 + 4 * ((nb + 1) // 2) and size(nb) % 256 == 0
 
 
 def test_compact_workspace(lib):
