@@ -44,6 +44,13 @@ namespace {
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
+// The lane's number, formed anew: nothing that follows from it is held from before.
+__device__ __forceinline__ int lane_anew() {
+  int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // Request b's rows of the packed tokens and positions in the cache.
 struct Chunk {
   int row0, rows;  // packed rows [row0, row0 + rows)
@@ -153,7 +160,7 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
                                            const bf16_t* q, int lo, int hi, const Sink<D>& sink) {
   constexpr int kPer = D / 64;
   constexpr float kDown = 0x1p-32f;
-  const int lane = threadIdx.x & 63;
+  const int lane = lane_anew();
   const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
   const int32_t* table = a.table + (size_t)b * a.max_blocks;
   // Element of the pools where the head's row of position p begins, or -1.
@@ -192,9 +199,10 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
     l += w;
 #pragma unroll 1
     for (uint64_t there = __ballot(at >= 0); there != 0; there &= there - 1) {
-      const int i = __ffsll((unsigned long long)there) - 1;
-      const float wi = __shfl(w, i);
-      const size_t from = (size_t)__shfl(at, i) + lane * kPer;
+      const int i = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)there) - 1);
+      const float wi = __builtin_bit_cast(float, read_lane(__builtin_bit_cast(int, w), i));
+      const uint32_t low = (uint32_t)read_lane((int)at, i), high = (uint32_t)read_lane((int)(at >> 32), i);
+      const size_t from = ((size_t)high << 32 | low) + lane * kPer;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const float v = load1<kFp8>(a.v_cache, from + j);
@@ -214,14 +222,14 @@ __device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block,
 }
 
 // Zeros for the rows that have no token in the cache; the whole grid takes part.
-__device__ __forceinline__ void clear_rows(const ChunkArgs& a) {
+__device__ __forceinline__ void clear_rows(const ChunkArgs& a, int tid) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Chunk c = chunk_of(a, b);
     const size_t from = (size_t)(c.row0 + c.live) * a.Hq, to = (size_t)(c.row0 + c.rows) * a.Hq;
-    for (size_t i = from * a.D + threadIdx.x * 8; i < to * a.D; i += blockDim.x * 8)
+    for (size_t i = from * a.D + tid * 8; i < to * a.D; i += blockDim.x * 8)
       store16(a.out + i, u32x4{0u, 0u, 0u, 0u});
     if (a.lse != nullptr)
-      for (size_t i = from + threadIdx.x; i < to; i += blockDim.x) a.lse[i] = -__builtin_huge_valf();
+      for (size_t i = from + tid; i < to; i += blockDim.x) a.lse[i] = -__builtin_huge_valf();
   }
 }
 

@@ -21,9 +21,13 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
 template <int D, bool kFp8>
 struct Tile {
-  static constexpr int kWaves = D == 256 ? 4 : 8;
-  static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kRows = 32 * kWaves;            // rows (token and query head) of a workgroup
+  static constexpr int kWaves = 8, kThreads = 64 * kWaves;
+  // Waves that share 32 rows and have a part of the channels each: of 256, the sums
+  // and what else a wave holds would not fit its registers.  (The products with the
+  // keys are then formed twice.)
+  static constexpr int kSplit = D == 256 ? 2 : 1;
+  static constexpr int kRowWaves = kWaves / kSplit;
+  static constexpr int kRows = 32 * kRowWaves;         // rows (token and query head) of a workgroup
   static constexpr int kKeys = D == 256 ? 32 : 64;     // of a tile
   static constexpr int kParts = kKeys / 32;
   static constexpr bool kQueriesInLds = D == 256;
@@ -135,6 +139,12 @@ __device__ __forceinline__ float max_of_halves(float x) {
   return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 
+__device__ __forceinline__ float sum_of_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
 // 16 e4m3 elements as bf16 or fp16 (both exact).
 template <bool kHalf>
 __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
@@ -161,14 +171,15 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
     ChunkArgs a, Parts parts, FastDiv by_block, Cut cut, FastDiv by_heads, long long* stretch_of) {
   using T = Tile<D, kFp8>;
   constexpr int kSteps = D / 16;    // products along the channels
-  constexpr int kBlocks = D / 32;   // 32-channel blocks of the output
+  constexpr int kBlocks = D / 32 / T::kSplit;  // 32-channel blocks of the output
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ Shared s_line;
+  __shared__ uint32_t s_again[T::kWaves];
 
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r32 = lane & 31, half = lane >> 5;
+  // The wave's rows, and its part of the channels.
+  const int row_wave = wave % T::kRowWaves, part_wave = wave / T::kRowWaves;
   const int G = a.Hq / a.H;
   const int jobs = a.H * cut.head_blocks;  // of a row tile
   // Neighbouring stretches on one XCD, whose workgroups then read the same keys.
@@ -184,10 +195,6 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
   };
   Line line;
   const bool work = chunk_line<T::kWaves>(a.B, slot, slots, kLeastStretch, cost, s_line, &line);
-
-  // This thread's pieces of a tile.
-  const int my_key = tid / T::kPieces, my_piece = tid % T::kPieces;
-  const bool my_load = T::kTotal >= T::kThreads || tid < T::kTotal;
 
   if (tid == 0) parts.split[slot].n = 0;
   if (tid == 0 && slot == 0) *stretch_of = line.stretch;
@@ -219,13 +226,15 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const long long x1 = min(w.units(k), x0 + left);
       left -= x1 - x0;
       const Segment seg = segment_of<T::kKeys>(w.lo(k), w.hi(k), x0, x1);
-      if (x0 == 0 && x1 < w.units(k) && tid == 0) {
+      if (x0 == 0 && x1 < w.units(k) && wave == 0 && lane_anew() == 0) {
         const int xb = job % cut.head_blocks;
         Split p;
         p.row0 = (long long)(ch.row0 + k * cut.tokens) * a.Hq +
                  (long long)(job / cut.head_blocks) * G + xb * cut.heads;
-        p.before = line.stretch - x1;
-        p.n = (int)floor_div(p.before + w.units(k) - 1, line.stretch) + 1;
+        long long stretch = line.stretch;
+        asm volatile("" : "+s"(stretch));
+        p.before = stretch - x1;
+        p.n = (int)floor_div(p.before + w.units(k) - 1, stretch) + 1;
         p.lo = w.lo(k);
         p.hi = w.hi(k);
         p.rows = min(cut.tokens, w.live - k * cut.tokens);
@@ -239,8 +248,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const int32_t* table = a.table + (size_t)b * a.max_blocks;
 
       // The lane's row: its token and query head.
-      int r = wave * 32 + r32;
-      loaded(r);  // no registers between tiles for what follows from it
+      const int lane = lane_anew();
+      const int r32 = lane & 31, half = lane >> 5, r = row_wave * 32 + r32;
+      // This thread's pieces of a key tile.
+      const int my_key = (wave * 64 + lane) / T::kPieces, my_piece = lane % T::kPieces;
+      const bool my_load = T::kTotal >= T::kThreads || wave * 64 + lane < T::kTotal;
       const int ti = fast_div(r, by_heads), hi = r - ti * cut.heads;
       const int token = k * cut.tokens + ti;
       const bool live = ti < cut.tokens && token < w.live && xb * cut.heads + hi < G;
@@ -257,10 +269,10 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const int lower = live && a.window > 0 ? max(0, limit + 1 - a.window) : 0;
       auto imax = [](int x, int y) { return max(x, y); };
       auto imin = [](int x, int y) { return min(x, y); };
-      const int most_limit = wave_reduce(live ? limit : -1, imax);
-      const int least_limit = wave_reduce(limit, imin);
-      const int least_lower = wave_reduce(live ? lower : 0x3fffffff, imin);
-      const int most_lower = wave_reduce(lower, imax);
+      const int most_limit = __builtin_amdgcn_readfirstlane(wave_reduce(live ? limit : -1, imax));
+      const int least_limit = __builtin_amdgcn_readfirstlane(wave_reduce(limit, imin));
+      const int least_lower = __builtin_amdgcn_readfirstlane(wave_reduce(live ? lower : 0x3fffffff, imin));
+      const int most_lower = __builtin_amdgcn_readfirstlane(wave_reduce(lower, imax));
 
       // Staging, through registers: in tile j's turn the keys of tile j + 2 and the
       // values of tile j + 1 go into LDS and those of the tiles behind them are asked
@@ -281,9 +293,10 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
 
       // Queries; a negative scale goes into their signs.
       const float ks = a.k_scale != nullptr ? a.k_scale[h] : 1.f;
-      const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
       const float signed_qs = a.scale * ks * kLog2e;
-      const float qs = fmaxf(fabsf(signed_qs), 0x1p-126f);  // logits in powers of two
+      const float qs = __builtin_bit_cast(
+          float, __builtin_amdgcn_readfirstlane(
+                     __builtin_bit_cast(int, fmaxf(fabsf(signed_qs), 0x1p-126f))));  // logits in powers of two
       const uint32_t flip = signed_qs < 0.f ? 0x80008000u : 0u;
       Frag16 qf[T::kQueriesInLds ? 1 : kSteps];
 #pragma unroll
@@ -293,10 +306,12 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         if (live) x.u = load16(q_rows + (uint32_t)(row_of(r) * D + 16 * u + 8 * half));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x.u[i] ^= flip;
-        if constexpr (T::kQueriesInLds)
+        if constexpr (T::kQueriesInLds) {
+          if (part_wave > 0) continue;
           store16(lds + r * T::kKeyRow + (2 * u + half) * 16, x.u);
-        else
+        } else {
           qf[u] = x;
+        }
       }
 
       auto ring = [&](int j) {
@@ -404,7 +419,6 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
 
       // (The reads of the last segment's slots and stages are behind a barrier.)
       if (wave < 5) put_slots(seg.begin + wave, page0);
-      if (T::kWaves == 4 && wave == 0) put_slots(seg.begin + 4, page_of(seg.begin + 4));
       __syncthreads();
       int slot_here = ring(seg.begin)[lane & (T::kKeys - 1)];
       {
@@ -535,7 +549,8 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
               const int key = 16 * y + 8 * z + 4 * half + r16 / 4;
-              char* from = st + T::kValuesAt + key * T::kValueRow + 64 * c + 32 * g + 8 * (r16 & 3);
+              char* from = st + T::kValuesAt + key * T::kValueRow + 64 * (kBlocks * part_wave + c) +
+                           32 * g + 8 * (r16 & 3);
               vf[n].q[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                   (__attribute__((address_space(3))) s16x4*)(uintptr_t)(lds_void*)from);
             }
@@ -598,8 +613,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         if (j + 1 < seg.end) turn(j + 1, std::integral_constant<int, 1>{});
       }
 
-      // The halves of a row hold its sum in parts.
-      l += __shfl_xor(l, 32);
+      // The halves of a row hold its sum in parts.  (Places are formed anew: none are
+      // held through the tiles for this.)
+      const int lane2 = lane_anew();
+      const int r32e = lane2 & 31, halfe = lane2 >> 5, re = row_wave * 32 + r32e;
+      l = sum_of_halves(l);
       float largest = 0.f;  // NaN counts as the largest
 #pragma unroll
       for (int c = 0; c < kBlocks; ++c)
@@ -609,7 +627,14 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
       const bool odd = live && l > 0.f && l < __builtin_huge_valf() &&
                        !(largest < __builtin_huge_valf());
       const uint64_t odd_lanes = __ballot(odd);
-      const uint32_t again = (uint32_t)odd_lanes | (uint32_t)(odd_lanes >> 32);
+      uint32_t again = (uint32_t)odd_lanes | (uint32_t)(odd_lanes >> 32);
+      if constexpr (T::kSplit > 1) {
+        // Of all channels.
+        if (lane2 == 0) s_again[wave] = again;
+        __syncthreads();
+        for (int x = 0; x < T::kSplit; ++x) again |= s_again[x * T::kRowWaves + row_wave];
+        again = (uint32_t)__builtin_amdgcn_readfirstlane((int)again);
+      }
       if (__any(l == 0.f)) {
         // No weight: nothing, also where a value is infinite or NaN.
 #pragma unroll
@@ -617,6 +642,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[c][i] = l == 0.f ? 0.f : o[c][i];
       }
+      const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
       const float f = l == 0.f ? 0.f : vs / l;
       auto sink_of = [&](int place) {
         const size_t row = (size_t)row_of(place);
@@ -628,15 +654,15 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         to.ml = parts.ml + part * 2;
         return to;
       };
-      const bool plain = live && !((again >> r32) & 1);
-      if (plain && half == 0)
-        sink_of(r).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
+      const bool plain = live && !((again >> r32e) & 1);
+      if (plain && halfe == 0 && part_wave == 0)
+        sink_of(re).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
       if (all) {
         // Rows lie across the lanes: through LDS (all waves are done with the stages),
         // so that a store has whole rows.
         constexpr int kOutRow = 2 * D + 16, kPieces = D / 8;
-        static_assert(32 * T::kWaves * kOutRow <= 2 * T::kStage, "rows fit the stages");
-        char* box = stages + wave * 32 * kOutRow;
+        static_assert(T::kRows * kOutRow <= 2 * T::kStage, "rows fit the stages");
+        char* box = stages + row_wave * 32 * kOutRow;
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
@@ -646,31 +672,34 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
                   ((uint32_t)f32_to_bf16_bits(o[c][i + 1] * f) << 16);
             x.y = (uint32_t)f32_to_bf16_bits(o[c][i + 2] * f) |
                   ((uint32_t)f32_to_bf16_bits(o[c][i + 3] * f) << 16);
-            *reinterpret_cast<uint2*>(box + r32 * kOutRow + (32 * c + 2 * i + 4 * half) * 2) = x;
+            *reinterpret_cast<uint2*>(box + r32e * kOutRow + (32 * (kBlocks * part_wave + c) + 2 * i + 4 * halfe) * 2) =
+                x;
           }
         const uint32_t rows = (uint32_t)__ballot(plain);
+        if constexpr (T::kSplit > 1) __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 32 * kPieces / 64; ++i) {
-          int x = i * 64 + lane;
+        for (int i = 0; i < 32 * kPieces / 64 / T::kSplit; ++i) {
+          int x = (i * T::kSplit + part_wave) * 64 + lane2;
           loaded(x);  // (as r)
           const int row = x / kPieces, piece = x % kPieces;
           const u32x4 y = *reinterpret_cast<const u32x4*>(box + row * kOutRow + piece * 16);
           if ((rows >> row) & 1)
-            store16(out_rows + (uint32_t)(row_of(wave * 32 + row) * D + piece * 8), y);
+            store16(out_rows + (uint32_t)(row_of(row_wave * 32 + row) * D + piece * 8), y);
         }
       } else if (plain) {
-        const Sink<D> to = sink_of(r);
+        const Sink<D> to = sink_of(re);
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<f32x4*>(to.o + 32 * c + 2 * i + 4 * half) =
+            *reinterpret_cast<f32x4*>(to.o + 32 * (kBlocks * part_wave + c) + 2 * i + 4 * halfe) =
                 f32x4{o[c][i] * f, o[c][i + 1] * f, o[c][i + 2] * f, o[c][i + 3] * f};
       }
 #pragma unroll 1
       for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
         const int x = __ffs((int)rest) - 1;
-        const int place = wave * 32 + x;
+        if (T::kSplit > 1 && x % T::kSplit != part_wave) continue;
+        const int place = row_wave * 32 + x;
         const int token2 = k * cut.tokens + fast_div(place, by_heads);
         const int end = w.at + token2 + 1;
         const int from = a.window > 0 ? max(0, end - a.window) : 0;
@@ -680,7 +709,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
     }
   }
 
-  if (a.few == 0) clear_rows(a);
+  if (a.few == 0) clear_rows(a, wave * 64 + lane_anew());
 }
 
 // Joins what the stretches left to be joined: workgroups (x, y) with x below `many`

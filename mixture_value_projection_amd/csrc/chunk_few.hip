@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
       a.B, slot, slots, kLeastTiles,
       [&](int b) { return few_of<kTracks>(a, b, kTileKeys).units(a.H); }, s_line, &line);
   if (tid == 0) parts.split[slot].n = 0;
-  clear_rows(a);
+  clear_rows(a, tid);
   if (!work) return;
 
   const uint32_t row_bytes = (uint32_t)a.H * T::kRow;
