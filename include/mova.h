@@ -579,10 +579,17 @@ size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_
  *   lse         float [T, n_heads] or NULL
  *
  * Rows without keys, infinite logits and infinite or NaN values that take part
- * or do not: as for mova_attention_paged, an infinite value gives NaN where its
- * key's weight is below 2^-126 of the row's largest.  Products accumulate in
- * fp32 and the softmax's maximum and sum are fp32.  Results are bitwise
- * reproducible for identical inputs; how a row's keys are split, and so its
+ * or do not: as for mova_attention_paged, but an infinite value gives NaN only
+ * where its key's weight is below 2^-126 of the row's largest, and where such
+ * weights are all that a part of the keys (of a row whose keys are split) has,
+ * what its values hold does not show.  Products accumulate in fp32 and the
+ * softmax's maximum and sum are fp32, the sum of the weights before they are
+ * rounded.  For the product with V the weights of a request of up to 16 rows a key
+ * head (tokens times n_heads / n_kv_heads), in batches of 32 requests and in those
+ * with no more than 16 rows on average, take part to 2^-16.  All others are rounded
+ * once: to bf16 (by 2^-9 at most) with bf16 pools, to fp16 (by 2^-12, or 2^-39 of
+ * the largest) with 8-bit ones.  The result is rounded once to bf16.  Results are
+ * bitwise reproducible for identical inputs; how a row's keys are split, and so its
  * last bits, depends on the lengths of the whole batch.  T <= 2^24, T * n_heads *
  * max_blocks * block_size <= 2^52, scale finite.  out and lse overlap no input.
  */

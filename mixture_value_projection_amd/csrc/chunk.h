@@ -7,8 +7,14 @@
 namespace mova {
 
 // Requests of so few rows (tokens times query heads of a key head) are the few-rows
-// kernel's, where it is launched.
-constexpr int kFewRows = 64;
+// kernel's, where it is launched: in batches with as few on average, and in those of
+// kFewRequests, where some will have few.  (64 requests of 500 to 8000 tokens, 32 heads
+// over 8, by that kernel and by the one of many rows: a token each 128 and 157 us, four
+// tokens, which fill sixteen rows, 142 and 165; eight, as two times sixteen, 260 and
+// 177.  60 with a token and 4 with 512, by both kernels and by one: 221 and 272 us; 32
+// with one and 32 with 64: 208 and 228.  Where no request has few rows the launch costs
+// 2 to 4 us, and where few short ones have, more: windows over 37 requests 87 and 78.)
+constexpr int kFewRows = 16, kFewRequests = 32;
 
 // What a stretch leaves to be joined.
 struct Split {
@@ -259,9 +265,10 @@ __device__ __forceinline__ void add_part(f32x4& o, float w, const f32x4& y) {
 //
 // Of up to kFew parts a row has D / 4 lanes, and a wave asks for all parts of kSets such
 // sets of rows at once: there are many rows, and what they cost is the round trips.  (The
-// parts of 255 tiles of 256 rows, 128 wide, two of each: a wave a row 44 us, so 26.)  Of
-// more parts a row has a wave: the maxima and sums come first, a lane a part, and then
-// the parts, 64 / (D / 4) times eight of them at once.
+// parts of 255 tiles of 256 rows, 128 wide, two of each: a wave a row 44 us, so 20; 28
+// with a branch around each read.)  Of more parts a row has a wave: the maxima and sums
+// come first, a lane a part, and then the parts, 64 / (D / 4) times eight of them at
+// once.  (24 parts of 32 rows: 30 us with a branch around each read, 8 so.)
 template <int D, int kWaves, int kFew, int kSets, class PartOf, class RowOf>
 __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts, int rows, int n,
                                           PartOf part_of, RowOf row_of) {
@@ -273,6 +280,7 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
   if (n <= kFew) {
     for (int r0 = wave * kAtOnce + mine; r0 < rows; r0 += waves * kAtOnce * kSets) {
       float pm[kSets][kFew], pl[kSets][kFew];
+      bool there[kSets][kFew];
       f32x4 y[kSets][kFew];
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
@@ -280,17 +288,20 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
         const bool live = r < rows && row_of(r) >= 0;
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
-          const long long p = live && i < n ? part_of(r, i) : -1;
-          pm[s][i] = -__builtin_huge_valf();
-          pl[s][i] = 0.f;
-          y[s][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (p >= 0) {
-            pm[s][i] = parts.ml[2 * p];
-            pl[s][i] = parts.ml[2 * p + 1];
-            y[s][i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)p * D + channel);
-          }
+          // (Reads of the first part where there is none: a branch would wait for the
+          // loads before it.)
+          const long long p = live && i < n ? part_of(r, i) : -1, at = max(p, 0ll);
+          there[s][i] = p >= 0;
+          pm[s][i] = parts.ml[2 * at];
+          pl[s][i] = parts.ml[2 * at + 1];
+          y[s][i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)at * D + channel);
         }
       }
+#pragma unroll
+      for (int s = 0; s < kSets; ++s)
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+          if (!there[s][i]) pl[s][i] = 0.f;
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
         const int r = r0 + s * waves * kAtOnce;
@@ -321,31 +332,44 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
     if (row < 0) continue;
     float m = -__builtin_huge_valf(), sum = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int x = lane; x < n; x += 64) {
-      const long long p = part_of(r, x);
-      if (p >= 0 && parts.ml[2 * p + 1] != 0.f) m = fmaxf(m, parts.ml[2 * p]);
+    // A lane's part among those from x0 on: its maximum and sum.
+    auto of_lane = [&](int x0, float* pm) {
+      const long long p = x0 + lane < n ? part_of(r, x0 + lane) : -1, at = max(p, 0ll);
+      *pm = parts.ml[2 * at];
+      const float pl = parts.ml[2 * at + 1];
+      return p < 0 ? 0.f : pl;
+    };
+    float first_m;
+    const float first_l = of_lane(0, &first_m);  // held: n is mostly below 64
+    if (first_l != 0.f) m = first_m;
+    for (int x0 = 64; x0 < n; x0 += 64) {
+      float pm;
+      if (of_lane(x0, &pm) != 0.f) m = fmaxf(m, pm);
     }
     m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
-    auto weight = [&](long long p) {
-      const float l = p < 0 ? 0.f : parts.ml[2 * p + 1];
-      return l == 0.f ? 0.f : l * __builtin_amdgcn_exp2f(parts.ml[2 * p] - finite_or_0(m));
+    auto weight = [&](int x0) {
+      float pm = first_m;
+      const float pl = x0 == 0 ? first_l : of_lane(x0, &pm);
+      return pl == 0.f ? 0.f : pl * __builtin_amdgcn_exp2f(pm - finite_or_0(m));
     };
-    for (int x = lane; x < n; x += 64) sum += weight(part_of(r, x));
+    for (int x0 = 0; x0 < n; x0 += 64) sum += weight(x0);
     sum = wave_sum(sum);
     const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
-    for (int x = 0; x < n; x += kAtOnce * kBatch) {
-      float w[kBatch];
-      f32x4 y[kBatch];
+    for (int x0 = 0; x0 < n; x0 += 64) {
+      const float w = weight(x0) * f;
+#pragma unroll 1
+      for (int x = 0; x < min(n - x0, 64); x += kAtOnce * kBatch) {
+        f32x4 y[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int at = x + i * kAtOnce + mine;
-        const long long p = at < n ? part_of(r, at) : -1;
-        w[i] = weight(p) * f;
-        y[i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)max(p, 0ll) * D + channel);
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = min(x0 + x + i * kAtOnce + mine, n - 1);
+          y[i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)max(part_of(r, at), 0ll) * D +
+                                                 channel);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) add_part(o, __shfl(w, x + i * kAtOnce + mine), y[i]);
       }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) add_part(o, w[i], y[i]);
     }
 #pragma unroll
     for (int step = kLanes; step < 64; step *= 2)

@@ -67,9 +67,13 @@ Cut cut_of(int G, int rows) {
 }
 
 // What a request brings to the line of work, in keys: each of its row tiles reads
-// keys [lo, hi), and kFixed more for what a tile costs beside them.
+// keys [lo, hi), and kFixed more for what a tile costs beside them.  (Of 0, 320 and 640:
+// a prompt of 8192 tokens 697, 596 and 599 us, 24 requests of 8 bits 606, 539 and 542,
+// 200 of 40 tokens 174, 113 and 127.)
 constexpr int kFixed = 320;
-// A stretch of the line is at least this long.
+// A stretch of the line is at least this long.  (Of 256, 512 and 1024: 19 tokens after
+// 130 21.8, 18.9 and 27.7 us, 64 after 2000 67.2, 70.5 and 55.0, 32 after 8000 208, 66
+// and 64, 4 requests of 64 after 500 46.0, 38.8 and 51.9.)
 constexpr int kLeastStretch = 512;
 struct Load {
   int at, live, tokens, window;
@@ -732,8 +736,7 @@ __global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts part
           return (((long long)slot + i) * 2 + (i == 0)) * all_rows + r;
         },
         [&](int r) -> long long {
-          const int place = p.lo + r % 16;  // lo: the first of the sixteen rows
-          const int token = fast_div(place, by_group);
+          const int place = r % 16, token = fast_div(place, by_group);
           return place < p.rows
                      ? p.row0 + (long long)token * a.Hq + (r / 16) * G + (place - token * G)
                      : -1;
@@ -787,7 +790,7 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
   });
   if (e != hipSuccess) return e;
   const long long rows = (long long)a.T * (a.Hq / a.H);
-  a.few = rows <= (long long)kFewRows * a.B ? kFewRows : 0;
+  a.few = rows <= (long long)kFewRows * a.B || a.B >= kFewRequests ? kFewRows : 0;
   const Parts few_parts = chunk_few_parts(a.part + many_floats(D));
   // The stretch, then what was split, then the parts.
   long long* stretch = (long long*)a.part;
@@ -810,7 +813,7 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  chunk_join_kernel<D, kFp8><<<dim3(many + few, few > 0 ? 4 : 8), 512, 0, stream>>>(
+  chunk_join_kernel<D, kFp8><<<dim3(many + few, 8), 512, 0, stream>>>(
       a, parts, many, cut.heads, by_heads, stretch, few_parts, chunk_few_tracks(a.H),
       make_fast_div(a.Hq / a.H));
   return hipGetLastError();

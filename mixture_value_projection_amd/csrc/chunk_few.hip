@@ -1,4 +1,4 @@
-// Chunk attention of requests with few rows (one token, drafts): up to kFewRows
+// Chunk attention of requests with few rows (one token, drafts): up to sixteen
 // rows, tokens times query heads, of a key head.
 //
 // Such a request does a few flops for each byte of cache, so everything serves
@@ -6,8 +6,8 @@
 // such requests lie in one line, cut into equal stretches; a workgroup's four waves
 // take four key heads at the same positions, or stripes of the tiles where there
 // are fewer; each wave is a pipeline of its own, a ring of tiles in LDS filled by
-// direct loads.  Sixteen rows take part in a wave's products; where a request has
-// more, others read the same keys past them, at about the same time.
+// direct loads.  Sixteen rows take part in a wave's products, so a request of more
+// would be read more than once.
 //
 // What differs from one token: rows see different keys, so logits are hidden row by
 // row in the tiles where the request's new tokens lie (and where its windows begin),
@@ -24,8 +24,12 @@ namespace mova {
 
 namespace {
 
+static_assert(kFewRows == 16, "the rows of a product");
 constexpr int kMaxGrid = 2 * kCus;
-// Tiles of a stretch at least: a row of so few is not cut.
+// Tiles of a stretch at least: a row of so few is not cut.  (Of one, two, four and
+// eight, with a row's parts read one after the other: 1 token after 130 17.0, 14.0, 15.2
+// and 18.1 us, 64 requests of 32 to 256 tokens 26.7, 26.5, 27.0 and 32.9, 4 tokens after
+// 2000 79.6, 48.4, 35.8 and 32.1.)
 constexpr int kLeastTiles = 4;
 
 // Request b as this kernel sees it.
@@ -34,10 +38,8 @@ struct Few {
   Chunk c;
   int lo;      // first key that any row sees
   int rows;    // of a key head; 0: another kernel's, or none
-  int qtiles;  // of 16 rows
   int n;       // tiles of the keys
-  __device__ __forceinline__ int groups(int H) const { return H / kTracks * qtiles; }
-  __device__ __forceinline__ long long units(int H) const { return (long long)n * groups(H); }
+  __device__ __forceinline__ long long units(int H) const { return (long long)n * (H / kTracks); }
 };
 template <int kTracks>
 __device__ __forceinline__ Few<kTracks> few_of(const ChunkArgs& a, int b, int tile_keys) {
@@ -45,7 +47,6 @@ __device__ __forceinline__ Few<kTracks> few_of(const ChunkArgs& a, int b, int ti
   f.c = chunk_of(a, b);
   f.rows = f.c.live * (a.Hq / a.H);
   if (f.rows > a.few) f.rows = 0;
-  f.qtiles = ceil_div(f.rows, 16);
   f.lo = a.window > 0 ? max(0, f.c.at + 1 - a.window) : 0;
   f.n = f.rows == 0 ? 0 : ceil_div(f.c.at + f.c.live - f.lo, tile_keys);
   return f;
@@ -97,13 +98,12 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
       if (++b >= a.B) return;
       f = few_of<kTracks>(a, b, kTileKeys);
     }
-    const int group = (int)floor_div(pos - first, f.n);
-    const int t0 = (int)(pos - first - (long long)group * f.n);
+    const int heads = (int)floor_div(pos - first, f.n);  // kTracks of them
+    const int t0 = (int)(pos - first - (long long)heads * f.n);
     const int t1 = (int)min((long long)f.n, t0 + (line.end - pos));
     pos += t1 - t0;
     const int nt = t1 - t0;
     const bool all = nt == f.n;
-    const int heads = group / f.qtiles, qt = group - heads * f.qtiles;
     const int h = heads * kTracks + tsub;
     const int len = f.c.at + f.c.live;
     const int32_t* table = a.table + (size_t)b * a.max_blocks;
@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
       p.row0 = (long long)f.c.row0 * a.Hq + (long long)heads * kTracks * G;
       p.before = 0;
       p.n = (int)floor_div(line.stretch - nt + f.n - 1, line.stretch) + 1;
-      p.lo = qt * 16;
+      p.lo = 0;
       p.hi = 0;
       p.rows = f.rows;
       p.heads = 0;
@@ -120,16 +120,14 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
     }
 
     // The lane's row.
-    const int place = qt * 16 + r16;
-    const bool has_row = place < f.rows;
-    const int token = fast_div(place, by_group);
-    const size_t row = (size_t)(f.c.row0 + token) * a.Hq + h * G + (place - token * G);
+    const bool has_row = r16 < f.rows;
+    const int token = fast_div(r16, by_group);
+    const size_t row = (size_t)(f.c.row0 + token) * a.Hq + h * G + (r16 - token * G);
     const int limit = has_row ? f.c.at + token : 0x3fffffff;
     const int lower = has_row && a.window > 0 ? max(0, limit + 1 - a.window) : 0;
     // Keys from `shared` up to `own` are seen by all rows here.
-    const int last_token = fast_div(min(qt * 16 + 15, f.rows - 1), by_group);
-    const int own = f.c.at + fast_div(qt * 16, by_group) + 1;
-    const int shared = a.window > 0 ? max(0, f.c.at + last_token + 1 - a.window) : 0;
+    const int own = f.c.at + 1;
+    const int shared = a.window > 0 ? max(0, f.c.at + f.c.live - a.window) : 0;
 
     auto key_of = [&](int x) { return f.lo + ((t0 + x) * kStripes + stripe) * T::kKeys; };
     auto table_address = [&](int x) {
@@ -407,8 +405,8 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
 #pragma unroll 1
     for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
       const int x = __ffs((int)rest) - 1;
-      const int t = fast_div(qt * 16 + x, by_group);
-      const size_t at = (size_t)(f.c.row0 + t) * a.Hq + h * G + (qt * 16 + x - t * G);
+      const int t = fast_div(x, by_group);
+      const size_t at = (size_t)(f.c.row0 + t) * a.Hq + h * G + (x - t * G);
       const int end = f.c.at + t + 1;
       const int from = a.window > 0 ? max(0, end - a.window) : 0;
       attend_row<D, kFp8>(a, by_block, b, h, a.q + at * D, max(from, f.lo + t0 * kTileKeys),

@@ -154,6 +154,26 @@ def test_free(seed, B, bs, longest, spare, share):
     check_free(lens, rng.integers(0, longest + 9, B) // bs * bs, *args, "whole blocks")
 
 
+@pytest.mark.parametrize("nb", [1023, 1025, 131073, 262145, 300001])
+def test_free_over_large_pools(nb):
+    """Blocks from all over the pool, more than the stack has room for."""
+    rng = np.random.default_rng(nb)
+    B, mb = 9, 110
+    table = rng.permutation(nb)[:B * mb].reshape(B, mb)
+    table[0, 0], table[1, 1] = nb - 1, 0
+    table[2:, :][(table[2:] == nb - 1) | (table[2:] == 0)] = -1
+    shares = np.zeros(nb, dtype=np.int64)
+    table[3, :20] = table[2, :20]
+    for p in table[3, :20]:
+        if p >= 0:
+            shares[p] += 1
+    lens = np.full(B, mb * 4)
+    for keep, cap in ((np.zeros(B), nb), (np.array([0, 9, 400, 0, 3, 0, 0, 8, 440]), nb),
+                      (np.zeros(B), 300)):
+        free = np.full(cap, -7)
+        check_free(lens, keep, 4, table, free, 5, shares, f"{nb} blocks, room for {cap}")
+
+
 def test_free_last_holder():
     """A block of four holders comes back with the fourth."""
     table = np.array([[3, 1, -1], [3, 2, -1], [3, 0, -1], [3, 4, 5]])
@@ -379,6 +399,26 @@ def test_a_life_of_the_cache(dtype):
     r = binding.paged_free(lens, torch.zeros_like(lens), bs, table, free, count, shares)
     assert int(r.free_count) == nb and sorted(host(free)[0].tolist()) == list(range(nb))
     assert int(shares.abs().sum()) == 0 and int(r.seq_lens.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("nb,bs,H,D,n,bounds", [
+    (5200, 16, 8, 128, 300, True),       # pools past the caches
+    (140000, 1, 1, 64, 70000, False),    # more items than a grid has workgroups
+])
+def test_copy_of_large_pools(nb, bs, H, D, n, bounds):
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(nb, bs, H, D, device=DEV, generator=g).bfloat16() for _ in range(2))
+    kb = torch.randn(nb, H, 2, D, device=DEV, generator=g).bfloat16() if bounds else None
+    perm = torch.randperm(nb, device=DEV, generator=g)[:2 * n].to(torch.int32)
+    src, dst = perm[:n].contiguous(), perm[n:].contiguous()
+    want = []
+    for x in (k, v, kb):
+        want.append(None if x is None else x.clone())
+        if x is not None:
+            want[-1][dst.long()] = x[src.long()]
+    binding.paged_copy(src, dst, k, v, k_bounds=kb)
+    for x, w in zip((k, v, kb), want):
+        assert x is None or torch.equal(x, w)
 
 
 def test_upkeep_in_graphs():
