@@ -587,7 +587,7 @@ size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_
  * rounded.  For the product with V the weights of a request of up to 16 rows a key
  * head (tokens times n_heads / n_kv_heads), in batches of 32 requests and in those
  * with no more than 16 rows on average, take part to 2^-16.  All others are rounded
- * once: to bf16 (by 2^-9 at most) with bf16 pools, to fp16 (by 2^-12, or 2^-39 of
+ * once: to bf16 (by 2^-8 at most) with bf16 pools, to fp16 (by 2^-11, or 2^-39 of
  * the largest) with 8-bit ones.  The result is rounded once to bf16.  Results are
  * bitwise reproducible for identical inputs; how a row's keys are split, and so its
  * last bits, depends on the lengths of the whole batch.  T <= 2^24, T * n_heads *

@@ -253,6 +253,8 @@ __device__ __forceinline__ void put_joined(const ChunkArgs& a, size_t row, int c
 __device__ __forceinline__ float finite_or_0(float m) {
   return m == -__builtin_huge_valf() ? 0.f : m;
 }
+typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+
 // o += w y; what a part without weight holds may be anything.
 __device__ __forceinline__ void add_part(f32x4& o, float w, const f32x4& y) {
 #pragma unroll
@@ -280,18 +282,19 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
   if (n <= kFew) {
     for (int r0 = wave * kAtOnce + mine; r0 < rows; r0 += waves * kAtOnce * kSets) {
       float pm[kSets][kFew], pl[kSets][kFew];
-      bool there[kSets][kFew];
+      uint32_t there[kSets];  // a bit a part
       f32x4 y[kSets][kFew];
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
         const int r = r0 + s * waves * kAtOnce;
         const bool live = r < rows && row_of(r) >= 0;
+        there[s] = 0;
 #pragma unroll
         for (int i = 0; i < kFew; ++i) {
           // (Reads of the first part where there is none: a branch would wait for the
           // loads before it.)
           const long long p = live && i < n ? part_of(r, i) : -1, at = max(p, 0ll);
-          there[s][i] = p >= 0;
+          there[s] |= (uint32_t)(p >= 0) << i;
           pm[s][i] = parts.ml[2 * at];
           pl[s][i] = parts.ml[2 * at + 1];
           y[s][i] = *reinterpret_cast<const f32x4*>(parts.o + (size_t)at * D + channel);
@@ -301,7 +304,7 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
       for (int s = 0; s < kSets; ++s)
 #pragma unroll
         for (int i = 0; i < kFew; ++i)
-          if (!there[s][i]) pl[s][i] = 0.f;
+          if (!(there[s] >> i & 1)) pl[s][i] = 0.f;
 #pragma unroll
       for (int s = 0; s < kSets; ++s) {
         const int r = r0 + s * waves * kAtOnce;
@@ -333,24 +336,23 @@ __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts
     float m = -__builtin_huge_valf(), sum = 0.f;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     // A lane's part among those from x0 on: its maximum and sum.
-    auto of_lane = [&](int x0, float* pm) {
+    auto of_lane = [&](int x0) {
       const long long p = x0 + lane < n ? part_of(r, x0 + lane) : -1, at = max(p, 0ll);
-      *pm = parts.ml[2 * at];
-      const float pl = parts.ml[2 * at + 1];
-      return p < 0 ? 0.f : pl;
+      f32x2 x = {parts.ml[2 * at], parts.ml[2 * at + 1]};
+      if (p < 0) x[1] = 0.f;
+      return x;
     };
-    float first_m;
-    const float first_l = of_lane(0, &first_m);  // held: n is mostly below 64
-    if (first_l != 0.f) m = first_m;
+    const f32x2 first = of_lane(0);  // held: n is mostly below 64
+    if (first[1] != 0.f) m = first[0];
     for (int x0 = 64; x0 < n; x0 += 64) {
-      float pm;
-      if (of_lane(x0, &pm) != 0.f) m = fmaxf(m, pm);
+      const f32x2 x = of_lane(x0);
+      if (x[1] != 0.f) m = fmaxf(m, x[0]);
     }
     m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
     auto weight = [&](int x0) {
-      float pm = first_m;
-      const float pl = x0 == 0 ? first_l : of_lane(x0, &pm);
-      return pl == 0.f ? 0.f : pl * __builtin_amdgcn_exp2f(pm - finite_or_0(m));
+      f32x2 x = first;
+      if (x0 > 0) x = of_lane(x0);
+      return x[1] == 0.f ? 0.f : x[1] * __builtin_amdgcn_exp2f(x[0] - finite_or_0(m));
     };
     for (int x0 = 0; x0 < n; x0 += 64) sum += weight(x0);
     sum = wave_sum(sum);

@@ -170,6 +170,34 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 
 }  // namespace
 
+// Rows, tokens times query heads of a key head, are many here, so a key tile is used
+// by 256 of them (128 where rows have 256 channels) and the matrix products bound it.
+//
+// A workgroup has eight waves of 32 rows.  Logits are K Q^T, which leaves 32 rows across
+// the lanes and a tile's 64 keys down the registers: maximum and sum of a row need one
+// exchange between two lanes, and the weights lie as the next product, V^T P^T, takes
+// them.  Queries and sums stay in registers.  Keys and values go through registers into
+// padded rows in LDS (8-bit ones are widened on the way, once for eight waves), keys two
+// tiles ahead and values one, so that a tile costs one barrier; slots of keys are looked
+// up by one wave, five tiles ahead.
+//
+// Two waves share a SIMD, and neither the products nor the softmax may wait for the other:
+// in a tile's turn the products of the next tile's keys stand between this tile's first
+// weights, the products with the values between the rest, and the next maximum is formed
+// behind them.  Sums are brought to a new maximum only once it is 2^kSlack times the old
+// one's weight, so most tiles multiply nothing.  The order is fixed by hand: the
+// compiler's own put the parts behind each other.
+//
+// The line of work is all row tiles of the batch, cut into equal stretches for 256
+// workgroups: lengths are on the device, and a tile's cost differs by its place in a
+// prompt.  A tile in two stretches leaves parts, which chunk_join_kernel joins.
+//
+// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 582 to 620 us (0.89 to 0.95
+// PF/s; a product of two 16384 matrices reaches 1.6), 2048 tokens after 129,024 4.1 to
+// 4.4 ms (1.0).  A tile of 64 keys takes 3900 cycles, 2130 of them matrix instructions; 32
+// exponentials, conversions and maxima a lane, twice on a SIMD, are what does not fit
+// between.  A row tile's start and end take 18,000.  With one tile ahead, by direct loads
+// to LDS, and a tile's products all ahead of its softmax, the long one took 4.97 ms.
 template <int D, bool kFp8>
 __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_kernel(
     ChunkArgs a, Parts parts, FastDiv by_block, Cut cut, FastDiv by_heads, long long* stretch_of) {
