@@ -217,9 +217,9 @@ hipError_t launch_paged_fork(const ForkArgs& a, hipStream_t stream) {
 // With those numbers the second one brings the counts down and puts the blocks on
 // the stack, highest first.
 //
-// A workgroup alone waits for memory at each turn: the 28,689 entries of 150 rows of
-// a pool of 15,000 blocks took one 80 us with atomics on the counts and 32 with counts
-// in LDS; these two take 17 and 4.  The 1051 of a step of 64 rows took it 8; 6 and 4.
+// A workgroup alone waits for memory at each turn: the 28,689 entries that 203 rows
+// give back took one 80 us with atomics on the counts and 32 with counts in LDS; these
+// two take 17 and 4.  The 1051 of a step of 64 rows took it 8; 6 and 4.
 __global__ __launch_bounds__(kFreeThreads) void free_count_kernel(FreeArgs a, FastDiv by_block,
                                                                   int run) {
   extern __shared__ __attribute__((aligned(16))) char free_lds[];
