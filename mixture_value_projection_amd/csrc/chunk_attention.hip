@@ -194,9 +194,12 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 582 to 620 us (0.89 to 0.95
 // PF/s; a product of two 16384 matrices reaches 1.6), 2048 tokens after 129,024 4.1 to
-// 4.4 ms (1.0).  A tile of 64 keys takes 3900 cycles, 2130 of them matrix instructions; 32
-// exponentials, conversions and maxima a lane, twice on a SIMD, are what does not fit
-// between.  A row tile's start and end take 18,000.  With one tile ahead, by direct loads
+// 4.4 ms (1.0).  A tile of 64 keys takes 3900 cycles.  The matrix instructions of a
+// SIMD's two waves are 2130 of them, and the eight waves' reads of keys and values 2050 of
+// LDS (256 KB at 128 bytes a cycle): both would have to go on without a pause, beside 32
+// exponentials, conversions and maxima a lane.  How the weights are spread over the
+// products, how far reads run ahead, and the waves' priorities change nothing (within 1 %).
+// A row tile's start and end take 18,000.  With one tile ahead, by direct loads
 // to LDS, and a tile's products all ahead of its softmax, the long one took 4.97 ms.
 template <int D, bool kFp8>
 __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_kernel(

@@ -184,3 +184,61 @@ def test_graph_whose_requests_change():
         torch.cuda.synchronize()
         want, _, tol, _ = c.want(before)
         assert bool(((out.cpu().double() - want).abs() <= tol).all()), str(new)
+
+
+@pytest.mark.parametrize("Hq,H,D,bs,dtype", SHAPES)
+def test_rows_behind_the_last_token(Hq, H, D, bs, dtype):
+    """Requests of which only the first rows have a token in the cache: the
+    others are zeros, whichever kernel reads the request."""
+    for new in ([4, 1, 3, 2], [40, 7, 90, 1]):
+        c = Case(16, [33, 0, 200, 64], new, Hq, H, D, bs, dtype)
+        c.lens = c.cached + np.array([2, 0, 1 + new[2] // 3, 1])
+        c.check(f"{new} {Hq}/{H}/{D}")
+
+
+@pytest.mark.parametrize("new", [[1, 2, 1], [70, 3, 100]])
+def test_scale_of_zero(new):
+    """Every key that a row sees has the same weight."""
+    c = Case(17, [300, 0, 64], new, 8, 2, 128, 16)
+    c.scale = 0.0
+    c.check("scale 0")
+
+
+@pytest.mark.parametrize("B", [31, 32, 33])
+def test_batches_around_the_number_of_both_kernels(B):
+    """Many rows on average, few in most requests."""
+    new = [1] * (B - 2) + [150, 200]
+    rng = np.random.default_rng(B)
+    Case(18, rng.integers(0, 200, B), new, 8, 2, 128, 16).check(f"{B} requests")
+
+
+def test_requests_that_share_their_blocks():
+    """Two rows of the table over the same blocks, one token apart."""
+    c = Case(19, [100, 100, 100], [2, 1, 40], 8, 2, 64, 16)
+    c.table[1] = c.table[0]
+    c.table[2, :6] = c.table[0, :6]
+    c.check("shared")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("new", [[2, 1, 1], [2, 300, 40]])
+def test_pools_past_32_bits(dtype, new):
+    """Blocks whose elements and bytes lie past 2^32: the same bits as from a small
+    pool; and the blocks moved there by a copy."""
+    c = Case(20, [500, 0, 90], new, 8, 2, 128, 64, dtype)
+    args, kw = c.args(), c.kw()
+    want = binding.attention_chunk_paged(*args, **kw)
+    n = c.k.shape[0]
+    slot = 64 * 2 * 128
+    nb = (1 << 32) // slot * (1 if dtype == BF16 else 2) + 1000
+    big = [torch.full((nb, 64, 2, 128), math.nan, device=DEV, dtype=BF16).to(dtype)
+           if dtype == BF16 else
+           torch.full((nb, 64, 2, 128), 0x7f, device=DEV, dtype=torch.uint8).view(dtype)
+           for _ in range(2)]
+    for x, small in zip(big, args[1:3]):
+        x.view(torch.uint8)[:n].copy_(small.view(torch.uint8))
+    src, dst = np.arange(n), nb - 1 - 7 * np.arange(n)
+    binding.paged_copy(i32(src), i32(dst), *big)
+    table = np.where(c.table < 0, -1, nb - 1 - 7 * np.clip(c.table, 0, n - 1))
+    got = binding.attention_chunk_paged(args[0], *big, i32(table), *args[4:], **kw)
+    assert torch.equal(got, want)
