@@ -557,6 +557,11 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
           constexpr int kGroups = 2 * T::kParts, kSums = kGroups * kBlocks;  // of 16 keys
           constexpr int kFirst = kValues * 5 / 8;  // weights among the products with keys
           static_assert(2 * T::kLoads <= kProducts / 2 && kFirst >= 8 * (kGroups / 2), "order");
+          // The weights are rounded once.  A second part, as the few-rows kernel has it,
+          // would be half as many products again with the values, where the products
+          // bound this: against 64 bits the results are off by 0.0021 to 0.0023 of their
+          // norm, 0.0016 of which is their own rounding to bf16.  The sum l is that of
+          // the weights as they were.
           union Weights {
             bf16_t e[8];
             f16_t f[8];

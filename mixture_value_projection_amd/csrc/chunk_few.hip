@@ -9,6 +9,9 @@
 // direct loads.  Sixteen rows take part in a wave's products, so a request of more
 // would be read more than once.
 //
+// Bound by the cache's bytes: 64 requests of 500 to 8000 tokens with four new ones, 32
+// heads over 8 of 128, 738 MB in 130 us, 5.7 TB/s.
+//
 // What differs from one token: rows see different keys, so logits are hidden row by
 // row in the tiles where the request's new tokens lie (and where its windows begin),
 // and a row whose sums become infinite or NaN is formed once more from the keys that

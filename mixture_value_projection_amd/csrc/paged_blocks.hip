@@ -43,7 +43,7 @@ __device__ __forceinline__ int clamp_len(int n, int most) { return min(max(n, 0)
 // own, as far as a grid goes (770 MB read and written in blocks of 32 KB: 2048
 // workgroups with items in turn 180 us, this 150).  Pools larger than the last cache
 // pass the caches by: that takes 132 us (5.8 TB/s) for those 770 MB, but for 60 MB of
-// a pool of 128 MB 14 us, and 11 through the caches.
+// a pool of 119 MB 14 us, and 11 through the caches.
 constexpr size_t kLastCache = (size_t)256 << 20;
 constexpr int kCopyGrid = 65536;
 constexpr int kCopyAtOnce = 4, kCopyPieces = 256 * kCopyAtOnce;
@@ -109,6 +109,8 @@ hipError_t launch_paged_copy(const CopyArgs& a, hipStream_t stream) {
 // Every workgroup reads all pairs and forms the running sum of the blocks that
 // they take; then it goes through its share of their entries.  Parents' rows
 // are only read and children's only written, so no workgroup waits for another.
+// Bound by its round trips: lengths, then entries, then counts.  56 rows of up to 500
+// blocks 4.6 us, 12 of up to 6250 4.8.
 __global__ __launch_bounds__(kForkThreads) void paged_fork_kernel(ForkArgs a, FastDiv by_block,
                                                                   int chunks) {
   extern __shared__ int fork_lds[];
@@ -377,7 +379,9 @@ hipError_t launch_paged_free(const FreeArgs& a, hipStream_t stream) {
 // The first kernel, one workgroup, turns the stack into bits and counts them by
 // runs of 256 blocks; with those counts in LDS, the second one ranks any block
 // in a step and finds the block of any rank in a search, so that table, stack,
-// counts and lists are written side by side.
+// counts and lists are written side by side.  Both are bound by their round trips: a
+// pool of 24,274 blocks, 9000 and more of them free, 4.8 and 7.3 us, one of 1752 2.7 and
+// 6.2.
 __global__ __launch_bounds__(kFreeThreads) void compact_rank_kernel(CompactArgs a) {
   extern __shared__ uint32_t compact_bits[];
   __shared__ long long tmp[kFreeThreads / 64];
