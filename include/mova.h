@@ -634,7 +634,7 @@ int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v
  *                free_count_out int32 [1], not the same address
  *   shares       int32 [num_blocks]     in / out
  *   seq_lens     int32 [B]  out: cached_lens, for the children the tokens they
- *                got; not the address of cached_lens
+ *                got; not the address of cached_lens or fork_lens
  *   copy_src, copy_dst int32 [n] out: -1 where nothing is to be copied
  *
  * n <= 2048.

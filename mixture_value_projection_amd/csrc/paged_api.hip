@@ -263,6 +263,8 @@ int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v
       !aligned(block_table, 4) || !aligned(cached_lens, 4) || !aligned(seq_lens, 4) ||
       !aligned(cu_new, 4) || !aligned(out, 16) || !aligned(lse, 4))
     return MOVA_ERR_INVALID_ARG;
+  // Several workgroups read a row of q, at different times.
+  if (out == q) return MOVA_ERR_INVALID_ARG;
   const size_t need = mova_attention_chunk_workspace_bytes(T, B, n_heads, n_kv_heads, head_dim,
                                                            max_blocks, block_size);
   rc = check_workspace(workspace, workspace_bytes, need);
@@ -325,7 +327,8 @@ int mova_paged_fork(const int32_t* parents, const int32_t* children, const int32
       !aligned(seq_lens, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4))
     return MOVA_ERR_INVALID_ARG;
   // Every workgroup reads these while one of them writes the others.
-  if (free_count == free_count_out || (B > 0 && cached_lens == seq_lens))
+  if (free_count == free_count_out || (B > 0 && cached_lens == seq_lens) ||
+      (n > 0 && (fork_lens == seq_lens || copy_src == copy_dst)))
     return MOVA_ERR_INVALID_ARG;
   const ForkArgs a{parents, children, fork_lens, n, cached_lens, B, block_size, max_blocks,
                    block_table, free_blocks, free_capacity, free_count, free_count_out, shares,

@@ -35,7 +35,7 @@ int main(void) {
          MOVA_ERR_UNSUPPORTED);
   expect("chunk workspace",
          mova_attention_chunk_paged(P, P, P, 1, f, f, 40, 16, i, 10, i, i, i, 9, 4, 32, 8, 128, 0.1f,
-                                    0, P, f, P, 16, 0),
+                                    0, (char*)P + 4096, f, P, 16, 0),
          MOVA_ERR_WORKSPACE);
   for (int b = 1; b <= 2048; b *= 2)
     for (int h = 1; h <= 64; h *= 2)

@@ -32,7 +32,7 @@ def call(fn, defaults, kw):
 
 CHUNK = dict(q=FAKE, k=FAKE, v=FAKE, dtype=1, ks=FAKE, vs=FAKE, nb=40, bs=16, table=FAKE, mb=10,
              cached=FAKE, lens=FAKE, cu=FAKE, T=8, B=4, Hq=32, H=8, D=128, scale=0.1, window=0,
-             out=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 40, stream=None)
+             out=FAKE + 4096, lse=FAKE, ws=FAKE, wsb=1 << 40, stream=None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -46,6 +46,7 @@ CHUNK = dict(q=FAKE, k=FAKE, v=FAKE, dtype=1, ks=FAKE, vs=FAKE, nb=40, bs=16, ta
     (dict(scale=float("nan")), UNSUPPORTED), (dict(scale=float("inf")), UNSUPPORTED),
     *[({n: None}, INVALID) for n in ("q", "k", "v", "table", "cached", "lens", "cu", "out")],
     *[({n: FAKE + 8}, INVALID) for n in ("q", "k", "v", "out")],
+    (dict(out=FAKE), INVALID),
     *[({n: FAKE + 2}, INVALID) for n in ("ks", "vs", "table", "cached", "lens", "cu", "lse")],
     (dict(ws=None), WORKSPACE), (dict(wsb=16), WORKSPACE), (dict(ws=FAKE + 16), INVALID),
     (dict(T=0, q=None, ws=None), OK), (dict(B=0, table=None, ws=None), OK),
@@ -64,7 +65,7 @@ def test_chunk_workspace(lib):
 
 FORK = dict(par=FAKE, chi=FAKE, take=None, n=3, cached=FAKE, B=4, bs=16, mb=10, table=FAKE, free=FAKE,
             cap=40, count=FAKE, count_out=FAKE + 4, shares=FAKE, nb=40, seq=FAKE + 64, src=FAKE,
-            dst=FAKE, stream=None)
+            dst=FAKE + 128, stream=None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -76,7 +77,8 @@ FORK = dict(par=FAKE, chi=FAKE, take=None, n=3, cached=FAKE, B=4, bs=16, mb=10, 
                                      "shares", "seq", "src", "dst")],
     *[({n: FAKE + 2}, INVALID) for n in ("par", "chi", "take", "cached", "table", "free", "count",
                                          "count_out", "shares", "seq", "src", "dst")],
-    (dict(count_out=FAKE), INVALID), (dict(seq=FAKE), INVALID),
+    (dict(count_out=FAKE), INVALID), (dict(seq=FAKE), INVALID), (dict(dst=FAKE), INVALID),
+    (dict(take=FAKE + 64), INVALID),
 ])
 def test_fork_rejects(lib, kw, rc):
     assert call(lib.mova_paged_fork, FORK, kw) == rc
