@@ -20,7 +20,8 @@ constexpr int kFewRows = 16, kFewRequests = 32;
 struct Split {
   long long row0;    // the rows' place in the output
   long long before;  // units of the stretch ahead of them
-  int n;             // stretches; 0: nothing was split
+  int n;             // stretches; 0: nothing was split; -x: in the middle of what the
+                     // stretch x before this one left
   int lo, hi;        // keys
   int rows, heads;   // tokens and query heads
   int pad;
@@ -255,14 +256,27 @@ __device__ __forceinline__ float finite_or_0(float m) {
 }
 typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
 
+// A record as the whole wave has it: what is found from it takes scalar registers, and no
+// branches per lane.
+__device__ __forceinline__ Split split_of(const Split* from) {
+  union {
+    Split s;
+    int w[sizeof(Split) / 4];
+  } x;
+  x.s = *from;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Split) / 4); ++i) x.w[i] = __builtin_amdgcn_readfirstlane(x.w[i]);
+  return x.s;
+}
+
 // o += w y; what a part without weight holds may be anything.
 __device__ __forceinline__ void add_part(f32x4& o, float w, const f32x4& y) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) o[c] = w == 0.f ? o[c] : fmaf(w, y[c], o[c]);
 }
 
-// Joins the parts of `rows` rows, n of each, with the kWaves waves of the gridDim.y
-// workgroups of a stretch.  part_of(r, i) is a part's place, or -1; row_of(r) the row's
+// Joins share `share` of `shares` of the parts of `rows` rows, n of each, with kWaves
+// waves.  part_of(r, i) is a part's place, or -1; row_of(r) the row's
 // in the output, or -1.
 //
 // Of up to kFew parts a row has D / 4 lanes, and a wave asks for all parts of kSets such
@@ -273,11 +287,11 @@ __device__ __forceinline__ void add_part(f32x4& o, float w, const f32x4& y) {
 // once.  (24 parts of 32 rows: 30 us with a branch around each read, 8 so.)
 template <int D, int kWaves, int kFew, int kSets, class PartOf, class RowOf>
 __device__ __forceinline__ void join_rows(const ChunkArgs& a, const Parts& parts, int rows, int n,
-                                          PartOf part_of, RowOf row_of) {
+                                          int share, int shares, PartOf part_of, RowOf row_of) {
   constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kBatch = 8;
   const int lane = threadIdx.x & 63;
-  const int wave = blockIdx.y * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = gridDim.y * kWaves;
+  const int wave = share * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = shares * kWaves;
   const int mine = lane / kLanes, channel = lane % kLanes * 4;
   if (n <= kFew) {
     for (int r0 = wave * kAtOnce + mine; r0 < rows; r0 += waves * kAtOnce * kSets) {

@@ -276,6 +276,12 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         p.heads = min(cut.heads, G - xb * cut.heads);
         parts.split[slot] = p;
       }
+      // A stretch in the middle of a tile: how far behind the tile's first one.
+      if (x0 > 0 && x1 < w.units(k) && wave == 0 && lane_anew() == 0) {
+        long long stretch = line.stretch;
+        asm volatile("" : "+s"(stretch));
+        parts.split[slot].n = -(int)floor_div(x0 + stretch - 1, stretch);
+      }
       if (seg.begin >= seg.end) continue;
       const bool all = seg.begin == seg.first && seg.end == seg.last;
       const int h = job / cut.head_blocks, xb = job - h * cut.head_blocks;
@@ -761,13 +767,20 @@ __global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts part
                                                          Parts few_parts, int few_tracks,
                                                          FastDiv by_group) {
   using T = Tile<D, kFp8>;
+  // The workgroups of a tile's first stretch and of those in its middle, which leave no
+  // tile of their own, have shares, in turn: a CU alone reads few bytes at once, and
+  // first stretches alone may all lie on one XCD.  (40 tokens after 30,000, 33 parts a
+  // row: by the first stretches' workgroups 111 us, by all 42; 32 after 8000 33 and 17.)
   if ((int)blockIdx.x >= many) {
-    const int slot = blockIdx.x - many;
-    const Split p = few_parts.split[slot];
+    int slot = blockIdx.x - many;
+    const int behind = max(-__builtin_amdgcn_readfirstlane(few_parts.split[slot].n), 0);
+    slot -= behind;
+    const Split p = split_of(few_parts.split + slot);
     if (p.n == 0) return;
+    const int share = blockIdx.y * (p.n - 1) + behind, shares = (p.n - 1) * gridDim.y;
     const int G = a.Hq / a.H, all_rows = 16 * few_tracks;
     join_rows<D, 8, 8, 1>(
-        a, few_parts, all_rows, p.n,
+        a, few_parts, all_rows, p.n, share, shares,
         [&](int r, int i) -> long long {
           return (((long long)slot + i) * 2 + (i == 0)) * all_rows + r;
         },
@@ -779,9 +792,12 @@ __global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts part
         });
     return;
   }
-  const int slot = blockIdx.x;
-  const Split p = parts.split[slot];
+  int slot = blockIdx.x;
+  const int behind = max(-__builtin_amdgcn_readfirstlane(parts.split[slot].n), 0);
+  slot -= behind;
+  const Split p = split_of(parts.split + slot);
   if (p.n == 0) return;
+  const int share = blockIdx.y * (p.n - 1) + behind, shares = (p.n - 1) * gridDim.y;
   const long long stretch = *stretch_of, size = p.hi - p.lo + kFixed;
   auto segment = [&](int i) {
     return segment_of<T::kKeys>(p.lo, p.hi, max(stretch * i - p.before, 0ll),
@@ -795,7 +811,7 @@ __global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts part
   }
   if (whole) return;
   join_rows<D, 8, 4, 2>(
-      a, parts, T::kRows, p.n,
+      a, parts, T::kRows, p.n, share, shares,
       [&](int r, int i) -> long long {
         const Segment s = segment(i);
         return s.begin < s.end ? ((long long)(slot + i) * 2 + (s.begin == s.first)) * T::kRows + r

@@ -121,6 +121,9 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
       p.heads = 0;
       parts.split[slot] = p;
     }
+    // (As in the other kernel.)
+    if (t0 > 0 && t0 + nt < f.n && tid == 0)
+      parts.split[slot].n = -(int)floor_div(t0 + line.stretch - 1, line.stretch);
 
     // The lane's row.
     const bool has_row = r16 < f.rows;
