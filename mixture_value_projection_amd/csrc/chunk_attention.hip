@@ -72,8 +72,8 @@ Cut cut_of(int G, int rows) {
 // 200 of 40 tokens 174, 113 and 127.)
 constexpr int kFixed = 320;
 // A stretch of the line is at least this long.  (Of 256, 512 and 1024: 19 tokens after
-// 130 21.8, 18.9 and 27.7 us, 64 after 2000 67.2, 70.5 and 55.0, 32 after 8000 208, 66
-// and 64, 4 requests of 64 after 500 46.0, 38.8 and 51.9.)
+// 130 21.5, 17.7 and 26.7 us, 64 after 2000 58, 63 and 54, 4 requests of 64 after 500 53,
+// 38 and 52, a prompt of 512 37, 40 and 52.)
 constexpr int kLeastStretch = 512;
 struct Load {
   int at, live, tokens, window;

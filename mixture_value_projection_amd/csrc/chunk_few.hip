@@ -29,10 +29,9 @@ namespace {
 
 static_assert(kFewRows == 16, "the rows of a product");
 constexpr int kMaxGrid = 2 * kCus;
-// Tiles of a stretch at least: a row of so few is not cut.  (Of one, two, four and
-// eight, with a row's parts read one after the other: 1 token after 130 17.0, 14.0, 15.2
-// and 18.1 us, 64 requests of 32 to 256 tokens 26.7, 26.5, 27.0 and 32.9, 4 tokens after
-// 2000 79.6, 48.4, 35.8 and 32.1.)
+// Tiles of a stretch at least: a row of so few is not cut.  (Of two, four and eight: 1
+// token after 130 12.7, 14.2 and 17.4 us, 64 requests of 32 to 256 tokens 24.5, 25.5 and
+// 31.9, 1 token after 8000 31.6, 25.9 and 27.3.)
 constexpr int kLeastTiles = 4;
 
 // Request b as this kernel sees it.
