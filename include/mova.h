@@ -590,7 +590,9 @@ size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_
  * once: to bf16 (by 2^-8 at most) with bf16 pools, to fp16 (by 2^-11, or 2^-39 of
  * the largest) with 8-bit ones.  The result is rounded once to bf16.  Results are
  * bitwise reproducible for identical inputs; how a row's keys are split, and so its
- * last bits, depends on the lengths of the whole batch.  T <= 2^24, T * n_heads *
+ * last bits, depends on the lengths of the whole batch.  Rows whose sums meet an
+ * infinite or NaN value, or pass the largest number, are formed twice, which takes up
+ * to some twenty times as long.  T <= 2^24, T * n_heads *
  * max_blocks * block_size <= 2^52, scale finite.  out and lse overlap no input.
  */
 int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v_cache,

@@ -53,7 +53,9 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 // The lane's number, formed anew: nothing that follows from it is held from before.
 __device__ __forceinline__ int lane_anew() {
-  int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  uint32_t all = ~0u;
+  asm volatile("" : "+s"(all));
+  int lane = (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u));
   asm volatile("" : "+v"(lane));
   return lane;
 }
@@ -75,27 +77,29 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, int b) {
   return c;
 }
 
-// 8 elements of the pool.
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+
+// 8 elements of the pool as bf16 (exact).
 template <bool kFp8>
-__device__ __forceinline__ void load8(const void* pool, size_t at, float (&x)[8]) {
+__device__ __forceinline__ Frag16 load8(const void* pool, size_t at) {
+  Frag16 f;
   if constexpr (kFp8) {
     const uint2 w = *reinterpret_cast<const uint2*>((const uint8_t*)pool + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.x >> (8 * i)), 0);
-      x[4 + i] = __builtin_amdgcn_cvt_f32_fp8((int)(w.y >> (8 * i)), 0);
-    }
+    for (int i = 0; i < 8; ++i)
+      f.h[i] = (__bf16)__builtin_amdgcn_cvt_f32_fp8((int)((i < 4 ? w.x : w.y) >> 8 * (i % 4)), 0);
   } else {
-    Frag16 f;
     f.u = load16((const bf16_t*)pool + at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)f.h[i];
   }
+  return f;
 }
+// One element's bits as bf16.
 template <bool kFp8>
-__device__ __forceinline__ float load1(const void* pool, size_t at) {
-  if constexpr (kFp8) return __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)pool)[at], 0);
-  else return (float)((const bf16_t*)pool)[at];
+__device__ __forceinline__ uint32_t load1(const void* pool, size_t at) {
+  if constexpr (kFp8)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)pool)[at], 0)) >> 16;
+  else
+    return ((const uint16_t*)pool)[at];
 }
 
 struct Shared {
@@ -156,76 +160,147 @@ struct Sink {
   }
 };
 
-// One row by one wave with everything in fp32, a lane a key for the logits and
-// D / 64 channels a lane for the values: the maximum first, then weights and
-// sums.  Only keys that take part are touched, so infinite and NaN values of
-// others do not show, and sums that pass the largest number are formed with
-// weights 2^-32 as large (a row has at most 2^30 keys).  For the rows whose sums
-// the matrix products left infinite or NaN.
-template <int D, bool kFp8>
-__device__ __forceinline__ void attend_row(const ChunkArgs& a, FastDiv by_block, int b, int h,
-                                           const bf16_t* q, int lo, int hi, const Sink<D>& sink) {
-  constexpr int kPer = D / 64;
-  constexpr float kDown = 0x1p-32f;
-  const int lane = lane_anew();
-  const float qs = a.scale * (a.k_scale != nullptr ? a.k_scale[h] : 1.f) * kLog2e;
+// Rows whose sums the matrix products left infinite or NaN, formed again by one wave,
+// up to 32 side by side: o = sum_p exp2(s_p - base) v_p over keys [lo, hi), for channels
+// [32 c0, 32 c1).  A lane has a row (lanes i and i + 32 the same): its query q (null:
+// none), the positions [lower, limit] that it sees and its base; put(c, y) takes factor
+// times its channels one by one.
+//
+// Finite values are summed as ever, with weights to 2^-16; where such a sum passes the
+// largest number, it is formed once more with weights 2^-40 as large.  Values that are
+// infinite or NaN take part as zeros, and which of them a row has is counted by a product
+// of their kinds with the kinds of the weights: so nothing shows of a value that a row
+// does not see, and one with a weight makes its channel infinite, or NaN.
+//
+// Keys and values come straight from the pool, and the logits are formed again for each
+// 32 channels, which keeps this in the registers that the kernels have.  Bound by round
+// trips to memory, some 1.5 us for 32 keys, 32 rows and 32 channels; a row at a time, with
+// its values key by key, took 140 times a call where this takes 8.  (A value that all rows
+// of a prompt see, 32 heads over 8 of 128: 512 tokens 294 us, a row at a time 5169, without
+// the value 47; 2048 tokens 657, 12,358 and 86; 8192 tokens 9.7 ms, without it 0.58.)
+template <int D, bool kFp8, class Put>
+__device__ __forceinline__ void attend_again(const ChunkArgs& a, FastDiv by_block, int b, int h,
+                                             const bf16_t* q, float qs, float base, int limit,
+                                             int lower, int lo, int hi, int c0, int c1,
+                                             float factor, Put put) {
+  constexpr float kDown = 0x1p-40f;
+  const int lane = lane_anew(), r32 = lane & 31, half = lane >> 5;
   const int32_t* table = a.table + (size_t)b * a.max_blocks;
-  // Element of the pools where the head's row of position p begins, or -1.
-  auto place = [&](int p) -> long long {
+  const size_t row = (size_t)a.H * D;  // elements between keys
+  auto slot_of = [&](int p) {
     if (p >= hi) return -1;
-    const int j = fast_div(p, by_block);
-    const int page = table[j];
+    const int j = fast_div(p, by_block), page = table[j];
     if (page < 0 || page >= a.num_blocks) return -1;
-    return (((long long)page * a.block_size + (p - j * a.block_size)) * a.H + h) * D;
+    return page * a.block_size + (p - j * a.block_size);
   };
-  auto logit = [&](long long at) {
-    float s = 0.f;
-#pragma unroll 1
-    for (int d = 0; d < D; d += 8) {
-      float k[8], x[8];
-      load8<kFp8>(a.k_cache, (size_t)at + d, k);
-      load8<false>(q, d, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(k[i], x[i], s);
-    }
-    return s * qs;
+  union Eight {
+    uint16_t e[8];
+    bf16x8 h;
   };
-  float m = -__builtin_huge_valf();
+  // Twice for each 32 channels at most: with weights as they are, and smaller.
+  uint32_t over = 0;               // a bit a channel of the lane: the first sum was too large
+  uint32_t plus = 0, minus = 0;    // infinities of its values; both: NaN
 #pragma unroll 1
-  for (int p = lo; p < hi; p += 64) {
-    const long long at = place(p + lane);
-    if (at >= 0) m = fmaxf(m, logit(at));
-  }
-  m = wave_reduce(m, [](float x, float y) { return fmaxf(x, y); });
-  const float safe = m == -__builtin_huge_valf() ? 0.f : m;
-  float l = 0.f, o[kPer] = {}, less[kPer] = {};
-#pragma unroll 1
-  for (int p = lo; p < hi; p += 64) {
-    const long long at = place(p + lane);
-    const float w = at >= 0 ? __builtin_amdgcn_exp2f(logit(at) - safe) : 0.f;
-    l += w;
-#pragma unroll 1
-    for (uint64_t there = __ballot(at >= 0); there != 0; there &= there - 1) {
-      const int i = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)there) - 1);
-      const float wi = __builtin_bit_cast(float, read_lane(__builtin_bit_cast(int, w), i));
-      const uint32_t low = (uint32_t)read_lane((int)at, i), high = (uint32_t)read_lane((int)(at >> 32), i);
-      const size_t from = ((size_t)high << 32 | low) + lane * kPer;
+  for (int turn = 2 * c0; turn < 2 * c1; ++turn) {
+    const int c = turn >> 1;
+    const bool again = turn & 1;
+    if (again && !__any(over != 0)) continue;
+    if (!again) plus = minus = 0;
+    const size_t channel = (size_t)h * D + 32 * c + r32;  // that the lane reads
+    f32x16 o;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float v = load1<kFp8>(a.v_cache, from + j);
-        o[j] = fmaf(wi, v, o[j]);
-        less[j] = fmaf(wi * kDown, v, less[j]);
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    int next = slot_of(lo + r32);
+#pragma unroll 1
+    for (int p0 = lo; p0 < hi; p0 += 32) {
+      const int slot = next;
+      next = slot_of(p0 + 32 + r32);
+      const uint32_t present = (uint32_t)__ballot(slot >= 0);
+      if (present == 0) continue;
+      // The lane's logits and values are of keys 8 (i / 4) + 4 half + i % 4.
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = __builtin_amdgcn_ds_bpermute(4 * (8 * (i / 4) + 4 * half + i % 4), slot);
+        v[i] = load1<kFp8>(a.v_cache, (size_t)(uint32_t)max(key, 0) * row + channel);
+        if (key < 0) v[i] = 0u;
+      }
+      f32x16 s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      const size_t at = (size_t)(uint32_t)max(slot, 0) * row + (size_t)h * D + 8 * half;
+#pragma unroll 4
+      for (int u = 0; u < D / 16; ++u) {
+        Frag16 x;
+        x.u = u32x4{0u, 0u, 0u, 0u};
+        if (q != nullptr) x.u = load16(q + 16 * u + 8 * half);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load8<kFp8>(a.k_cache, at + 16 * u).h, x.h, s, 0,
+                                                    0, 0);
+      }
+      // Bits of the keys that the row sees; the lane's begin at 4 half.
+      const int above = limit - p0, below = lower - p0;
+      uint32_t seen = above < 0 ? 0u : present;
+      if (above < 31) seen &= (2u << max(above, 0)) - 1;
+      if (below > 0) seen &= below > 31 ? 0u : ~0u << below;
+      seen >>= 4 * half;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float w[8];
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          odd = odd || (v[8 * y + e] & 0x7f80u) == 0x7f80u;
+          const bool sees = (seen >> (16 * y + 8 * (e / 4) + e % 4)) & 1;
+          w[e] = sees ? __builtin_amdgcn_exp2f(fmaf(s[8 * y + e], qs, -base)) : 0.f;
+        }
+        Eight high, low, value;
+        if (__any(odd)) {
+          // A value's kind: 1 for one that adds to plus infinity, 64 to minus, 65 NaN.  A
+          // weight's: 1, or 4096 where it is rounded to 0 (times an infinity NaN).
+          // Sums of 16 keys stay below 2^24.
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t bits = v[8 * y + e];
+            const bool inf = (bits & 0x7fffu) == 0x7f80u, nan = (bits & 0x7fffu) > 0x7f80u;
+            const bool sees = (seen >> (16 * y + 8 * (e / 4) + e % 4)) & 1;
+            value.e[e] = f32_to_bf16_bits(nan ? 65.f : inf ? (bits >> 15 ? 64.f : 1.f) : 0.f);
+            high.e[e] = f32_to_bf16_bits(w[e] > 0.f ? 1.f : sees ? 4096.f : 0.f);
+            if (inf || nan) v[8 * y + e] = 0u;
+          }
+          f32x16 sum;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value.h, high.h, sum, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t n = (uint32_t)sum[i];
+            const bool none = n >> 12 != 0;  // of a weight of 0
+            plus |= (uint32_t)(none || (n & 63u) != 0) << i;
+            minus |= (uint32_t)(none || (n >> 6 & 63u) != 0) << i;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = again ? w[e] * kDown : w[e];
+          high.e[e] = f32_to_bf16_bits(x);
+          low.e[e] = f32_to_bf16_bits(x - __builtin_bit_cast(float, (uint32_t)high.e[e] << 16));
+          value.e[e] = (uint16_t)v[8 * y + e];
+        }
+        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value.h, high.h, o, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value.h, low.h, o, 0, 0, 0);
       }
     }
-  }
-  l = wave_sum(l);
-  const float f = l == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[h] : 1.f) / l;
+    if (!again) over = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const float y = fabsf(o[j]) < __builtin_huge_valf() ? o[j] * f : less[j] * (f / kDown);
-    sink.put1(lane * kPer + j, l == 0.f ? 0.f : y);
+    for (int i = 0; i < 16; ++i) {
+      const bool up = (plus >> i) & 1, dn = (minus >> i) & 1, fits = fabsf(o[i]) < __builtin_huge_valf();
+      if (!again) over |= (uint32_t)(!up && !dn && !fits) << i;
+      float y = o[i] * factor;
+      if (again) y *= 1 / kDown;
+      if (up || dn) y = (up ? __builtin_huge_valf() : 0.f) - (dn ? __builtin_huge_valf() : 0.f);
+      if (!again || ((over >> i) & 1)) put(32 * c + 8 * (i / 4) + 4 * half + i % 4, y);
+    }
   }
-  if (lane == 0) sink.put_sum(m, l);
 }
 
 // Zeros for the rows that have no token in the cache; the whole grid takes part.

@@ -15,7 +15,6 @@ namespace mova {
 
 namespace {
 
-typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 
@@ -701,7 +700,7 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
         return to;
       };
       const bool plain = live && !((again >> r32e) & 1);
-      if (plain && halfe == 0 && part_wave == 0)
+      if (live && halfe == 0 && part_wave == 0)
         sink_of(re).put_sum(l == 0.f ? -__builtin_huge_valf() : m * qs - T::kLift, l);
       if (all) {
         // Rows lie across the lanes: through LDS (all waves are done with the stages),
@@ -741,16 +740,20 @@ __global__ __launch_bounds__((Tile<D, kFp8>::kThreads)) void chunk_attention_ker
             *reinterpret_cast<f32x4*>(to.o + 32 * (kBlocks * part_wave + c) + 2 * i + 4 * halfe) =
                 f32x4{o[c][i] * f, o[c][i + 1] * f, o[c][i + 2] * f, o[c][i + 3] * f};
       }
-#pragma unroll 1
-      for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
-        const int x = __ffs((int)rest) - 1;
-        if (T::kSplit > 1 && x % T::kSplit != part_wave) continue;
-        const int place = row_wave * 32 + x;
-        const int token2 = k * cut.tokens + fast_div(place, by_heads);
-        const int end = w.at + token2 + 1;
-        const int from = a.window > 0 ? max(0, end - a.window) : 0;
-        attend_row<D, kFp8>(a, by_block, b, h, q_rows + (size_t)row_of(place) * D, max(from, seg.begin * T::kKeys),
-                            min(end, seg.end * T::kKeys), sink_of(place));
+      if (__builtin_expect(again != 0, 0)) {
+        const int row2 = lane_anew() & 31, place = row_wave * 32 + row2;
+        const bool mine = (again >> row2) & 1;
+        const int at = w.at + k * cut.tokens + fast_div(place, by_heads);
+        const int from = a.window > 0 ? max(0, at + 1 - a.window) : 0;
+        const int first = wave_reduce(mine ? from : 0x3fffffff, [](int x, int y) { return min(x, y); });
+        const int last = wave_reduce(mine ? at : -1, [](int x, int y) { return max(x, y); });
+        attend_again<D, kFp8>(a, by_block, b, h, mine ? q_rows + (size_t)row_of(place) * D : nullptr,
+                              flip != 0u ? -qs : qs, m * qs - T::kLift, mine ? at : -1, from,
+                              max(first, seg.begin * T::kKeys), min(last + 1, seg.end * T::kKeys),
+                              kBlocks * part_wave, kBlocks * (part_wave + 1), f,
+                              [&](int channel, float y) {
+                                if (mine) sink_of(place).put1(channel, y);
+                              });
       }
     }
   }

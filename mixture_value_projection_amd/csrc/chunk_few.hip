@@ -390,32 +390,34 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
       to.ml = parts.ml + part * 2;
       return to;
     };
-    if (has_row && !((again >> r16) & 1)) {
+    const float scale = l == 0.f ? 0.f : vs / l;
+    if (has_row) {
       const Sink<D> to = sink_of(row, r16);
-      const float scale = l == 0.f ? 0.f : vs / l;
+      if (!((again >> r16) & 1)) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const f32x4 y = {o[c][0] * scale, o[c][1] * scale, o[c][2] * scale, o[c][3] * scale};
-        if (all) {
-          uint2 w;
-          w.x = (uint32_t)f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16);
-          w.y = (uint32_t)f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16);
-          *reinterpret_cast<uint2*>(to.out + 16 * c + 4 * g4) = w;
-        } else {
-          *reinterpret_cast<f32x4*>(to.o + 16 * c + 4 * g4) = y;
+        for (int c = 0; c < kCols; ++c) {
+          const f32x4 y = {o[c][0] * scale, o[c][1] * scale, o[c][2] * scale, o[c][3] * scale};
+          if (all) {
+            uint2 w;
+            w.x = (uint32_t)f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16);
+            w.y = (uint32_t)f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16);
+            *reinterpret_cast<uint2*>(to.out + 16 * c + 4 * g4) = w;
+          } else {
+            *reinterpret_cast<f32x4*>(to.o + 16 * c + 4 * g4) = y;
+          }
         }
       }
       if (g4 == 0) to.put_sum(l == 0.f ? -__builtin_huge_valf() : m, l);
     }
-#pragma unroll 1
-    for (uint32_t rest = again; rest != 0; rest &= rest - 1) {
-      const int x = __ffs((int)rest) - 1;
-      const int t = fast_div(x, by_group);
-      const size_t at = (size_t)(f.c.row0 + t) * a.Hq + h * G + (x - t * G);
-      const int end = f.c.at + t + 1;
-      const int from = a.window > 0 ? max(0, end - a.window) : 0;
-      attend_row<D, kFp8>(a, by_block, b, h, a.q + at * D, max(from, f.lo + t0 * kTileKeys),
-                          min(end, f.lo + t1 * kTileKeys), sink_of(at, x));
+    if (__builtin_expect(again != 0, 0)) {
+      // (Lanes i and i + 32 have row i % 32 there, so i % 16 where it is one of these.)
+      const bool mine = (lane & 16) == 0 && ((again >> r16) & 1);
+      attend_again<D, kFp8>(a, by_block, b, h, mine ? a.q + row * D : nullptr, qs, m,
+                            mine ? limit : -1, lower, f.lo + t0 * kTileKeys,
+                            min(len, f.lo + t1 * kTileKeys), 0, D / 32, scale,
+                            [&](int channel, float y) {
+                              if (mine) sink_of(row, r16).put1(channel, y);
+                            });
     }
   }
 }
