@@ -834,7 +834,10 @@ size_t many_floats(int D) { return 64 + split_floats(kCus) + part_rows(D) * (2 +
 
 // Requests of few rows (single tokens, drafts) are read by the few-rows kernel, whose
 // waves go through keys of their own, where such requests are most: where the rows of
-// the batch, whose lengths the host does not know, are on average as few.
+// the batch, whose lengths the host does not know, are on average as few.  A token of
+// more query heads to a key head than that is no request of few rows.  (64 requests of a
+// token after 500 to 2000, 32 heads over 1: 36 us, and 42 with a launch that finds nothing
+// and its places in the join.)
 template <int D, bool kFp8>
 hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
   using T = Tile<D, kFp8>;
@@ -844,8 +847,9 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
                                hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   });
   if (e != hipSuccess) return e;
-  const long long rows = (long long)a.T * (a.Hq / a.H);
-  a.few = rows <= (long long)kFewRows * a.B || a.B >= kFewRequests ? kFewRows : 0;
+  const int G = a.Hq / a.H;
+  const long long rows = (long long)a.T * G;
+  a.few = G <= kFewRows && (rows <= (long long)kFewRows * a.B || a.B >= kFewRequests) ? kFewRows : 0;
   const Parts few_parts = chunk_few_parts(a.part + many_floats(D));
   // The stretch, then what was split, then the parts.
   long long* stretch = (long long*)a.part;
@@ -853,7 +857,7 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
   parts.split = (Split*)(a.part + 64);
   parts.ml = a.part + 64 + split_floats(kCus);
   parts.o = parts.ml + part_rows(D) * 2;
-  const Cut cut = cut_of(a.Hq / a.H, T::kRows);
+  const Cut cut = cut_of(G, T::kRows);
   const FastDiv by_heads = make_fast_div(cut.heads);
   int many = 0, few = 0;
   if (a.few > 0) {
@@ -869,8 +873,7 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   chunk_join_kernel<D, kFp8><<<dim3(many + few, 8), 512, 0, stream>>>(
-      a, parts, many, cut.heads, by_heads, stretch, few_parts, chunk_few_tracks(a.H),
-      make_fast_div(a.Hq / a.H));
+      a, parts, many, cut.heads, by_heads, stretch, few_parts, chunk_few_tracks(a.H), make_fast_div(G));
   return hipGetLastError();
 }
 
