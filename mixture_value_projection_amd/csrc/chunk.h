@@ -38,13 +38,20 @@ struct Parts {
 constexpr size_t split_floats(int groups) { return (size_t)groups * sizeof(Split) / 4; }
 static_assert(sizeof(Split) % 8 == 0, "whole words");
 
-// Of the few-rows kernel: floats of scratch, workgroups, key heads (tracks) of one, the
-// parts in the scratch, and the launch, without the joining of its parts.
-size_t chunk_few_scratch_floats(int D);
-int chunk_few_groups(const ChunkArgs& a);
+// Of the few-rows kernel, for calls of T tokens in B requests of at most `most` keys:
+// workgroups, key heads (tracks) of one, floats of scratch, the parts in the scratch, and
+// the launch, without the joining of its parts.
+int chunk_few_groups(int T, int B, int H, int D, long long most);
 int chunk_few_tracks(int H);
-Parts chunk_few_parts(float* scratch);
-hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, hipStream_t stream);
+size_t chunk_few_floats(int groups, int H, int D);
+Parts chunk_few_parts(float* scratch, int groups, int H);
+hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, int groups, hipStream_t stream);
+
+// Workgroups for a line of at most `units` units of work, in stretches of `least` or more:
+// as many as there can be stretches (neighbours are dealt out in eights), up to `most`.
+inline int groups_for(double units, int least, int most) {
+  return units >= (double)least * most ? most : ((int)(units / least) / 8 + 1) * 8;
+}
 
 namespace {
 

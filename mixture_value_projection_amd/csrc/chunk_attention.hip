@@ -187,7 +187,7 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 // one's weight, so most tiles multiply nothing.  The order is fixed by hand: the
 // compiler's own put the parts behind each other.
 //
-// The line of work is all row tiles of the batch, cut into equal stretches for 256
+// The line of work is all row tiles of the batch, cut into equal stretches for up to 256
 // workgroups: lengths are on the device, and a tile's cost differs by its place in a
 // prompt.  A tile in two stretches leaves parts, which chunk_join_kernel joins.
 //
@@ -828,9 +828,29 @@ __global__ __launch_bounds__(512) void chunk_join_kernel(ChunkArgs a, Parts part
 
 namespace {
 
-size_t part_rows(int D) { return (size_t)kCus * 2 * 32 * (D == 256 ? 4 : 8); }
+// The workgroups of a call, 0 of a kernel that such calls never launch.  By the sizes
+// alone, not by the launch rule: a call of fewer tokens or requests, or over a shorter
+// table, has no more, so that its scratch fits the other's.
+struct Groups {
+  int many, few;
+};
+int rows_of(int D) { return 32 * (D == 256 ? 4 : 8); }
+Groups groups_of(int T, int B, int Hq, int H, int D, long long most) {
+  const int G = Hq / H;
+  const Cut cut = cut_of(G, rows_of(D));
+  const double tiles = std::min(T, T / cut.tokens + B);  // of rows
+  Groups g{0, 0};
+  if ((long long)T * G > kFewRows)
+    g.many = groups_for(tiles * H * cut.head_blocks * (most + kFixed), kLeastStretch, kCus);
+  if (G <= kFewRows) g.few = chunk_few_groups(T, B, H, D, most);
+  return g;
+}
 
-size_t many_floats(int D) { return 64 + split_floats(kCus) + part_rows(D) * (2 + D); }
+size_t part_rows(int groups, int D) { return (size_t)groups * 2 * rows_of(D); }
+
+size_t many_floats(int groups, int D) {
+  return groups == 0 ? 0 : 64 + split_floats(groups) + part_rows(groups, D) * (2 + D);
+}
 
 // Requests of few rows (single tokens, drafts) are read by the few-rows kernel, whose
 // waves go through keys of their own, where such requests are most: where the rows of
@@ -850,23 +870,24 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
   const int G = a.Hq / a.H;
   const long long rows = (long long)a.T * G;
   a.few = G <= kFewRows && (rows <= (long long)kFewRows * a.B || a.B >= kFewRequests) ? kFewRows : 0;
-  const Parts few_parts = chunk_few_parts(a.part + many_floats(D));
+  const Groups groups = groups_of(a.T, a.B, a.Hq, a.H, D, (long long)a.max_blocks * a.block_size);
+  const Parts few_parts = chunk_few_parts(a.part + many_floats(groups.many, D), groups.few, a.H);
   // The stretch, then what was split, then the parts.
   long long* stretch = (long long*)a.part;
   Parts parts;
   parts.split = (Split*)(a.part + 64);
-  parts.ml = a.part + 64 + split_floats(kCus);
-  parts.o = parts.ml + part_rows(D) * 2;
+  parts.ml = a.part + 64 + split_floats(groups.many);
+  parts.o = parts.ml + part_rows(groups.many, D) * 2;
   const Cut cut = cut_of(G, T::kRows);
   const FastDiv by_heads = make_fast_div(cut.heads);
   int many = 0, few = 0;
   if (a.few > 0) {
-    few = chunk_few_groups(a);
-    e = launch_chunk_few(a, few_parts, stream);
+    few = groups.few;
+    e = launch_chunk_few(a, few_parts, few, stream);
     if (e != hipSuccess) return e;
   }
   if (a.few == 0 || rows > kFewRows) {
-    many = kCus;
+    many = groups.many;
     chunk_attention_kernel<D, kFp8><<<many, T::kThreads, T::kLds, stream>>>(
         a, parts, make_fast_div(a.block_size), cut, by_heads, stretch);
     e = hipGetLastError();
@@ -879,9 +900,10 @@ hipError_t launch_cfg(ChunkArgs a, hipStream_t stream) {
 
 }  // namespace
 
-size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D) {
+size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D, long long most) {
   if (T == 0 || B == 0) return 0;
-  return many_floats(D) + chunk_few_scratch_floats(D);
+  const Groups g = groups_of(T, B, Hq, H, D, most);
+  return many_floats(g.many, D) + (g.few == 0 ? 0 : chunk_few_floats(g.few, H, D));
 }
 
 hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream) {

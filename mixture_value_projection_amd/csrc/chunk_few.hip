@@ -28,7 +28,6 @@ namespace mova {
 namespace {
 
 static_assert(kFewRows == 16, "the rows of a product");
-constexpr int kMaxGrid = 2 * kCus;
 // Tiles of a stretch at least: a row of so few is not cut.  (Of two, four and eight: 1
 // token after 130 12.7, 14.2 and 17.4 us, 64 requests of 32 to 256 tokens 24.5, 25.5 and
 // 31.9, 1 token after 8000 31.6, 25.9 and 27.3.)
@@ -424,10 +423,10 @@ __global__ __launch_bounds__(256) void chunk_few_kernel(ChunkArgs a, Parts parts
 
 namespace {
 
-size_t few_part_rows() { return (size_t)kMaxGrid * 2 * 4 * 16; }
+size_t part_rows(int groups, int H) { return (size_t)groups * 2 * chunk_few_tracks(H) * 16; }
 
 template <int D, bool kFp8, int kTracks>
-hipError_t launch_cfg(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
+hipError_t launch_cfg(const ChunkArgs& a, const Parts& parts, int groups, hipStream_t stream) {
   using T = Tile<D, kFp8>;
   static std::atomic<unsigned long long> done{0};
   hipError_t e = once_per_device(done, [&] {
@@ -435,58 +434,67 @@ hipError_t launch_cfg(const ChunkArgs& a, const Parts& parts, hipStream_t stream
                                hipFuncAttributeMaxDynamicSharedMemorySize, 4 * T::kLds);
   });
   if (e != hipSuccess) return e;
-  chunk_few_kernel<D, kFp8, kTracks><<<chunk_few_groups(a), 256, 4 * T::kLds, stream>>>(
+  chunk_few_kernel<D, kFp8, kTracks><<<groups, 256, 4 * T::kLds, stream>>>(
       a, parts, make_fast_div(a.block_size), make_fast_div(a.Hq / a.H));
   return hipGetLastError();
 }
 
 template <int D, bool kFp8>
-hipError_t launch_tracks(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
+hipError_t launch_tracks(const ChunkArgs& a, const Parts& parts, int groups, hipStream_t stream) {
   switch (chunk_few_tracks(a.H)) {
-    case 4: return launch_cfg<D, kFp8, 4>(a, parts, stream);
-    case 2: return launch_cfg<D, kFp8, 2>(a, parts, stream);
-    default: return launch_cfg<D, kFp8, 1>(a, parts, stream);
+    case 4: return launch_cfg<D, kFp8, 4>(a, parts, groups, stream);
+    case 2: return launch_cfg<D, kFp8, 2>(a, parts, groups, stream);
+    default: return launch_cfg<D, kFp8, 1>(a, parts, groups, stream);
   }
 }
 
+// Workgroups where the keys are many, and the line's units: both types of pool are taken
+// for the one with more, as the scratch's size is asked for without the type.
 template <int D>
-int groups_of(bool fp8) {
-  return kCus * (fp8 ? Tile<D, true>::kPerCu : Tile<D, false>::kPerCu);
+int groups_of(int B, int H, long long most) {
+  static_assert(Tile<D, true>::kPerCu == Tile<D, false>::kPerCu, "a size for both types");
+  constexpr int kKeys = std::min(Tile<D, true>::kKeys, Tile<D, false>::kKeys);
+  const int tracks = chunk_few_tracks(H);
+  const double tiles = (double)((most + kKeys - 1) / kKeys);  // a stripe's are at most as many
+  return groups_for(tiles * B * (H / tracks), kLeastTiles, kCus * Tile<D, true>::kPerCu);
 }
 
 }  // namespace
 
-size_t chunk_few_scratch_floats(int D) {
-  return split_floats(kMaxGrid) + few_part_rows() * (2 + D);
-}
-
-int chunk_few_groups(const ChunkArgs& a) {
-  const bool fp8 = a.dtype == kCacheFp8;
-  return a.D == 64 ? groups_of<64>(fp8) : a.D == 128 ? groups_of<128>(fp8) : groups_of<256>(fp8);
+int chunk_few_groups(int T, int B, int H, int D, long long most) {
+  const int requests = std::min(T, B);  // that have a token
+  return D == 64    ? groups_of<64>(requests, H, most)
+         : D == 128 ? groups_of<128>(requests, H, most)
+                    : groups_of<256>(requests, H, most);
 }
 
 int chunk_few_tracks(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
 
-Parts chunk_few_parts(float* scratch) {
+size_t chunk_few_floats(int groups, int H, int D) {
+  return split_floats(groups) + part_rows(groups, H) * (2 + D);
+}
+
+Parts chunk_few_parts(float* scratch, int groups, int H) {
   Parts parts;
   parts.split = (Split*)scratch;
-  parts.ml = scratch + split_floats(kMaxGrid);
-  parts.o = parts.ml + few_part_rows() * 2;
+  parts.ml = scratch + split_floats(groups);
+  parts.o = parts.ml + part_rows(groups, H) * 2;
   return parts;
 }
 
-hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, hipStream_t stream) {
+hipError_t launch_chunk_few(const ChunkArgs& a, const Parts& parts, int groups,
+                            hipStream_t stream) {
   const bool fp8 = a.dtype == kCacheFp8;
   switch (a.D) {
     case 64:
-      return fp8 ? launch_tracks<64, true>(a, parts, stream)
-                 : launch_tracks<64, false>(a, parts, stream);
+      return fp8 ? launch_tracks<64, true>(a, parts, groups, stream)
+                 : launch_tracks<64, false>(a, parts, groups, stream);
     case 128:
-      return fp8 ? launch_tracks<128, true>(a, parts, stream)
-                 : launch_tracks<128, false>(a, parts, stream);
+      return fp8 ? launch_tracks<128, true>(a, parts, groups, stream)
+                 : launch_tracks<128, false>(a, parts, groups, stream);
     case 256:
-      return fp8 ? launch_tracks<256, true>(a, parts, stream)
-                 : launch_tracks<256, false>(a, parts, stream);
+      return fp8 ? launch_tracks<256, true>(a, parts, groups, stream)
+                 : launch_tracks<256, false>(a, parts, groups, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -122,8 +122,8 @@ struct ChunkArgs {
   float* part;  // scratch of chunk_scratch_floats
   int few = 0;  // requests of at most so many rows are the few-rows kernel's
 };
-// Floats of scratch; depends on the sizes alone.
-size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D);
+// Floats of scratch, for requests of at most `most` tokens; depends on the sizes alone.
+size_t chunk_scratch_floats(int T, int B, int Hq, int H, int D, long long most);
 hipError_t launch_chunk_attention(const ChunkArgs& a, hipStream_t stream);
 
 // Blocks of a pool whose upkeep is done here (a bit of each in LDS).

@@ -237,7 +237,8 @@ size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_
                                             int head_dim, int max_blocks, int block_size) {
   if (check_chunk(T, B, n_heads, n_kv_heads, head_dim, max_blocks, block_size) != MOVA_OK)
     return (size_t)-1;
-  return align256(4 * chunk_scratch_floats(T, B, n_heads, n_kv_heads, head_dim));
+  return align256(4 * chunk_scratch_floats(T, B, n_heads, n_kv_heads, head_dim,
+                                           (long long)max_blocks * block_size));
 }
 
 int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v_cache,
