@@ -555,7 +555,7 @@ int mova_attention_paged(const void* q, const void* k_cache, const void* v_cache
  * tokens or requests or over a shorter table too; (size_t)-1 outside the
  * domain.  What may be left to be joined of rows whose keys are split: 0.5 MB for
  * one token of 32 heads over 8 of 128 and up to 160 cached, 34 MB for any length,
- * 102 MB at most (135 with 256 channels). */
+ * 102 MB at most. */
 size_t mova_attention_chunk_workspace_bytes(int T, int B, int n_heads, int n_kv_heads,
                                             int head_dim, int max_blocks, int block_size);
 
