@@ -1034,15 +1034,20 @@ def paged_copy(copy_src: torch.Tensor, copy_dst: torch.Tensor, k_cache: Optional
     """mova_paged_copy: block ``copy_dst[i]`` of each pool given becomes as
     block ``copy_src[i]`` (int32 [n], as from ``paged_fork`` or
     ``paged_compact``); pairs outside the pool, and those behind ``count``
-    (int32 [1], None: n), are passed over."""
+    (int32 [1], None: n), are passed over.  Any of the keys, values and bounds
+    may be left out, as long as one is there."""
     lib = load_library()
     (n,) = _dims(copy_src, "copy_src", 1, "[n]")
-    pool = k_cache if k_cache is not None else v_cache
-    if pool is None:
-        raise ValueError("neither keys nor values are given")
-    nb, bs, H, D = _dims(pool, "the pools", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")
     dev = copy_src.device
-    dtype = CACHE_DTYPES.get(pool.dtype)
+    pool = k_cache if k_cache is not None else v_cache
+    if pool is not None:
+        nb, bs, H, D = _dims(pool, "the pools", 4, "[num_blocks, block_size, n_kv_heads, head_dim]")
+    elif k_bounds is not None:
+        nb, H, _, D = _dims(k_bounds, "k_bounds", 4, "[num_blocks, n_kv_heads, 2, head_dim]")
+        bs = 1  # (of no account without keys or values)
+    else:
+        raise ValueError("neither keys, values nor bounds are given")
+    dtype = CACHE_DTYPES.get(torch.bfloat16 if pool is None else pool.dtype)
     for p, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if p is not None and _check_pool(p, name, (nb, bs, H, D), dev) != dtype:
             raise ValueError("the pools must have the same dtype")
