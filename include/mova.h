@@ -629,9 +629,10 @@ int mova_attention_chunk_paged(const void* q, const void* k_cache, const void* v
  * pools.
  *
  * A pair gets nothing (its child's row and length stay) when a row number lies
- * outside [0, B) -- -1 pads a list --, the child is a parent in this call or the
- * child of an earlier pair, or when the pairs up to and with it need more blocks
- * than the stack has and it needs one.  The child's row has to hold no blocks.
+ * outside [0, B) -- -1 pads a list -- or both are the same; when its child is the
+ * parent of one of the other pairs, or the child of an earlier one; or when these
+ * pairs up to and with it need more blocks than the stack has and it needs one.
+ * The child's row has to hold no blocks.
  *
  *   parents, children int32 [n], fork_lens int32 [n] or NULL
  *   block_table  int32 [B, max_blocks]  in / out

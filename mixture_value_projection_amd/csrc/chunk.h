@@ -13,7 +13,11 @@ namespace mova {
 // tokens, which fill sixteen rows, 142 and 165; eight, as two times sixteen, 260 and
 // 177.  60 with a token and 4 with 512, by both kernels and by one: 221 and 272 us; 32
 // with one and 32 with 64: 208 and 228.  Where no request has few rows the launch costs
-// 2 to 4 us, and where few short ones have, more: windows over 37 requests 87 and 78.)
+// 2 to 4 us, and where few short ones have, more: windows over 37 requests 87 and 78.
+// Below 32 requests, single tokens after 500 to 8000 and one chunk of 512: 8 requests 99
+// by both and 83 by one, 16 112 and 104, 24 118 and 116, 31 157 and 159; after 100 to 1000
+// 24 65 and 55; in 8 bits, where a chunk of 2048 pays for the launch, 8 196 and 193, 16 189
+// and 202, 24 183 and 209.)
 constexpr int kFewRows = 16, kFewRequests = 32;
 
 // What a stretch leaves to be joined.

@@ -71,8 +71,8 @@ Cut cut_of(int G, int rows) {
 // 200 of 40 tokens 174, 113 and 127.)
 constexpr int kFixed = 320;
 // A stretch of the line is at least this long.  (Of 256, 512 and 1024: 19 tokens after
-// 130 21.5, 17.7 and 26.7 us, 64 after 2000 58, 63 and 54, 4 requests of 64 after 500 53,
-// 38 and 52, a prompt of 512 37, 40 and 52.)
+// 130 18.6, 16.9 and 25.0 us, 64 after 2000 36, 42 and 49, 32 after 8000 60, 39 and 41, 4
+// requests of 64 after 500 31, 33 and 47, a prompt of 512 39, 38 and 46.)
 constexpr int kLeastStretch = 512;
 struct Load {
   int at, live, tokens, window;
@@ -191,12 +191,13 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 // workgroups: lengths are on the device, and a tile's cost differs by its place in a
 // prompt.  A tile in two stretches leaves parts, which chunk_join_kernel joins.
 //
-// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 582 to 620 us (0.89 to 0.95
+// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 575 to 589 us (0.93 to 0.96
 // PF/s; a product of two 16384 matrices reaches 1.6), 2048 tokens after 129,024 4.1 to
-// 4.4 ms (1.0).  A tile of 64 keys takes 3900 cycles.  The matrix instructions of a
-// SIMD's two waves are 2130 of them, and the eight waves' reads of keys and values 2050 of
-// LDS (256 KB at 128 bytes a cycle): both would have to go on without a pause, beside 32
-// exponentials, conversions and maxima a lane.  How the weights are spread over the
+// 4.2 ms (1.05).  A tile of 64 keys takes 3900 cycles.  The matrix instructions of a
+// SIMD's two waves are 2130 of them, their 129 vector instructions and 32 exponentials each
+// 1830 (at 4.9 and 8.8 cycles): nearly the sum of both, so the two waves hardly overlap.
+// The eight waves' reads of keys and values are 2050 cycles of LDS (256 KB at 128 bytes a
+// cycle).  How the weights are spread over the
 // products, how far reads run ahead, and the waves' priorities change nothing (within 1 %).
 // A row tile's start and end take 18,000.  With one tile ahead, by direct loads
 // to LDS, and a tile's products all ahead of its softmax, the long one took 4.97 ms.

@@ -29,8 +29,8 @@ namespace {
 
 static_assert(kFewRows == 16, "the rows of a product");
 // Tiles of a stretch at least: a row of so few is not cut.  (Of two, four and eight: 1
-// token after 130 12.7, 14.2 and 17.4 us, 64 requests of 32 to 256 tokens 24.5, 25.5 and
-// 31.9, 1 token after 8000 31.6, 25.9 and 27.3.)
+// token after 130 12.0, 13.7 and 16.7 us, 64 requests of 32 to 256 tokens 25.4, 26.0 and
+// 29.4, 1 token after 8000 30.8, 20.2 and 19.5.)
 constexpr int kLeastTiles = 4;
 
 // Request b as this kernel sees it.

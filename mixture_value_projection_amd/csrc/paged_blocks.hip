@@ -43,7 +43,10 @@ __device__ __forceinline__ int clamp_len(int n, int most) { return min(max(n, 0)
 // own, as far as a grid goes (770 MB read and written in blocks of 32 KB: 2048
 // workgroups with items in turn 180 us, this 150).  Pools larger than the last cache
 // pass the caches by: that takes 132 us (5.8 TB/s) for those 770 MB, but for 60 MB of
-// a pool of 119 MB 14 us, and 11 through the caches.
+// a pool of 119 MB 14 us, and 11 through the caches.  (The host knows the pool, not how
+// many of the pairs are there.  Copied again and again in pools of 2 GB, so that what fits
+// stays in the caches: 2 MB 5.3 past and 4.9 through them, 121 MB 26.7 and 22.3, 393 MB 81
+// and 83, 1573 MB 309 and 326.)
 constexpr size_t kLastCache = (size_t)256 << 20;
 constexpr int kCopyGrid = 65536;
 constexpr int kCopyAtOnce = 4, kCopyPieces = 256 * kCopyAtOnce;
@@ -221,7 +224,9 @@ hipError_t launch_paged_fork(const ForkArgs& a, hipStream_t stream) {
 //
 // A workgroup alone waits for memory at each turn: the 28,689 entries that 203 rows
 // give back took one 80 us with atomics on the counts and 32 with counts in LDS; these
-// two take 17 and 4.  The 1051 of a step of 64 rows took it 8; 6 and 4.
+// two take 17 and 4.  The 1051 of a step of 64 rows took it 8; 6 and 4.  As each workgroup
+// reads all entries, the time grows with them: 262,144 129 us for both, 1,048,576 470, a
+// sixteenth of those 45.
 __global__ __launch_bounds__(kFreeThreads) void free_count_kernel(FreeArgs a, FastDiv by_block,
                                                                   int run) {
   extern __shared__ __attribute__((aligned(16))) char free_lds[];
@@ -380,8 +385,9 @@ hipError_t launch_paged_free(const FreeArgs& a, hipStream_t stream) {
 // runs of 256 blocks; with those counts in LDS, the second one ranks any block
 // in a step and finds the block of any rank in a search, so that table, stack,
 // counts and lists are written side by side.  Both are bound by their round trips: a
-// pool of 24,274 blocks, 9000 and more of them free, 4.8 and 7.3 us, one of 1752 2.7 and
-// 6.2.
+// pool of 24,274 blocks, 9000 and more of them free, 4.8 and 7.1 us, one of 1752 2.8 and
+// 5.9.  Of larger ones, half free, the first takes most: 262,144 blocks 36 us for both,
+// 1,048,576 217.
 __global__ __launch_bounds__(kFreeThreads) void compact_rank_kernel(CompactArgs a) {
   extern __shared__ uint32_t compact_bits[];
   __shared__ long long tmp[kFreeThreads / 64];
