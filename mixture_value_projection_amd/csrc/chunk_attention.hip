@@ -191,9 +191,9 @@ __device__ __forceinline__ void widen16(const u32x4& w, u32x4* a, u32x4* b) {
 // workgroups: lengths are on the device, and a tile's cost differs by its place in a
 // prompt.  A tile in two stretches leaves parts, which chunk_join_kernel joins.
 //
-// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 575 to 589 us (0.93 to 0.96
+// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, 575 to 611 us (0.90 to 0.96
 // PF/s; a product of two 16384 matrices reaches 1.6), 2048 tokens after 129,024 4.1 to
-// 4.2 ms (1.05).  A tile of 64 keys takes 3900 cycles.  The matrix instructions of a
+// 4.4 ms (1.0).  A tile of 64 keys takes 3900 cycles.  The matrix instructions of a
 // SIMD's two waves are 2130 of them, their 129 vector instructions and 32 exponentials each
 // 1830 (at 4.9 and 8.8 cycles): nearly the sum of both, so the two waves hardly overlap.
 // The eight waves' reads of keys and values are 2050 cycles of LDS (256 KB at 128 bytes a
