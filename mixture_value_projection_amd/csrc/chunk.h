@@ -185,7 +185,7 @@ struct Sink {
 //
 // Keys and values come straight from the pool, and the logits are formed again for each
 // 32 channels, which keeps this in the registers that the kernels have.  Bound by round
-// trips to memory, some 1.5 us for 32 keys, 32 rows and 32 channels; a row at a time, with
+// trips to memory, some 3 to 5 us for 32 keys, 32 rows and 32 channels; a row at a time, with
 // its values key by key, took 140 times a call where this takes 8.  (A value that all rows
 // of a prompt see, 32 heads over 8 of 128: 512 tokens 294 us, a row at a time 5169, without
 // the value 47; 2048 tokens 657, 12,358 and 86; 8192 tokens 9.7 ms, without it 0.58.)
